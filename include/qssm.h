@@ -16,6 +16,9 @@
  *  - Quamba-SE soft-edge quantization (blog post), sections 2.1, 2.2 and 4.1: a three-scale
  *    8-bit code (scale/4, scale, scale*4) with the mode in the top bits.
  *
+ * Around the recurrence: the 4-bit and 8-bit linear layers, the root-mean-square norm that writes
+ * their int8 input, and an int8 recurrent state for decoding.
+ *
  * The recurrence, per channel d and state n:
  *     h_t = exp(delta_t * A) * h_{t-1} + delta_t * B_t * x_t,     y_t = sum_n C_t * h_t + D * x_t
  * with int8 x, B, C (dequantized as scale * code), fp32 delta/A/D, a higher-precision state and
@@ -52,7 +55,9 @@
 extern "C" {
 #endif
 
-#define QSSM_VERSION 180 /* 1.8.0: instruction-rate probes */
+/* 1.8.0. Entry points that leave every older one and its argument struct as they were do not
+ * change it. */
+#define QSSM_VERSION 180
 
 typedef int32_t qssm_status;
 enum {
@@ -406,6 +411,118 @@ typedef struct qssm_update_args {
 qssm_status qssm_state_update(const qssm_update_args* a, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * int8 recurrent state: the decode cache in 8 bits, one fp32 scale per state row (b, h, p).
+ * Quamba2, abstract (W8A8 generation stage: decoding is bound by the bytes of the state).
+ *
+ * A row of N values h is held as codes q and a scale s, by the quantization rule above:
+ *     s = fl32(absmax * fl32(1/127)), absmax the largest finite |h| of the row (absmax 0: s = 1;
+ *     clamped to [2^-100, 2^100]),   q = clamp(RNE(h / s), -128, 127);      the value read back is fl32(s * q).
+ *
+ * qssm_state_quant writes rows (h [rows, N] fp32 or fp16: a scan's h_last) to codes [rows, N] and
+ * scales [rows]; qssm_state_dequant reads them back (out [rows, N] fp32 or fp16, e.g. the h0 of a
+ * following scan); a row whose scale is not valid reads back as 0. Any rows >= 0, N >= 1 (at most
+ * 2^31 - 1).
+ */
+qssm_status qssm_state_quant(const void* h, int32_t h_dtype, int64_t rows, int64_t N, int8_t* codes,
+                             float* scales, hipStream_t stream);
+qssm_status qssm_state_dequant(const int8_t* codes, const float* scales, int64_t rows, int64_t N,
+                               void* out, int32_t out_dtype, hipStream_t stream);
+
+/* The decode update of qssm_state_update on an int8 state. `a` as there with state_dtype QSSM_I8 and
+ * state = the codes [B, nh, P, N] written; state_scales [B, nh, P] receives the new row scales.
+ * state_in and scales_in are the codes and scales read: both NULL updates state and state_scales in
+ * place; given, they are left as they were (a caller that may take a token back keeps them). They
+ * may be a->state and state_scales themselves, else the two must not overlap.
+ * Per row, with dA = fl32(exp(fl32(delta * A[h]))) (exp in fp64) and every value fp32:
+ *     h[n] = fma(fl(dA * s), q[n], fl(fl(delta * xh) * Bh[n]))      (one rounding; s invalid: 0)
+ *     y = sum_n Ch[n] * h[n] + Dskip[h] * xh         (h before it is rounded to codes)
+ *     s' and q'[n] from h as qssm_state_quant makes them.
+ * The new codes and scales are fixed bit for bit by this rule.
+ * Supported: N = 16 * 2^k with 16 <= N <= 256; state and state_in 16-byte aligned; headdim as there.
+ */
+qssm_status qssm_state_update_i8(const qssm_update_args* a, const int8_t* state_in,
+                                 const float* scales_in, float* state_scales, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * RMS norm with an int8 output: the norm in front of a W8A8 or W4A8 projection, with the residual
+ * stream's addition or Mamba2's gate fused.
+ * Quamba2, abstract (W8A8 and W4A8 blocks: 8-bit activations into the in and out projections).
+ *
+ * Rows m < rows of D = dim channels, in norm_groups groups of Dg = D / norm_groups:
+ *     h = x[m, c] + residual[m, c], rounded to residual_dtype       (h = x without a residual)
+ *     t = fl32(h * silu(gate[m, c]))        (t = h without a gate), silu(z) = fl32(z / (1 + e^-z))
+ *     r = fl32(1 / sqrt(sum of t^2 over c's group / Dg + eps))      (sum and root in fp64)
+ *     v = fl32(fl32(t * r) * weight[c])     (weight NULL: 1)
+ *     q[m, c] = clamp(RNE(v / s), -128, 127) by the quantization rule above
+ * compute_scales != 0: scales [rows] is an output, one scale per row: s = scales[m] =
+ *     fl32(absmax * fl32(1/127)) of the row's largest finite |v| (absmax 0: 1; clamped to
+ *     [2^-100, 2^100]).
+ * compute_scales == 0: scales [1] is an input, the static scale of every row.
+ * residual_out (may be NULL) receives h; it may be residual itself (then with the same stride). With
+ * no residual it receives x in residual_dtype, and h is that value. A gate together with a residual
+ * or residual_out is QSSM_ERR_UNSUPPORTED.
+ * A group with a NaN or an infinity has codes 0 (r is 0 or NaN there).
+ * x and residual are fp32 or fp16, the gate too; rows of each tensor lie `*_stride` elements apart
+ * (>= D), so a slice of a wider tensor's columns can be given.
+ * Supported: D <= 8192; up to 32768 when D / norm_groups is a multiple of 8, every stride a multiple
+ * of 8, q 8-byte aligned and the other tensors 16-byte aligned (the form with wide loads).
+ */
+typedef struct qssm_rmsnorm_args {
+  int64_t rows, dim;
+  int32_t norm_groups;        /* dim % norm_groups == 0 */
+  int32_t x_dtype;            /* QSSM_F32 or QSSM_F16 */
+  const void* x;              /* [rows, dim] */
+  int64_t x_stride;
+  int32_t residual_dtype;     /* of residual and residual_out: QSSM_F32 or QSSM_F16 */
+  int32_t gate_dtype;         /* QSSM_F32 or QSSM_F16 */
+  const void* residual;       /* [rows, dim] or NULL */
+  int64_t residual_stride;
+  void* residual_out;         /* [rows, dim] or NULL */
+  int64_t residual_out_stride;
+  const void* gate;           /* [rows, dim] or NULL */
+  int64_t gate_stride;
+  const float* weight;        /* [dim] or NULL */
+  float eps;                  /* finite, >= 0 */
+  int32_t compute_scales;
+  float* scales;              /* [rows] out or [1] in */
+  int8_t* q;                  /* [rows, dim] */
+  int64_t q_stride;
+} qssm_rmsnorm_args;
+
+qssm_status qssm_rmsnorm_i8(const qssm_rmsnorm_args* a, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * W8A8 linear layer: int8 weights x int8 activations on int8 MFMA with int32 accumulation, one scale
+ * per token and per output channel.
+ * Quamba2, abstract (W8A8 for the Mamba1 and Mamba2 backbones, prefill and generation).
+ *   y[m, n] = bias[n] + fl32(sa[m] * sw[n]) * sum_k a[m, k] * w[n, k]
+ * a: int8 codes [M, K], rows a_stride apart; a_scales [M] (a_per_row != 0: the token scales of
+ *    qssm_rmsnorm_i8) or [1]; w: int8 codes [N, K], rows w_stride apart, and w_scales [N], as
+ *    qssm_quant_w8 writes them; bias [N] fp32 or NULL; y [M, N] fp32 or fp16, rows y_stride apart.
+ * A scale that is not valid gives its row or column y = bias. The integer sum is exact (K <= 131071,
+ * else QSSM_ERR_UNSUPPORTED), is rounded once to fp32, and one fused multiply-add scales it and
+ * adds the bias; an fp16 y is rounded once more. K == 0 gives y = bias. Any M, N >= 0, any
+ * alignment of a and w; rows of K bytes with strides and addresses that are multiples of 16 take
+ * the fast forms.
+ */
+typedef struct qssm_gemm_w8a8_args {
+  int64_t M, N, K;
+  int32_t a_per_row;
+  int32_t y_dtype;          /* QSSM_F32 or QSSM_F16 */
+  const int8_t* a;          /* [M, K] */
+  int64_t a_stride;         /* >= K */
+  const float* a_scales;    /* [M] or [1] */
+  const int8_t* w;          /* [N, K] */
+  int64_t w_stride;         /* >= K */
+  const float* w_scales;    /* [N] */
+  const float* bias;        /* [N] or NULL */
+  void* y;                  /* [M, N] */
+  int64_t y_stride;         /* >= N */
+} qssm_gemm_w8a8_args;
+
+qssm_status qssm_gemm_w8a8(const qssm_gemm_w8a8_args* a, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
  * W4A8 linear layer: 4-bit weights x int8 activations on int8 MFMA with int32 accumulation.
  * Quamba2, abstract (W4A8 for large-batch decoding: the in and out projections around the
  * recurrence).
@@ -501,14 +618,19 @@ qssm_status qssm_calib_s4d_state_scale(int64_t H, int64_t N, int64_t L, const in
 qssm_status qssm_quant_w4(const float* w, int64_t N, int64_t K, int32_t group, float* scales,
                           uint8_t* packed);
 
+/* Offline 8-bit weight quantization for qssm_gemm_w8a8 (host): for weights w [N, K] fp32, scales[n] =
+ * fl32(absmax / 127) of row n's finite values (absmax 0 -> 1, clamped to [2^-100, 2^100]) and
+ * codes[n, k] = clamp(RNE(w / s), -128, 127) by the exact quotient (NaN -> 0, +-Inf saturate). */
+qssm_status qssm_quant_w8(const float* w, int64_t N, int64_t K, float* scales, int8_t* codes);
+
 /* ---------------------------------------------------------------------------------------------
  * Library information. */
 const char* qssm_status_string(qssm_status s);
 /* Message of the last failing call on this host thread ("" if none). */
 const char* qssm_last_error(void);
 int32_t qssm_version(void);
-/* sizeof of the argument structs as compiled (0: scan, 1: s4d, 2: ssd, 3: update, 4: gemm), so
- * bindings can check their layout. Returns 0 for an unknown kind. */
+/* sizeof of the argument structs as compiled (0: scan, 1: s4d, 2: ssd, 3: update, 4: gemm, 5:
+ * rmsnorm, 6: gemm_w8a8), so bindings can check their layout. Returns 0 for an unknown kind. */
 size_t qssm_args_size(int32_t kind);
 
 /* ---------------------------------------------------------------------------------------------

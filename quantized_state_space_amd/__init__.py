@@ -8,6 +8,7 @@ fallback: if ``libqssm.so`` is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -73,7 +74,23 @@ class GemmArgs(ctypes.Structure):
                 ("a", _P), ("a_scale", _P), ("w", _P), ("w_scales", _P), ("bias", _P), ("y", _P)]
 
 
-ARG_STRUCTS = {0: ScanArgs, 1: S4dArgs, 2: SsdArgs, 3: UpdateArgs, 4: GemmArgs}
+class RmsnormArgs(ctypes.Structure):
+    _fields_ = [("rows", _I64), ("dim", _I64), ("norm_groups", _I32), ("x_dtype", _I32), ("x", _P),
+                ("x_stride", _I64), ("residual_dtype", _I32), ("gate_dtype", _I32),
+                ("residual", _P), ("residual_stride", _I64), ("residual_out", _P),
+                ("residual_out_stride", _I64), ("gate", _P), ("gate_stride", _I64),
+                ("weight", _P), ("eps", ctypes.c_float), ("compute_scales", _I32),
+                ("scales", _P), ("q", _P), ("q_stride", _I64)]
+
+
+class GemmW8A8Args(ctypes.Structure):
+    _fields_ = [("M", _I64), ("N", _I64), ("K", _I64), ("a_per_row", _I32), ("y_dtype", _I32),
+                ("a", _P), ("a_stride", _I64), ("a_scales", _P), ("w", _P), ("w_stride", _I64),
+                ("w_scales", _P), ("bias", _P), ("y", _P), ("y_stride", _I64)]
+
+
+ARG_STRUCTS = {0: ScanArgs, 1: S4dArgs, 2: SsdArgs, 3: UpdateArgs, 4: GemmArgs, 5: RmsnormArgs,
+               6: GemmW8A8Args}
 
 # Every symbol include/qssm.h declares, with its ctypes signature.
 SIGNATURES = {
@@ -92,6 +109,12 @@ SIGNATURES = {
     "qssm_ssd_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(SsdArgs)]),
     "qssm_ssd_chunk_int8": (_I32, [ctypes.POINTER(SsdArgs), _P, ctypes.c_size_t, _P]),
     "qssm_state_update": (_I32, [ctypes.POINTER(UpdateArgs), _P]),
+    "qssm_state_update_i8": (_I32, [ctypes.POINTER(UpdateArgs), _P, _P, _P, _P]),
+    "qssm_state_quant": (_I32, [_P, _I32, _I64, _I64, _P, _P, _P]),
+    "qssm_state_dequant": (_I32, [_P, _P, _I64, _I64, _P, _I32, _P]),
+    "qssm_rmsnorm_i8": (_I32, [ctypes.POINTER(RmsnormArgs), _P]),
+    "qssm_gemm_w8a8": (_I32, [ctypes.POINTER(GemmW8A8Args), _P]),
+    "qssm_quant_w8": (_I32, [_P, _I64, _I64, _P, _P]),
     "qssm_gemm_w4a8": (_I32, [ctypes.POINTER(GemmArgs), _P]),
     "qssm_quant_w4": (_I32, [_P, _I64, _I64, _I32, _P, _P]),
     "qssm_calib_channel_absmax": (_I32, [_P, _I64, _I64, _I64, _P]),
@@ -404,15 +427,26 @@ def update_args(x, x_group_of, x_scales, Bm, Cm, B_scales, C_scales, gs, delta, 
                 Dskip=None, xq_out=None, Bq_out=None, Cq_out=None, y_group_of=None,
                 y_scales=None, y_bias=None):
     """y is float32 or int8 (then y_group_of [nh * P], y_scales [Gy] and the optional correction
-    y_bias [nh * P] are given)."""
+    y_bias [nh * P] are given). state: float32 or float16 for qssm_state_update, int8 codes for
+    qssm_state_update_i8."""
     torch = _t()
     B, nh, P = x.shape
     Gbc, N = Bm.shape[1], Bm.shape[2]
-    sdt = QSSM_F32 if state.dtype == torch.float32 else QSSM_F16
+    sdt = {torch.float32: QSSM_F32, torch.int8: QSSM_I8}.get(state.dtype, QSSM_F16)
+    if sdt == QSSM_I8:
+        want = {"state": (state, (B, nh, P, N)), "y": (y, (B, nh, P)), "C": (Cm, (B, Gbc, N)),
+                "delta": (delta, (B, nh)), "A": (A, (nh,)), "x_group_of": (x_group_of, (nh * P,)),
+                "B_scales": (B_scales, (Gbc * N // gs,)), "C_scales": (C_scales, (Gbc * N // gs,)),
+                "Dskip": (Dskip, (nh,)), "xq_out": (xq_out, (B, nh, P)),
+                "Bq_out": (Bq_out, (B, Gbc, N)), "Cq_out": (Cq_out, (B, Gbc, N))}
+        for name, (t, shape) in want.items():
+            if t is not None and (t.numel() != math.prod(shape) or
+                                  (name == "state" and tuple(t.shape) != shape)):
+                raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     keep = (x, x_group_of, x_scales, Bm, Cm, B_scales, C_scales, delta, A, state, y, Dskip, xq_out,
             Bq_out, Cq_out, y_group_of, y_scales, y_bias)
     ydt = {torch.float32: QSSM_F32, torch.int8: QSSM_I8}.get(y.dtype, -1)
-    return _fill(UpdateArgs(), keep=keep, **_y_out_fields(y, nh * P, y_group_of, y_scales, y_bias),
+    st = _fill(UpdateArgs(), keep=keep, **_y_out_fields(y, nh * P, y_group_of, y_scales, y_bias),
                  y_dtype=ydt, batch=B, nheads=nh, headdim=P, dstate=N, ngroups=Gbc,
                  x_groups=int(x_scales.numel()), x=_ptr(x, torch.float32, "x"),
                  x_group_of=_ptr(x_group_of, torch.uint8, "x_group_of"),
@@ -426,10 +460,198 @@ def update_args(x, x_group_of, x_scales, Bm, Cm, B_scales, C_scales, gs, delta, 
                  xq_out=_ptr(xq_out, torch.int8, "xq_out", True),
                  Bq_out=_ptr(Bq_out, torch.int8, "Bq_out", True),
                  Cq_out=_ptr(Cq_out, torch.int8, "Cq_out", True))
+    st._state = state
+    return st
 
 
 def qssm_state_update(args, stream=None):
     _check("qssm_state_update", load().qssm_state_update(ctypes.byref(args), _stream(stream)))
+
+
+# ------------------------------------------------------------------------------------------------
+# int8 state, RMS norm with an int8 output, W8A8 linear layer. These run on their tensors' device
+# whatever the current one is; its current stream is the default.
+
+def _device_of(*tensors):
+    """The one GPU that holds every tensor given."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
+    return dev
+
+
+def _call(name, dev, stream, *args, keep=()):
+    """Calls an entry point on device `dev`: on `stream`, or on that device's current stream. The
+    tensors in `keep` are marked as used by a stream that is not theirs by default."""
+    torch = _t()
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    else:
+        if stream.device != dev:
+            raise ValueError(f"stream of {stream.device} for tensors on {dev}")
+        if not torch.cuda.is_current_stream_capturing():
+            for t in keep:
+                t.record_stream(stream)
+    f = getattr(load(), name)
+    if torch.cuda.current_device() == dev.index:
+        status = f(*args, ctypes.c_void_p(stream.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, ctypes.c_void_p(stream.cuda_stream))
+    _check(name, status)
+
+
+def _float_type(t, name):
+    """QSSM_F32 or QSSM_F16 of a tensor (0 for None)."""
+    torch = _t()
+    if t is None:
+        return QSSM_F32
+    if t.dtype == torch.float32:
+        return QSSM_F32
+    if t.dtype == torch.float16:
+        return QSSM_F16
+    raise TypeError(f"{name} must be float32 or float16, got {t.dtype}")
+
+
+def _rows(t, dtype, name, shape, optional=False):
+    """(address, row stride) of a 2-D GPU tensor whose rows are contiguous."""
+    if t is None:
+        if optional:
+            return None, 0
+        raise ValueError(f"{name} is required")
+    torch = _t()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    rows, cols = shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    stride = cols if rows <= 1 else t.stride(0)
+    if stride < cols:
+        raise ValueError(f"{name} has overlapping rows")
+    return ctypes.c_void_p(t.data_ptr()), stride
+
+
+def _row_values(h, codes, scales, name):
+    """(rows, N) of state rows h [..., N] with codes of the same shape and one scale a row."""
+    torch = _t()
+    if h.dim() < 1 or codes.shape != h.shape or scales.shape != h.shape[:-1]:
+        raise ValueError(f"{name} and codes must be [..., N] of one shape and scales [...]")
+    if codes.dtype != torch.int8 or scales.dtype != torch.float32:
+        raise TypeError("codes must be int8 and scales float32")
+    return scales.numel(), h.shape[-1]
+
+
+def qssm_state_quant(h, codes, scales, stream=None):
+    """h [..., N] float32 or float16 -> codes int8 [..., N] and scales float32 [...], one a row."""
+    rows, N = _row_values(h, codes, scales, "h")
+    _call("qssm_state_quant", _device_of(h, codes, scales), stream, _ptr(h, None, "h"),
+          _float_type(h, "h"), rows, N, _ptr(codes, None, "codes"), _ptr(scales, None, "scales"),
+          keep=(h, codes, scales))
+    return codes, scales
+
+
+def qssm_state_dequant(codes, scales, out, stream=None):
+    """out [..., N] float32 or float16 = scales * codes."""
+    rows, N = _row_values(out, codes, scales, "out")
+    _call("qssm_state_dequant", _device_of(out, codes, scales), stream, _ptr(codes, None, "codes"),
+          _ptr(scales, None, "scales"), rows, N, _ptr(out, None, "out"), _float_type(out, "out"),
+          keep=(codes, scales, out))
+    return out
+
+
+def qssm_state_update_i8(args, state_scales, state_in=None, scales_in=None, stream=None):
+    """The decode update on an int8 state: args from update_args with an int8 state (the codes
+    written), state_scales float32 [B, nh, P] the scales written; state_in and scales_in the codes
+    and scales read (both None: in place)."""
+    torch = _t()
+    state = args._state
+    if state.dtype != torch.int8:
+        raise TypeError("update_args was given a state that is not int8")
+    if state_scales.shape != state.shape[:-1] or (scales_in is not None and
+                                                  scales_in.shape != state.shape[:-1]):
+        raise ValueError("the scales must be [B, nh, P]")
+    if state_in is not None and state_in.shape != state.shape:
+        raise ValueError("state_in must have the state's shape")
+    given = (state_scales, state_in, scales_in)
+    _call("qssm_state_update_i8", _device_of(state, *given), stream, ctypes.byref(args),
+          _ptr(state_in, torch.int8, "state_in", True), _ptr(scales_in, torch.float32, "scales_in", True),
+          _ptr(state_scales, torch.float32, "state_scales"),
+          keep=[t for t in given if t is not None] + args._keep)
+
+
+def rmsnorm_args(x, q, scales, weight=None, eps=1e-5, residual=None, residual_out=None, gate=None,
+                 norm_groups=1, compute_scales=True):
+    """x [M, D] float32 or float16 (rows may lie apart, as slices of a wider tensor do), q int8
+    [M, D]; scales float32 [M] (written) or, with compute_scales False, [1] (the static scale);
+    weight float32 [D]; residual and residual_out [M, D] of one type; gate [M, D]."""
+    torch = _t()
+    if x.dim() != 2:
+        raise ValueError("x must be [M, D]")
+    M, D = x.shape
+    if residual is not None and residual_out is not None and residual.dtype != residual_out.dtype:
+        raise TypeError("residual and residual_out must have one type")
+    if scales.numel() != (M if compute_scales else 1):
+        raise ValueError("scales must be [M], or [1] with compute_scales False")
+    if weight is not None and weight.numel() != D:
+        raise ValueError("weight must be [D]")
+    px, xs = _rows(x, None, "x", (M, D))
+    pr, rs = _rows(residual, None, "residual", (M, D), True)
+    po, ros = _rows(residual_out, None, "residual_out", (M, D), True)
+    pg, gs = _rows(gate, None, "gate", (M, D), True)
+    pq, qst = _rows(q, torch.int8, "q", (M, D))
+    keep = (x, q, scales, weight, residual, residual_out, gate)
+    st = _fill(RmsnormArgs(), keep=keep, rows=M, dim=D, norm_groups=int(norm_groups),
+               x_dtype=_float_type(x, "x"), x=px, x_stride=xs,
+               residual_dtype=_float_type(residual if residual is not None else residual_out,
+                                          "residual"),
+               gate_dtype=_float_type(gate, "gate"), residual=pr, residual_stride=rs,
+               residual_out=po, residual_out_stride=ros, gate=pg, gate_stride=gs,
+               weight=_ptr(weight, torch.float32, "weight", True), eps=float(eps),
+               compute_scales=int(bool(compute_scales)),
+               scales=_ptr(scales, torch.float32, "scales"), q=pq, q_stride=qst)
+    st._device = _device_of(*keep)
+    return st
+
+
+def qssm_rmsnorm_i8(args, stream=None):
+    _call("qssm_rmsnorm_i8", args._device, stream, ctypes.byref(args), keep=args._keep)
+
+
+def gemm_w8a8_args(a, a_scales, w, w_scales, y, bias=None):
+    """a int8 [M, K] and w int8 [N, K] (rows may lie apart); a_scales float32 [M] or [1], w_scales
+    float32 [N]; y float32 or float16 [M, N] (rows may lie apart); bias float32 [N] or None."""
+    torch = _t()
+    if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1]:
+        raise ValueError("a must be [M, K] and w [N, K]")
+    (M, K), N = a.shape, w.shape[0]
+    if a_scales.numel() not in (1, M) or w_scales.numel() != N or (bias is not None and
+                                                                   bias.numel() != N):
+        raise ValueError("a_scales must be [M] or [1], w_scales [N] and bias [N]")
+    pa, sa = _rows(a, torch.int8, "a", (M, K))
+    pw, sw = _rows(w, torch.int8, "w", (N, K))
+    py, sy = _rows(y, None, "y", (M, N))
+    keep = (a, a_scales, w, w_scales, y, bias)
+    st = _fill(GemmW8A8Args(), keep=keep, M=M, N=N, K=K, a_per_row=int(a_scales.numel() == M),
+               y_dtype=_float_type(y, "y"), a=pa, a_stride=sa,
+               a_scales=_ptr(a_scales, torch.float32, "a_scales"), w=pw, w_stride=sw,
+               w_scales=_ptr(w_scales, torch.float32, "w_scales"),
+               bias=_ptr(bias, torch.float32, "bias", True), y=py, y_stride=sy)
+    st._device = _device_of(*keep)
+    return st
+
+
+def qssm_gemm_w8a8(args, stream=None):
+    _call("qssm_gemm_w8a8", args._device, stream, ctypes.byref(args), keep=args._keep)
 
 
 # ------------------------------------------------------------------------------------------------
@@ -472,6 +694,18 @@ def qssm_quant_w4(w, group):
     _check("qssm_quant_w4", load().qssm_quant_w4(_np_ptr(w), N, K, group, _np_ptr(scales),
                                                   _np_ptr(packed)))
     return scales, packed
+
+
+def qssm_quant_w8(w):
+    """Offline 8-bit weight quantization (host): returns (scales [N] float32, codes [N, K] int8)."""
+    import numpy as np
+    w = np.ascontiguousarray(w, dtype=np.float32)
+    N, K = w.shape
+    scales = np.empty(N, np.float32)
+    codes = np.empty((N, K), np.int8)
+    _check("qssm_quant_w8", load().qssm_quant_w8(_np_ptr(w), N, K, _np_ptr(scales), _np_ptr(codes)))
+    return scales, codes
+
 
 def _np_ptr(a):
     return ctypes.c_void_p(a.ctypes.data)

@@ -19,8 +19,11 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", os.path.
           "-Wall", "-Wno-unused-function",
           # packed fp32 instructions are kept out of every kernel
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
-# per-source extra flags: host calibration evaluates its arithmetic exactly as written
-EXTRA = {"calib.cpp": ["-ffp-contract=off"]}
+# per-source extra flags: host calibration, and the kernels whose roundings are part of their
+# definition, evaluate their arithmetic exactly as written (a product rounded to fp16 would else
+# become one mixed-precision fma, which skips the rounding to fp32)
+EXACT = ["-ffp-contract=off"]
+EXTRA = {"calib.cpp": EXACT, "rmsnorm_i8.hip": EXACT, "state_cache.hip": EXACT, "gemm_w8a8.hip": EXACT}
 
 
 def sources():

@@ -283,4 +283,24 @@ qssm_status qssm_quant_w4(const float* w, int64_t N, int64_t K, int32_t group, f
   return QSSM_OK;
 }
 
+qssm_status qssm_quant_w8(const float* w, int64_t N, int64_t K, float* scales, int8_t* codes) {
+  qssm::clear_error();
+  if (N < 0 || K < 0) return fail(QSSM_ERR_INVALID_ARG, "negative extent");
+  if ((N > 0 && !scales) || (N > 0 && K > 0 && (!w || !codes)))
+    return fail(QSSM_ERR_INVALID_ARG, "null pointer");
+  for (int64_t n = 0; n < N; ++n) {
+    float m = 0.0f;
+    for (int64_t k = 0; k < K; ++k) {
+      const float a = std::fabs(w[n * K + k]);
+      if (a <= std::numeric_limits<float>::max() && a > m) m = a;
+    }
+    float s = (m == 0.0f) ? 1.0f : m / 127.0f;
+    if (s < 0x1p-100f) s = 0x1p-100f;
+    if (s > 0x1p100f) s = 0x1p100f;
+    scales[n] = s;
+    for (int64_t k = 0; k < K; ++k) codes[n * K + k] = qssm::quant8(w[n * K + k], s);
+  }
+  return QSSM_OK;
+}
+
 }  // extern "C"

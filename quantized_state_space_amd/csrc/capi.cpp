@@ -55,6 +55,8 @@ size_t qssm_args_size(int32_t kind) {
     case 2: return sizeof(qssm_ssd_args);
     case 3: return sizeof(qssm_update_args);
     case 4: return sizeof(qssm_gemm_args);
+    case 5: return sizeof(qssm_rmsnorm_args);
+    case 6: return sizeof(qssm_gemm_w8a8_args);
     default: return 0;
   }
 }

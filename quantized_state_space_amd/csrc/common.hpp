@@ -131,10 +131,55 @@ __device__ __forceinline__ float scale_from_absmax(float a) {
   return fminf(fmaxf(s, 0x1p-100f), 0x1p100f);
 }
 
+// Scale of one row from its absmax, where a kernel makes a scale for every row: the product with
+// fl32(1/127) (within one unit in the last place of absmax / 127, without a division), 0 -> 1, clamped
+// to the valid range. absmax / scale stays below 127.0001.
+__device__ __forceinline__ float row_scale(float a) {
+  if (a == 0.0f) return 1.0f;
+  return fminf(fmaxf(a * (1.0f / 127.0f), 0x1p-100f), 0x1p100f);
+}
+
 // |v| if finite, else 0 (absmax ignores NaN and infinities).
 __device__ __forceinline__ float finite_abs(float v) {
   float a = fabsf(v);
   return (a <= 3.402823466e38f) ? a : 0.0f;
+}
+
+// Codes of N values with one scale, packed little-endian: clamp(RNE(v / s), -128, 127), NaN 0, every
+// code 0 for an invalid scale (the rule above). With r = fl32(1/s), adding 1.5 * 2^23 in the fused
+// multiply-add leaves c = RNE(v r) in the low bits of m. c is the nearest code when the remainder
+// e = v - c s is inside (-s/2, s/2): the fma rounds it once, rounding is monotone and s/2 is a
+// float, so |e| < s/2 after rounding implies it before. That fails only within ~2^-16 of a
+// half-integer (or for a NaN); a wave with such a lane decides all its codes by quant8_r. Values are
+// clamped to [-128 s, 127 s] first (fl(127 s) / s still rounds to 127). IN_RANGE: the caller knows
+// that every value is finite and |v| <= 127.4 s, as with the scale of the row's own absmax.
+template <bool IN_RANGE, int N>
+__device__ __forceinline__ void quant_row(const float (&v)[N], float s, uint32_t (&w)[N / 4]) {
+  constexpr float kMagic = 12582912.0f;
+  const float r = recip_or_zero(s);
+  const float half = 0.5f * s, hi = 127.0f * s, lo = -128.0f * s;
+  uint32_t m[N];
+  bool bad = r == 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float x = IN_RANGE ? v[i] : __builtin_amdgcn_fmed3f(v[i], lo, hi);
+    const float mi = fmaf(x, r, kMagic);
+    const float e = fmaf(-(mi - kMagic), s, x);
+    bad |= !(fabsf(e) < half);
+    if (!IN_RANGE) bad |= v[i] != v[i];
+    m[i] = __float_as_uint(mi);
+  }
+  if (bad) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) m[i] = (uint32_t)(int)quant8_r(v[i], s, r);
+  }
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    // bytes [m0, m1, 0, 0] and [m2, m3, 0, 0], then the low halves side by side
+    const uint32_t lo2 = __builtin_amdgcn_perm(m[4 * i + 1], m[4 * i], 0x0c0c0400u);
+    const uint32_t hi2 = __builtin_amdgcn_perm(m[4 * i + 3], m[4 * i + 2], 0x0c0c0400u);
+    w[i] = lo2 | (hi2 << 16);
+  }
 }
 
 // Wave-uniform value in an SGPR (so loads indexed by it can go through the scalar cache).

@@ -1,0 +1,345 @@
+// RMS norm with an int8 output: the residual stream's addition or Mamba2's gate, the norm over one
+// or several channel groups, and the quantization of a W8A8 / W4A8 projection's input, in one pass.
+//
+//     h = round(x + residual)      t = fl32(h * silu(gate))      r_g = fl32((sum t^2 / Dg + eps)^-1/2)
+//     v = fl32(fl32(t r_g) w)      s = row_scale(absmax v) or static      q = quant8(v, s)
+//
+// One workgroup owns one row and holds it in registers from the loads to the codes (VPT vectors of
+// VEC channels per thread, vector v of thread i at channel (v T + i) VEC), so every tensor is read
+// and written once: the floor is the bytes. Two workgroup reductions join the threads: the sum of
+// squares and the largest |v|. The sum is taken in fp64 (squares of fp32 values are exact there), so
+// that r, and with it every code, does not depend on the order of the sum beyond ~2^-50; silu is
+// evaluated in fp64 to the same end.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "common.hpp"
+
+using namespace qssm;
+
+namespace {
+
+constexpr int kMaxThreads = 1024;
+constexpr int kMaxWaves = kMaxThreads / 64;
+constexpr int64_t kMaxDimNarrow = 8192;  // VEC = 1: 8 channels per thread
+constexpr int64_t kMaxDimWide = 32768;   // VEC = 8: 4 vectors of 8 per thread
+
+struct NormParams {
+  int64_t D, Dg;
+  int32_t Gn, dynamic;
+  const void* x;
+  const void* res;
+  void* res_out;
+  const void* gate;
+  int64_t xs, rs, ros, gs, qs;
+  const float* w;
+  float eps;
+  float* scales;
+  int8_t* q;
+};
+
+// VEC consecutive elements of row data as fp32 (VEC = 8: 16-byte aligned)
+template <int VEC, bool F16>
+__device__ __forceinline__ void load_vec(const void* base, int64_t i, float (&o)[VEC]) {
+  if constexpr (F16) {
+    const __half* p = reinterpret_cast<const __half*>(base) + i;
+    if constexpr (VEC == 8) {
+      const uint4 raw = *reinterpret_cast<const uint4*>(p);
+      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const __half2 v = *reinterpret_cast<const __half2*>(&w[k]);
+        o[2 * k] = __low2float(v);
+        o[2 * k + 1] = __high2float(v);
+      }
+    } else {
+      o[0] = __half2float(p[0]);
+    }
+  } else {
+    const float* p = reinterpret_cast<const float*>(base) + i;
+    if constexpr (VEC == 8) {
+      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+      o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+      o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+    } else {
+      o[0] = p[0];
+    }
+  }
+}
+
+// Rounds v to the stream's type and stores it; v becomes the stored value.
+template <int VEC, bool F16>
+__device__ __forceinline__ void round_store(void* base, int64_t i, float (&v)[VEC]) {
+  if constexpr (F16) {
+    __half h[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      h[k] = __float2half_rn(v[k]);
+      v[k] = __half2float(h[k]);
+    }
+    if (!base) return;
+    __half* p = reinterpret_cast<__half*>(base) + i;
+    if constexpr (VEC == 8) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = (uint32_t)__half_as_ushort(h[2 * k]) | ((uint32_t)__half_as_ushort(h[2 * k + 1]) << 16);
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      p[0] = h[0];
+    }
+  } else {
+    if (!base) return;
+    float* p = reinterpret_cast<float*>(base) + i;
+    if constexpr (VEC == 8) {
+      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      p[0] = v[0];
+    }
+  }
+}
+
+// silu(z) = z / (1 + e^-z), in fp64 and rounded once to fp32. e^x with x = -z clamped to +-700 (beyond
+// that silu is z or rounds to -0 either way): x = n ln2 + f, |f| <= ln2 / 2, the Taylor polynomial of
+// degree 10 in f (error f^11 / 11! < 2.2e-13). One Newton step takes the reciprocal to ~2^-47.
+__device__ __forceinline__ float silu_f64(float z) {
+  const double x = fmin(fmax(-(double)z, -700.0), 700.0);
+  const double n = rint(x * 1.4426950408889634);  // 1 / ln2
+  double f = fma(-n, 0x1.62e42fefa2000p-1, x);  // the leading 40 bits of ln2: n times it is exact
+  f = fma(-n, 0x1.9ef35793c7673p-41, f);          // the rest of ln2
+  double e = 1.0 / 3628800.0;
+  e = fma(e, f, 1.0 / 362880.0);
+  e = fma(e, f, 1.0 / 40320.0);
+  e = fma(e, f, 1.0 / 5040.0);
+  e = fma(e, f, 1.0 / 720.0);
+  e = fma(e, f, 1.0 / 120.0);
+  e = fma(e, f, 1.0 / 24.0);
+  e = fma(e, f, 1.0 / 6.0);
+  e = fma(e, f, 0.5);
+  e = fma(e, f, 1.0);
+  e = fma(e, f, 1.0);
+  const double d = 1.0 + ldexp(e, (int)n);
+  double r = __builtin_amdgcn_rcp(d);
+  r = fma(fma(-d, r, 1.0), r, r);
+  return (float)((double)z * r);
+}
+
+__device__ __forceinline__ float group_r(double sum, int64_t Dg, float eps) {
+  return (float)(1.0 / sqrt(sum / (double)Dg + (double)eps));
+}
+
+// RES: 0 no residual stream, 1 fp16, 2 fp32. GATE: 0 none, 1 fp16, 2 fp32.
+template <int VEC, int VPT, bool XF16, int RES, int GATE>
+__global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];  // several groups: one partial per vector
+  __shared__ double red_sum[kMaxWaves];
+  __shared__ float red_max[kMaxWaves];
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, T = blockDim.x, lane = tid & 63, wave = tid >> 6, nw = T >> 6;
+
+  float t[VPT][VEC];
+  double sum = 0.0;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int64_t c = (int64_t)(v * T + tid) * VEC;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) t[v][k] = 0.0f;
+    if (c < p.D) {
+      load_vec<VEC, XF16>(p.x, row * p.xs + c, t[v]);
+      if constexpr (RES != 0) {
+        if (p.res) {
+          float o[VEC];
+          load_vec<VEC, RES == 1>(p.res, row * p.rs + c, o);
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) t[v][k] += o[k];
+        }
+        // res_out may be res: each element is read above by the thread that writes it here
+        round_store<VEC, RES == 1>(p.res_out, row * p.ros + c, t[v]);
+      }
+      if constexpr (GATE != 0) {
+        float z[VEC];
+        load_vec<VEC, GATE == 1>(p.gate, row * p.gs + c, z);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) t[v][k] *= silu_f64(z[k]);
+      }
+    }
+    double part = 0.0;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) part = fma((double)t[v][k], (double)t[v][k], part);
+    if (p.Gn > 1) {
+      // a vector lies in one group (Dg % VEC == 0)
+      if (c < p.D) {
+        if constexpr (VEC == 1) reinterpret_cast<float*>(smem)[c] = t[v][0];
+        else reinterpret_cast<double*>(smem)[c / VEC] = part;
+      }
+    } else {
+      sum += part;
+    }
+  }
+
+  float r1 = 0.0f;
+  if (p.Gn > 1) {
+    // wave k sums the groups k, k + nw, ... and leaves r in the group's first slot
+    __syncthreads();
+    const int64_t per = p.Dg / VEC;
+    for (int64_t g = wave; g < p.Gn; g += nw) {
+      double a = 0.0;
+      for (int64_t i = g * per + lane; i < (g + 1) * per; i += 64) {
+        if constexpr (VEC == 1) {
+          const double u = (double)reinterpret_cast<const float*>(smem)[i];
+          a = fma(u, u, a);
+        } else {
+          a += reinterpret_cast<const double*>(smem)[i];
+        }
+      }
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) a += __shfl_xor(a, off, 64);
+      // every lane's reads precede: the shuffles wait for all of them
+      if (lane == 0) {
+        const float r = group_r(a, p.Dg, p.eps);
+        if constexpr (VEC == 1) reinterpret_cast<float*>(smem)[g * per] = r;
+        else reinterpret_cast<float*>(smem)[2 * g * per] = r;
+      }
+    }
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+    if (lane == 0) red_sum[wave] = sum;
+    __syncthreads();
+    double a = 0.0;
+    for (int k = 0; k < nw; ++k) a += red_sum[k];
+    r1 = group_r(a, p.Dg, p.eps);
+  }
+
+  float amax = 0.0f;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int64_t c = (int64_t)(v * T + tid) * VEC;
+    if (c < p.D) {
+      float r = r1;
+      if (p.Gn > 1) {
+        const int64_t g = c / p.Dg, per = p.Dg / VEC;
+        r = reinterpret_cast<const float*>(smem)[VEC == 1 ? g * per : 2 * g * per];
+      }
+      float w[VEC];
+      if (p.w) load_vec<VEC, false>(p.w, c, w);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        t[v][k] *= r;
+        if (p.w) t[v][k] *= w[k];
+        amax = fmaxf(amax, finite_abs(t[v][k]));
+      }
+    }
+  }
+
+  float s;
+  if (p.dynamic) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
+    if (lane == 0) red_max[wave] = amax;
+    __syncthreads();
+    for (int k = 0; k < nw; ++k) amax = fmaxf(amax, red_max[k]);
+    s = row_scale(amax);
+    if (tid == 0) p.scales[row] = s;
+  } else {
+    s = p.scales[0];
+  }
+
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int64_t c = (int64_t)(v * T + tid) * VEC;
+    if (c < p.D) {
+      int8_t* o = p.q + row * p.qs + c;
+      if constexpr (VEC == 8) {
+        uint32_t w[2];
+        quant_row<false, 8>(t[v], s, w);
+        *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+      } else {
+        *o = quant8_r(t[v][0], s, recip_or_zero(s));
+      }
+    }
+  }
+}
+
+template <int VEC, int VPT, bool XF16>
+void launch_vpt(const NormParams& p, int res, int gate, unsigned rows, int threads, hipStream_t st) {
+  size_t smem = 0;
+  if (p.Gn > 1) smem = VEC == 1 ? (size_t)p.D * 4 : (size_t)(p.D / VEC) * 8;
+  if (gate == 1) k_rmsnorm_i8<VEC, VPT, XF16, 0, 1><<<rows, threads, smem, st>>>(p);
+  else if (gate == 2) k_rmsnorm_i8<VEC, VPT, XF16, 0, 2><<<rows, threads, smem, st>>>(p);
+  else if (res == 1) k_rmsnorm_i8<VEC, VPT, XF16, 1, 0><<<rows, threads, smem, st>>>(p);
+  else if (res == 2) k_rmsnorm_i8<VEC, VPT, XF16, 2, 0><<<rows, threads, smem, st>>>(p);
+  else k_rmsnorm_i8<VEC, VPT, XF16, 0, 0><<<rows, threads, smem, st>>>(p);
+}
+
+template <int VEC, bool XF16>
+void launch_vec(const NormParams& p, int res, int gate, unsigned rows, hipStream_t st) {
+  const int64_t nvec = p.D / VEC;
+  const int threads = (int)std::min<int64_t>(cdiv(nvec, 64) * 64, kMaxThreads);
+  const int64_t vpt = cdiv(nvec, threads);
+  if (vpt == 1) launch_vpt<VEC, 1, XF16>(p, res, gate, rows, threads, st);
+  else if (VEC == 8 && vpt == 2) launch_vpt<VEC, 2, XF16>(p, res, gate, rows, threads, st);
+  else launch_vpt<VEC, VEC == 8 ? 4 : 8, XF16>(p, res, gate, rows, threads, st);
+}
+
+bool dtype_ok(int32_t t) { return t == QSSM_F32 || t == QSSM_F16; }
+
+}  // namespace
+
+extern "C" qssm_status qssm_rmsnorm_i8(const qssm_rmsnorm_args* a, hipStream_t stream) {
+  clear_error();
+  if (!a) return fail(QSSM_ERR_INVALID_ARG, "args is null");
+  const int64_t M = a->rows, D = a->dim;
+  if (M < 0 || D < 1) return fail(QSSM_ERR_INVALID_ARG, "rows must be >= 0 and dim >= 1");
+  if (a->norm_groups < 1 || D % a->norm_groups != 0)
+    return fail(QSSM_ERR_INVALID_ARG, "norm_groups must divide dim");
+  if (!dtype_ok(a->x_dtype)) return fail(QSSM_ERR_INVALID_ARG, "x_dtype must be QSSM_F32 or QSSM_F16");
+  const bool stream_on = a->residual || a->residual_out;
+  if (stream_on && !dtype_ok(a->residual_dtype))
+    return fail(QSSM_ERR_INVALID_ARG, "residual_dtype must be QSSM_F32 or QSSM_F16");
+  if (a->gate && !dtype_ok(a->gate_dtype))
+    return fail(QSSM_ERR_INVALID_ARG, "gate_dtype must be QSSM_F32 or QSSM_F16");
+  if (a->gate && stream_on)
+    return fail(QSSM_ERR_UNSUPPORTED, "a gate together with a residual stream");
+  if (!(a->eps >= 0.0f) || a->eps > 3.402823466e38f)
+    return fail(QSSM_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  const int64_t lim = (int64_t)1 << 40;  // row offsets stay far inside 64 bits
+  if (a->x_stride < D || a->q_stride < D || (a->residual && a->residual_stride < D) ||
+      (a->residual_out && a->residual_out_stride < D) || (a->gate && a->gate_stride < D))
+    return fail(QSSM_ERR_INVALID_ARG, "a row stride is smaller than dim");
+  if (a->x_stride > lim || a->q_stride > lim || (a->residual && a->residual_stride > lim) ||
+      (a->residual_out && a->residual_out_stride > lim) || (a->gate && a->gate_stride > lim) ||
+      M > 0x7fffffff)
+    return fail(QSSM_ERR_UNSUPPORTED, "rows above 2^31 - 1 or a stride above 2^40");
+  if (a->residual && a->residual == a->residual_out && a->residual_stride != a->residual_out_stride)
+    return fail(QSSM_ERR_INVALID_ARG, "residual_out == residual needs one stride");
+  const int64_t Dg = D / a->norm_groups;
+  uint64_t a16 = (uint64_t)(uintptr_t)a->x | (uintptr_t)a->residual | (uintptr_t)a->residual_out |
+                 (uintptr_t)a->gate | (uintptr_t)a->weight;
+  int64_t strides = a->x_stride | a->q_stride;
+  if (a->residual) strides |= a->residual_stride;
+  if (a->residual_out) strides |= a->residual_out_stride;
+  if (a->gate) strides |= a->gate_stride;
+  const bool wide = Dg % 8 == 0 && strides % 8 == 0 && a16 % 16 == 0 && (uintptr_t)a->q % 8 == 0;
+  if (D > (wide ? kMaxDimWide : kMaxDimNarrow))
+    return fail(QSSM_ERR_UNSUPPORTED, "dim above 8192 (32768 with aligned rows and groups)");
+  if (M == 0) return QSSM_OK;
+  if (!a->x || !a->scales || !a->q) return fail(QSSM_ERR_INVALID_ARG, "null required pointer");
+  NormParams p{D, Dg, a->norm_groups, a->compute_scales != 0, a->x, a->residual, a->residual_out,
+               a->gate, a->x_stride, a->residual_stride, a->residual_out_stride, a->gate_stride,
+               a->q_stride, a->weight, a->eps, a->scales, a->q};
+  const int res = !stream_on ? 0 : (a->residual_dtype == QSSM_F16 ? 1 : 2);
+  const int gate = !a->gate ? 0 : (a->gate_dtype == QSSM_F16 ? 1 : 2);
+  const bool xf16 = a->x_dtype == QSSM_F16;
+  if (wide) {
+    if (xf16) launch_vec<8, true>(p, res, gate, (unsigned)M, stream);
+    else launch_vec<8, false>(p, res, gate, (unsigned)M, stream);
+  } else {
+    if (xf16) launch_vec<1, true>(p, res, gate, (unsigned)M, stream);
+    else launch_vec<1, false>(p, res, gate, (unsigned)M, stream);
+  }
+  return launch_status("rmsnorm_i8");
+}

@@ -43,17 +43,10 @@ struct UpdParams {
   const float* y_bias;        // int8 output: [nh * P] or NULL
 };
 
-// CH consecutive states per thread access: 4 for fp32 (16 bytes), 8 for fp16 (16 bytes).
-// R = N / CH lanes share one state row.
-template <int F16, int R>
-__global__ __launch_bounds__(kThreads) void k_state_update(UpdParams p) {
-  constexpr int CH = F16 ? 8 : 4;
-  extern __shared__ float smem[];
-  float* xs = smem;                    // [P], padded to a multiple of 4
-  float* bs = xs + ((p.P + 3) & ~3);   // [N], 16-byte aligned (N % 4 == 0)
-  float* cs = bs + p.N;                // [N]
-
-  const int64_t bh = blockIdx.x;  // b * nh + h
+// Quantizes and dequantizes the P x values of (b, h) = bh and the N B/C values of its group into
+// LDS, publishing the codes where asked, and waits for the workgroup.
+__device__ __forceinline__ void stage_inputs(const UpdParams& p, int64_t bh, float* xs, float* bs,
+                                             float* cs) {
   const int64_t b = bh / p.nh, h = bh % p.nh;
   const int64_t g = h / p.hpg;
   const int ngs = (int)(p.N / p.gs);
@@ -79,6 +72,34 @@ __global__ __launch_bounds__(kThreads) void k_state_update(UpdParams p) {
     cs[n] = scale_ok(sc) ? (float)qc * sc : 0.0f;
   }
   __syncthreads();
+}
+
+// y of one row, fp32 or int8 codes. Persistent int8 output: fl32(y + correction term), the exact rule
+// with the channel's static output scale.
+__device__ __forceinline__ void store_y(const UpdParams& p, int64_t bh, int64_t h, int64_t row, float yv) {
+  if (p.yi8) {
+    const int64_t ch = h * p.P + row;
+    const float sy = p.y_scales[min((int)p.y_group_of[ch], p.Gy - 1)];
+    const float yb = p.y_bias ? p.y_bias[ch] : 0.0f;
+    reinterpret_cast<int8_t*>(p.y)[bh * p.P + row] = quant8_r(yv + yb, sy, recip_or_zero(sy));
+  } else {
+    reinterpret_cast<float*>(p.y)[bh * p.P + row] = yv;
+  }
+}
+
+// CH consecutive states per thread access: 4 for fp32 (16 bytes), 8 for fp16 (16 bytes).
+// R = N / CH lanes share one state row.
+template <int F16, int R>
+__global__ __launch_bounds__(kThreads) void k_state_update(UpdParams p) {
+  constexpr int CH = F16 ? 8 : 4;
+  extern __shared__ float smem[];
+  float* xs = smem;                    // [P], padded to a multiple of 4
+  float* bs = xs + ((p.P + 3) & ~3);   // [N], 16-byte aligned (N % 4 == 0)
+  float* cs = bs + p.N;                // [N]
+
+  const int64_t bh = blockIdx.x;  // b * nh + h
+  const int64_t h = bh % p.nh;
+  stage_inputs(p, bh, xs, bs, cs);
 
   const float dt = p.delta[bh];
   const float dA = expf(dt * p.A[h]);
@@ -145,16 +166,72 @@ __global__ __launch_bounds__(kThreads) void k_state_update(UpdParams p) {
 #pragma unroll
     for (int off = R / 2; off > 0; off >>= 1) yp += __shfl_xor(yp, off, 64);
     if (on && (lane % R) == 0) {
-      const float yv = fmaf(Dh, xs[row], yp);
-      if (p.yi8) {
-        // persistent int8 output: fl32(y + correction term), the exact rule with the channel's
-        // static output scale
-        const int64_t ch = h * p.P + row;
-        const float sy = p.y_scales[min((int)p.y_group_of[ch], p.Gy - 1)];
-        const float yb = p.y_bias ? p.y_bias[ch] : 0.0f;
-        reinterpret_cast<int8_t*>(p.y)[bh * p.P + row] = quant8_r(yv + yb, sy, recip_or_zero(sy));
-      } else {
-        reinterpret_cast<float*>(p.y)[bh * p.P + row] = yv;
+      store_y(p, bh, h, row, fmaf(Dh, xs[row], yp));
+    }
+  }
+}
+
+// int8 state: R = N / 16 lanes share one row, 16 codes (16 bytes) each, and the row's scale. The row's
+// new absmax and its readout are shuffle reductions over those lanes; the new state stays in
+// registers until its scale is known, so the codes are read and written once.
+struct StateI8 {
+  const int8_t* in;
+  const float* s_in;
+  int8_t* out;
+  float* s_out;
+};
+
+template <int R>
+__global__ __launch_bounds__(kThreads) void k_state_update_i8(UpdParams p, StateI8 st) {
+  constexpr int N = 16 * R;
+  extern __shared__ float smem[];
+  float* xs = smem;
+  float* bs = xs + ((p.P + 3) & ~3);
+  float* cs = bs + N;
+  const int64_t bh = blockIdx.x;  // b * nh + h
+  const int64_t h = bh % p.nh;
+  stage_inputs(p, bh, xs, bs, cs);
+
+  const float dt = p.delta[bh];
+  const float dA = (float)exp((double)(dt * p.A[h]));
+  const float Dh = p.Dskip ? p.Dskip[h] : 0.0f;
+  const int sub = threadIdx.x % R, n0 = 16 * sub;
+  for (int64_t base = 0; base < p.P; base += kThreads / R) {
+    const int64_t row = base + threadIdx.x / R;
+    const bool on = row < p.P;
+    const int64_t at = bh * p.P + row;
+    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+    float s = 0.0f, x = 0.0f;
+    if (on) {
+      raw = *reinterpret_cast<const uint4*>(st.in + at * N + n0);
+      s = st.s_in[at];
+      x = xs[row];
+    }
+    const float keep = scale_ok(s) ? dA * s : 0.0f;
+    const float dtx = dt * x;
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    float v[16];
+    float yp = 0.0f, amax = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float q = (float)(int8_t)(w[k / 4] >> (8 * (k % 4)));
+      v[k] = fmaf(keep, q, dtx * bs[n0 + k]);
+      yp = fmaf(cs[n0 + k], v[k], yp);
+      amax = fmaxf(amax, finite_abs(v[k]));
+    }
+#pragma unroll
+    for (int off = R / 2; off > 0; off >>= 1) {
+      yp += __shfl_xor(yp, off, 64);
+      amax = fmaxf(amax, __shfl_xor(amax, off, 64));
+    }
+    const float sn = row_scale(amax);
+    uint32_t o[4];
+    quant_row<false, 16>(v, sn, o);
+    if (on) {
+      *reinterpret_cast<uint4*>(st.out + at * N + n0) = make_uint4(o[0], o[1], o[2], o[3]);
+      if (sub == 0) {
+        st.s_out[at] = sn;
+        store_y(p, bh, h, row, fmaf(Dh, x, yp));
       }
     }
   }
@@ -172,11 +249,9 @@ qssm_status launch_r(const UpdParams& p, int f16, hipStream_t st) {
   return launch_status("state_update");
 }
 
-}  // namespace
-
-extern "C" qssm_status qssm_state_update(const qssm_update_args* a, hipStream_t stream) {
-  clear_error();
-  if (!a) return fail(QSSM_ERR_INVALID_ARG, "args is null");
+// Checks shared by the state types: before (shapes and types) and after (pointers and sizes) the
+// checks of the state's own type.
+qssm_status check_shape(const qssm_update_args* a) {
   const int64_t B = a->batch, nh = a->nheads, P = a->headdim, N = a->dstate;
   if (B < 0 || nh < 1 || P < 1 || N < 1) return fail(QSSM_ERR_INVALID_ARG, "bad shape");
   if (a->ngroups < 1 || nh % a->ngroups != 0)
@@ -184,8 +259,6 @@ extern "C" qssm_status qssm_state_update(const qssm_update_args* a, hipStream_t 
   if (a->bc_group_size < 1 || N % a->bc_group_size != 0)
     return fail(QSSM_ERR_INVALID_ARG, "bc_group_size must divide dstate");
   if (a->x_groups < 1 || a->x_groups > 256) return fail(QSSM_ERR_INVALID_ARG, "x_groups not in 1..256");
-  if (a->state_dtype != QSSM_F32 && a->state_dtype != QSSM_F16)
-    return fail(QSSM_ERR_INVALID_ARG, "state_dtype must be QSSM_F32 or QSSM_F16");
   if (a->y_dtype != QSSM_F32 && a->y_dtype != QSSM_I8)
     return fail(QSSM_ERR_INVALID_ARG, "y_dtype must be QSSM_F32 or QSSM_I8");
   if (a->y_dtype == QSSM_I8) {
@@ -194,23 +267,52 @@ extern "C" qssm_status qssm_state_update(const qssm_update_args* a, hipStream_t 
     if (!a->y_group_of || !a->y_scales)
       return fail(QSSM_ERR_INVALID_ARG, "QSSM_I8 output needs y_group_of and y_scales");
   }
-  const int64_t R = N / 4;
-  if (N % 4 != 0 || !(R == 1 || R == 2 || R == 4 || R == 8 || R == 16 || R == 32 || R == 64))
-    return fail(QSSM_ERR_UNSUPPORTED, "dstate must be 4 * 2^k with 4 <= dstate <= 256");
-  if (a->state_dtype == QSSM_F16 && N < 8)
-    return fail(QSSM_ERR_UNSUPPORTED, "an fp16 state needs dstate >= 8");
-  if ((((P + 3) & ~3) + 2 * N) * 4 > 64 * 1024) return fail(QSSM_ERR_UNSUPPORTED, "headdim too large");
-  if (B == 0) return QSSM_OK;
+  return QSSM_OK;
+}
+
+qssm_status check_rest(const qssm_update_args* a) {
+  const int64_t B = a->batch, nh = a->nheads;
   if (!a->x || !a->x_group_of || !a->x_scales || !a->B || !a->C || !a->B_scales || !a->C_scales ||
       !a->delta || !a->A || !a->state || !a->y)
     return fail(QSSM_ERR_INVALID_ARG, "null required pointer");
   if ((uintptr_t)a->state % 16 != 0) return fail(QSSM_ERR_INVALID_ARG, "state must be 16-byte aligned");
   if (B * nh > 0x7fffffffLL) return fail(QSSM_ERR_INVALID_ARG, "batch * nheads too large");
-  UpdParams p{B, nh, P, N, a->ngroups, (int32_t)(nh / a->ngroups), a->bc_group_size, a->x_groups, a->x,
+  return QSSM_OK;
+}
+
+qssm_status check_headdim(const qssm_update_args* a) {
+  const int64_t P = a->headdim, N = a->dstate;
+  if ((((P + 3) & ~3) + 2 * N) * 4 > 64 * 1024) return fail(QSSM_ERR_UNSUPPORTED, "headdim too large");
+  return QSSM_OK;
+}
+
+UpdParams params_of(const qssm_update_args* a) {
+  const int64_t B = a->batch, nh = a->nheads, P = a->headdim, N = a->dstate;
+  return UpdParams{B, nh, P, N, a->ngroups, (int32_t)(nh / a->ngroups), a->bc_group_size, a->x_groups, a->x,
               a->x_group_of, a->x_scales, a->B, a->C, a->B_scales, a->C_scales, a->delta, a->A,
               a->Dskip, a->state, a->y, a->xq_out, a->Bq_out, a->Cq_out,
               a->y_dtype == QSSM_I8, a->y_dtype == QSSM_I8 ? a->y_groups : 1, a->y_group_of,
               a->y_scales, a->y_bias};
+}
+
+}  // namespace
+
+extern "C" qssm_status qssm_state_update(const qssm_update_args* a, hipStream_t stream) {
+  clear_error();
+  if (!a) return fail(QSSM_ERR_INVALID_ARG, "args is null");
+  if (a->state_dtype != QSSM_F32 && a->state_dtype != QSSM_F16)
+    return fail(QSSM_ERR_INVALID_ARG, "state_dtype must be QSSM_F32 or QSSM_F16");
+  if (qssm_status st = check_shape(a)) return st;
+  const int64_t N = a->dstate;
+  const int64_t R = N / 4;
+  if (N % 4 != 0 || !(R == 1 || R == 2 || R == 4 || R == 8 || R == 16 || R == 32 || R == 64))
+    return fail(QSSM_ERR_UNSUPPORTED, "dstate must be 4 * 2^k with 4 <= dstate <= 256");
+  if (a->state_dtype == QSSM_F16 && N < 8)
+    return fail(QSSM_ERR_UNSUPPORTED, "an fp16 state needs dstate >= 8");
+  if (qssm_status st = check_headdim(a)) return st;
+  if (a->batch == 0) return QSSM_OK;
+  if (qssm_status st = check_rest(a)) return st;
+  const UpdParams p = params_of(a);
   const int f16 = a->state_dtype == QSSM_F16;
   switch (R) {
     case 1: return launch_r<1>(p, f16, stream);
@@ -221,4 +323,37 @@ extern "C" qssm_status qssm_state_update(const qssm_update_args* a, hipStream_t 
     case 32: return launch_r<32>(p, f16, stream);
     default: return launch_r<64>(p, f16, stream);
   }
+}
+
+extern "C" qssm_status qssm_state_update_i8(const qssm_update_args* a, const int8_t* state_in,
+                                            const float* scales_in, float* state_scales,
+                                            hipStream_t stream) {
+  clear_error();
+  if (!a) return fail(QSSM_ERR_INVALID_ARG, "args is null");
+  if (a->state_dtype != QSSM_I8) return fail(QSSM_ERR_INVALID_ARG, "state_dtype must be QSSM_I8");
+  if (qssm_status st = check_shape(a)) return st;
+  const int64_t R = a->dstate / 16;
+  if (a->dstate % 16 != 0 || !(R == 1 || R == 2 || R == 4 || R == 8 || R == 16))
+    return fail(QSSM_ERR_UNSUPPORTED, "an int8 state needs dstate = 16 * 2^k with 16 <= dstate <= 256");
+  if (qssm_status st = check_headdim(a)) return st;
+  if ((state_in == nullptr) != (scales_in == nullptr))
+    return fail(QSSM_ERR_INVALID_ARG, "state_in and scales_in go together");
+  if (a->batch == 0) return QSSM_OK;
+  if (!state_scales) return fail(QSSM_ERR_INVALID_ARG, "null required pointer");
+  if (qssm_status st = check_rest(a)) return st;
+  if ((uintptr_t)state_in % 16 != 0)
+    return fail(QSSM_ERR_INVALID_ARG, "state_in must be 16-byte aligned");
+  const UpdParams p = params_of(a);
+  int8_t* out = reinterpret_cast<int8_t*>(a->state);
+  const StateI8 st{state_in ? state_in : out, scales_in ? scales_in : state_scales, out, state_scales};
+  const size_t smem = (size_t)(((p.P + 3) & ~3) + 2 * p.N) * sizeof(float);
+  const unsigned grid = (unsigned)(p.B * p.nh);
+  switch (R) {
+    case 1: k_state_update_i8<1><<<grid, kThreads, smem, stream>>>(p, st); break;
+    case 2: k_state_update_i8<2><<<grid, kThreads, smem, stream>>>(p, st); break;
+    case 4: k_state_update_i8<4><<<grid, kThreads, smem, stream>>>(p, st); break;
+    case 8: k_state_update_i8<8><<<grid, kThreads, smem, stream>>>(p, st); break;
+    default: k_state_update_i8<16><<<grid, kThreads, smem, stream>>>(p, st); break;
+  }
+  return launch_status("state_update_i8");
 }
