@@ -502,8 +502,8 @@ qssm_status qssm_rmsnorm_i8(const qssm_rmsnorm_args* a, hipStream_t stream);
  * A scale that is not valid gives its row or column y = bias. The integer sum is exact (K <= 131071,
  * else QSSM_ERR_UNSUPPORTED), is rounded once to fp32, and one fused multiply-add scales it and
  * adds the bias; an fp16 y is rounded once more. K == 0 gives y = bias. Any M, N >= 0, any
- * alignment of a and w; rows of K bytes with strides and addresses that are multiples of 16 take
- * the fast forms.
+ * alignment of a and w (addresses and strides that are multiples of 4 bytes take the fast forms);
+ * a_stride and w_stride at most 2^22.
  */
 typedef struct qssm_gemm_w8a8_args {
   int64_t M, N, K;

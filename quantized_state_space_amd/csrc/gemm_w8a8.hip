@@ -4,8 +4,16 @@
 // recurrence).
 //     y[m, n] = bias[n] + fl32(sa[m] sw[n]) * sum_k a[m, k] w[n, k]
 // Both operands have k contiguous, which is the operand order of v_mfma_i32_32x32x32_i8: lane l of a
-// wave holds row (or column) l % 32 and the 16 consecutive k at 16 (l / 32).
+// wave holds row (or column) l % 32 and the 16 consecutive k at 16 (l / 32). The weights go in as the
+// first operand, so a lane ends with one token and groups of 4 consecutive output channels.
+//
+// Two forms: tiles shared by a workgroup's waves with K in common steps (many tokens: bound by the
+// matrix cores and the power they draw), and small tiles with K split over the waves (few tokens,
+// few tiles: bound by the bytes of the weights and by latency). choose() picks by estimated time.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
 
 #include "common.hpp"
 
@@ -33,10 +41,12 @@ struct GemmParams {
 __device__ __forceinline__ float valid_or_zero(float s) { return scale_ok(s) ? s : 0.0f; }
 
 // y[m, n] from the integer sum: one rounding of the sum to fp32 (sums above 2^24), one of the product
-// of the scales, one of the fused multiply-add, one more to fp16.
-__device__ __forceinline__ void put(const GemmParams& p, int64_t m, int64_t n, int acc, float sa,
-                                    float sw, float bn) {
-  const float v = fmaf(sa * sw, (float)acc, bn);
+// of the scales, one of the fused multiply-add (and one more to an fp16 y).
+__device__ __forceinline__ float scaled(float sa, float sw, int acc, float bias) {
+  return fmaf(sa * sw, (float)acc, bias);
+}
+
+__device__ __forceinline__ void put(const GemmParams& p, int64_t m, int64_t n, float v) {
   if (p.yf16) reinterpret_cast<__half*>(p.y)[m * p.ys + n] = __float2half_rn(v);
   else reinterpret_cast<float*>(p.y)[m * p.ys + n] = v;
 }
@@ -57,7 +67,381 @@ __device__ __forceinline__ uint4 load16(const int8_t* row, int64_t k, int64_t K)
   return v;
 }
 
-// Any shape and alignment: 128 x 128 tiles of y, K in steps of 64 through LDS (rows padded to 80
+typedef __attribute__((address_space(3))) void* lds_ptr;
+constexpr int kBufferWord3 = 0x00020000;  // buffer resource word 3 for raw 32-bit access (gfx9)
+
+// 16 bytes per lane from byte voff + soff of the buffer straight to LDS, at dst (wave-uniform) + 16 lane
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, int8_t* dst, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)dst, 16, voff, soff, 0, 0);
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const int8_t* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p), (short)0, 0x7fffffff, kBufferWord3);
+}
+
+// Keeps the compiler's LDS accesses on their side (the direct loads are not its accesses).
+__device__ __forceinline__ void fence() { asm volatile("" ::: "memory"); }
+
+// Waits until at most N vector memory operations are outstanding, and for every LDS read.
+// (vmcnt in bits 3:0 and 15:14, expcnt 6:4 not waited for, lgkmcnt 11:8)
+template <int N>
+__device__ __forceinline__ void wait_vm_lds() {
+  static_assert(N <= 63, "vmcnt has 6 bits");
+  fence();
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x70);
+  fence();
+}
+
+// LDS rows of BK bytes; the 16-byte chunk c of row r is in slot c ^ swizzle(r), which spreads the rows
+// that a 16-byte read serves together over all 64 banks (measured: no conflicts; 4 of 8 cycles of
+// every read without it).
+template <int BK>
+__device__ __forceinline__ int swizzle(int row) {
+  return BK == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
+}
+
+// ------------------------------------------------------------------------------------------------
+// Tiles of (32 WM TM) x (32 WN TN) shared by WM x WN waves. K runs in steps of 64 bytes through NS LDS
+// stages that direct loads fill NS - 1 steps ahead; one barrier per step, placed where every wave has
+// the step's last fragments in registers, so that the products of half a step hide it. Fragments are
+// read half a step ahead and the reads and loads are issued between the products.
+// The partial step of a K that is no multiple of 64 is the first and goes through registers, with
+// zeros past K. Rows past M or N read the last row and are not stored.
+// Tile order: the tiles are cut into 8 contiguous ranges, one per XCD (workgroups are dealt to the
+// XCDs in turn), in groups of 4 row tiles, so the workgroups that run together on an XCD share rows
+// and columns in its L2 (16384 x 18560 x 4096: groups of 4 / 8 / 16 take 1151 / 1161 / 1195 us).
+// Output: each wave scales its sums and turns 32 rows at a time through LDS into whole-row stores
+// (stores straight from the registers took 23 us a tile, a third of the whole at K = 4096).
+template <int WM, int WN, int TM, int TN, int NS>
+struct Tile {
+  static constexpr int kWaves = WM * WN, kBM = WM * TM * 32, kBN = WN * TN * 32;
+  static constexpr int kNA = kBM / 16 / kWaves, kNB = kBN / 16 / kWaves;  // direct loads of a wave (16 rows each)
+  static constexpr int kStage = (kBM + kBN) * 64;
+};
+
+__device__ __forceinline__ void to_type(float v, __half& o) { o = __float2half_rn(v); }
+__device__ __forceinline__ void to_type(float v, float& o) { o = v; }
+
+// The wave's TM x TN tiles: lane l holds row l % 32 and, in register 4 j + i, column
+// 8 j + 4 (l / 32) + i.
+template <int TM, int TN, typename T>
+__device__ __forceinline__ void epilogue(const GemmParams& p, int8_t* sm, const float* s_sw, const float* s_bias,
+                                         const v16i (&acc)[TM][TN], const float (&sa)[TM], int64_t mw, int64_t nw,
+                                         int wave, int lane) {
+  constexpr int kCols = TN * 32, kRowB = kCols * (int)sizeof(T) + 16, kPer = 16 / (int)sizeof(T);
+  constexpr int kLanes = kCols / kPer;  // lanes per row of 16-byte stores
+  int8_t* buf = sm + wave * 32 * kRowB;
+  const int kh = lane >> 5;
+  T* y = reinterpret_cast<T*>(p.y);
+  const bool vec = nw + kCols <= p.N && ((uintptr_t)p.y | (uintptr_t)(p.ys * (int64_t)sizeof(T))) % 16 == 0;
+#pragma unroll
+  for (int mt = 0; mt < TM; ++mt) {
+#pragma unroll
+    for (int nt = 0; nt < TN; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = nt * 32 + 8 * j + 4 * kh;
+        const float4 sw = *reinterpret_cast<const float4*>(s_sw + c), bn = *reinterpret_cast<const float4*>(s_bias + c);
+        const v16i& d = acc[mt][nt];
+        T o[4];
+        to_type(scaled(sa[mt], sw.x, d[4 * j], bn.x), o[0]);
+        to_type(scaled(sa[mt], sw.y, d[4 * j + 1], bn.y), o[1]);
+        to_type(scaled(sa[mt], sw.z, d[4 * j + 2], bn.z), o[2]);
+        to_type(scaled(sa[mt], sw.w, d[4 * j + 3], bn.w), o[3]);
+        __builtin_memcpy(__builtin_assume_aligned(buf + (lane & 31) * kRowB + c * sizeof(T), 8), o, 4 * sizeof(T));
+      }
+    wait_vm_lds<63>();  // the wave's own buffer: its LDS operations run in order
+    const int64_t mb = mw + mt * 32;
+    if (vec) {
+#pragma unroll
+      for (int r = 0; r < 32; r += 64 / kLanes) {
+        const int row = r + lane / kLanes;
+        const uint4 v = *reinterpret_cast<const uint4*>(buf + row * kRowB + (lane % kLanes) * 16);
+        if (mb + row < p.M) *reinterpret_cast<uint4*>(y + (mb + row) * p.ys + nw + (lane % kLanes) * kPer) = v;
+      }
+    } else {
+      for (int c = lane; c < kCols; c += 64)
+        if (nw + c < p.N)
+          for (int row = 0; row < 32; ++row)
+            if (mb + row < p.M) y[(mb + row) * p.ys + nw + c] = *reinterpret_cast<const T*>(buf + row * kRowB + c * sizeof(T));
+    }
+    wait_vm_lds<63>();
+  }
+}
+
+template <int WM, int WN, int TM, int TN, int NS>
+__global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
+  using G = Tile<WM, WN, TM, TN, NS>;
+  constexpr int kLd = G::kNA + G::kNB;
+  static_assert(WM * WN * 32 * (TN * 32 * 4 + 16) <= NS * G::kStage, "the output buffers fit the stages");
+  // one array: with several the compiler waits for all direct loads before every LDS read
+  __shared__ __align__(1024) int8_t sm[NS * G::kStage + 8 * G::kBN];
+  float* s_sw = reinterpret_cast<float*>(sm + NS * G::kStage);
+  float* s_bias = s_sw + G::kBN;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = uniform(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN, kh = lane >> 5;
+  const int64_t nm = (p.M + G::kBM - 1) / G::kBM, nn = (p.N + G::kBN - 1) / G::kBN, T = nm * nn;
+  const int64_t id = (int64_t)(blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8;
+  if (id >= T) return;  // grid padding (the whole workgroup)
+  constexpr int64_t kGM = 4;
+  const int64_t grp = id / (kGM * nn), fm = grp * kGM;
+  const int64_t gsz = min(nm - fm, kGM), within = id - grp * kGM * nn;
+  const int64_t m0 = (fm + within % gsz) * G::kBM, n0 = (within / gsz) * G::kBN;
+
+  for (int i = tid; i < G::kBN; i += G::kWaves * 64) {
+    const int64_t n = min(n0 + i, p.N - 1);
+    s_sw[i] = valid_or_zero(p.w_scales[n]);
+    s_bias[i] = p.bias ? p.bias[n] : 0.0f;
+  }
+  float sa[TM];
+#pragma unroll
+  for (int mt = 0; mt < TM; ++mt) {
+    const int64_t m = min(m0 + (wm * TM + mt) * 32 + (lane & 31), p.M - 1);
+    sa[mt] = valid_or_zero(p.a_scales[p.per_row ? m : 0]);
+  }
+  // direct load i of this wave: 16 rows, lane l at row l / 4, slot l % 4 (32-bit offsets: host)
+  const int8_t* abase = p.a + m0 * p.as;
+  const int8_t* wbase = p.w + n0 * p.ws;
+  const int lrow = lane >> 2, chunk = (lane & 3) ^ swizzle<64>(lrow);
+  int aoff[G::kNA], woff[G::kNB];
+#pragma unroll
+  for (int i = 0; i < G::kNA; ++i)
+    aoff[i] = (int)(min((int64_t)((wave * G::kNA + i) * 16 + lrow), p.M - 1 - m0) * p.as) + chunk * 16;
+#pragma unroll
+  for (int i = 0; i < G::kNB; ++i)
+    woff[i] = (int)(min((int64_t)((wave * G::kNB + i) * 16 + lrow), p.N - 1 - n0) * p.ws) + chunk * 16;
+  const __amdgpu_buffer_rsrc_t ra = rsrc_of(abase), rw = rsrc_of(wbase);
+  const int full = (int)(p.K / 64), tail = (int)(p.K % 64) != 0;  // host: full >= 1
+  const int nsteps = full + tail;
+  int8_t* dst_a = sm + wave * G::kNA * 1024;
+  int8_t* dst_w = sm + G::kBM * 64 + wave * G::kNB * 1024;
+
+  // step s into stage st; past the last step the last one again, so that the waits stay exact
+  auto issue = [&](int s, int st) {
+    const int koff = (min(s, nsteps - 1) - tail) * 64;
+#pragma unroll
+    for (int i = 0; i < G::kNA; ++i) load_lds(ra, dst_a + st * G::kStage + i * 1024, aoff[i], koff);
+#pragma unroll
+    for (int i = 0; i < G::kNB; ++i) load_lds(rw, dst_w + st * G::kStage + i * 1024, woff[i], koff);
+  };
+
+  v16i acc[TM][TN];
+#pragma unroll
+  for (int mt = 0; mt < TM; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < TN; ++nt) acc[mt][nt] = v16i{};
+  v4i fa[2][TM], fb[2][TN];
+  const int slot0 = (kh ^ swizzle<64>(lane & 31)) * 16;
+  const int arow = (wm * TM * 32 + (lane & 31)) * 64, brow = (G::kBM + wn * TN * 32 + (lane & 31)) * 64;
+  auto frags = [&](int st, int ks) {
+    const int8_t* base = sm + st * G::kStage + (slot0 ^ (ks * 32));
+#pragma unroll
+    for (int mt = 0; mt < TM; ++mt) fa[ks][mt] = *reinterpret_cast<const v4i*>(base + arow + mt * 2048);
+#pragma unroll
+    for (int nt = 0; nt < TN; ++nt) fb[ks][nt] = *reinterpret_cast<const v4i*>(base + brow + nt * 2048);
+  };
+
+  if (tail) {
+#pragma unroll
+    for (int i = 0; i < G::kNA; ++i)
+      *reinterpret_cast<uint4*>(dst_a + i * 1024 + lane * 16) = load16(abase + aoff[i] - chunk * 16, full * 64 + chunk * 16, p.K);
+#pragma unroll
+    for (int i = 0; i < G::kNB; ++i)
+      *reinterpret_cast<uint4*>(dst_w + i * 1024 + lane * 16) = load16(wbase + woff[i] - chunk * 16, full * 64 + chunk * 16, p.K);
+  } else {
+    issue(0, 0);
+  }
+#pragma unroll
+  for (int d = 1; d < NS; ++d) issue(d, d);
+  wait_vm_lds<(NS - 1) * kLd>();
+  __builtin_amdgcn_s_barrier();
+  fence();
+  frags(0, 0);
+  int st = 0;
+  constexpr int kMf = TM * TN, kDs = TM + TN;
+  for (int s = 0; s < nsteps; ++s) {
+    const int nx = st + 1 == NS ? 0 : st + 1;
+    auto products = [&](int ks) {
+#pragma unroll
+      for (int mt = 0; mt < TM; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < TN; ++nt)
+          acc[mt][nt] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks][nt], fa[ks][mt], acc[mt][nt], 0, 0, 0);
+      // issue order: a product, two fragment reads, ... (second half: then a product, a load, ...)
+#pragma unroll
+      for (int i = 0; i < kDs / 2; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      }
+      if (ks == 1) {
+#pragma unroll
+        for (int i = 0; i < kLd; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x10, 1, 0);
+        }
+      }
+      __builtin_amdgcn_sched_group_barrier(0x8, kMf, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    frags(st, 1);
+    products(0);
+    // every wave has the last fragments of stage st in registers, and step s + 1 has landed
+    wait_vm_lds<(NS - 2) * kLd>();
+    __builtin_amdgcn_s_barrier();
+    fence();
+    frags(nx, 0);
+    issue(s + NS, st);
+    products(1);
+    st = nx;
+  }
+  wait_vm_lds<0>();  // no direct load outlives the stages it writes
+  __syncthreads();   // every wave is done with them: they become the waves' output buffers
+  const int64_t mw = m0 + wm * TM * 32, nw = n0 + wn * TN * 32;
+  if (p.yf16) epilogue<TM, TN, __half>(p, sm, s_sw + wn * TN * 32, s_bias + wn * TN * 32, acc, sa, mw, nw, wave, lane);
+  else epilogue<TM, TN, float>(p, sm, s_sw + wn * TN * 32, s_bias + wn * TN * 32, acc, sa, mw, nw, wave, lane);
+}
+
+// ------------------------------------------------------------------------------------------------
+// Tiles of (32 TM) x (32 TN) with K split over the W waves of a workgroup: wave k takes the units
+// k, k + W, ... of BK bytes, each through two LDS stages of its own that it fills and reads alone, so
+// no barrier is needed until the waves' integer sums are joined (exactly, in any order) in LDS.
+// ROWS: token rows that are loaded (a multiple of 1024 / BK; tokens past M up to ROWS read the last
+// row, those past ROWS are whatever the LDS held: their sums are not stored).
+template <int TM, int TN, int BK, int W, int ROWS>
+struct Split {
+  static constexpr int kBM = TM * 32, kBN = TN * 32, kRpl = 1024 / BK;  // rows per load instruction
+  static constexpr int kNA = ROWS / kRpl, kNB = kBN / kRpl, kStages = 2;
+  static constexpr int kStage = (kBM + kBN) * BK, kRow = kBN + 4;
+  static constexpr int kMain = kStages * W * kStage, kEnd = W * kBM * kRow * 4;
+  static constexpr int kLds = kMain > kEnd ? kMain : kEnd;
+};
+
+template <int TM, int TN, int BK, int W, int ROWS, int PER>
+__global__ __launch_bounds__(W * 64, PER) void k_gemm_w8a8_split(GemmParams p) {
+  using G = Split<TM, TN, BK, W, ROWS>;
+  constexpr int BM = G::kBM, BN = G::kBN, kSlots = BK / 16, kLd = G::kNA + G::kNB;
+  __shared__ __align__(1024) int8_t sm[G::kLds];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), kh = lane >> 5;
+  const int64_t nm = (p.M + BM - 1) / BM, nn = (p.N + BN - 1) / BN;
+  const int64_t id = (int64_t)(blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8;
+  if (id >= nm * nn) return;  // grid padding (the whole workgroup)
+  const int64_t m0 = id % nm * BM, n0 = id / nm * BN;
+  const int8_t* abase = p.a + m0 * p.as;
+  const int8_t* wbase = p.w + n0 * p.ws;
+  const int lrow = lane / kSlots;
+  // load i: rows i kRpl ..., lane l at row l / kSlots, slot l % kSlots; byte offset of its chunk
+  int aoff[G::kNA], woff[G::kNB], achk[G::kNA], wchk[G::kNB];
+#pragma unroll
+  for (int i = 0; i < G::kNA; ++i) {
+    const int row = i * G::kRpl + lrow;
+    achk[i] = ((lane % kSlots) ^ swizzle<BK>(row)) * 16;
+    aoff[i] = (int)(min((int64_t)row, p.M - 1 - m0) * p.as);
+  }
+#pragma unroll
+  for (int i = 0; i < G::kNB; ++i) {
+    const int row = i * G::kRpl + lrow;
+    wchk[i] = ((lane % kSlots) ^ swizzle<BK>(row)) * 16;
+    woff[i] = (int)(min((int64_t)row, p.N - 1 - n0) * p.ws);
+  }
+  int8_t* mine = sm + wave * G::kStages * G::kStage;
+  const int full = (int)(p.K / BK);
+
+  v16i acc[TM][TN];
+#pragma unroll
+  for (int mt = 0; mt < TM; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < TN; ++nt) acc[mt][nt] = v16i{};
+  auto products = [&](int st) {
+    const int8_t* base = mine + st * G::kStage;
+    v4i fa[BK / 32][TM], fb[BK / 32][TN];
+#pragma unroll
+    for (int ks = 0; ks < BK / 32; ++ks) {
+      const int slot = ((2 * ks + kh) ^ swizzle<BK>(lane & 31)) * 16;
+#pragma unroll
+      for (int mt = 0; mt < TM; ++mt) fa[ks][mt] = *reinterpret_cast<const v4i*>(base + (mt * 32 + (lane & 31)) * BK + slot);
+#pragma unroll
+      for (int nt = 0; nt < TN; ++nt) fb[ks][nt] = *reinterpret_cast<const v4i*>(base + (BM + nt * 32 + (lane & 31)) * BK + slot);
+    }
+#pragma unroll
+    for (int ks = 0; ks < BK / 32; ++ks)
+#pragma unroll
+      for (int mt = 0; mt < TM; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < TN; ++nt)
+          acc[mt][nt] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks][nt], fa[ks][mt], acc[mt][nt], 0, 0, 0);
+  };
+  // a unit through registers, codes at or past K as 0
+  auto to_lds = [&](const uint4 (&va)[G::kNA], const uint4 (&vw)[G::kNB]) {
+#pragma unroll
+    for (int i = 0; i < G::kNA; ++i) *reinterpret_cast<uint4*>(mine + i * 1024 + lane * 16) = va[i];
+#pragma unroll
+    for (int i = 0; i < G::kNB; ++i) *reinterpret_cast<uint4*>(mine + BM * BK + i * 1024 + lane * 16) = vw[i];
+    wait_vm_lds<63>();
+  };
+
+  const __amdgpu_buffer_rsrc_t ra = rsrc_of(abase), rw = rsrc_of(wbase);
+  // past the last unit the last one again, so that the waits stay exact
+  auto issue = [&](int u, int st) {
+    const int koff = min(u, full - 1) * BK;
+#pragma unroll
+    for (int i = 0; i < G::kNA; ++i) load_lds(ra, mine + st * G::kStage + i * 1024, aoff[i] + achk[i], koff);
+#pragma unroll
+    for (int i = 0; i < G::kNB; ++i) load_lds(rw, mine + st * G::kStage + BM * BK + i * 1024, woff[i] + wchk[i], koff);
+  };
+  if (wave < full) {
+    issue(wave, 0);
+    issue(wave + W, 1);
+    int st = 0;
+    for (int u = wave; u < full; u += W) {
+      wait_vm_lds<kLd>();
+      products(st);
+      wait_vm_lds<63>();  // the stage's fragments are in registers
+      issue(u + 2 * W, st);
+      st ^= 1;
+    }
+    wait_vm_lds<0>();
+  }
+  // the last K % BK codes
+  if (p.K % BK != 0 && wave == full % W) {
+    uint4 va[G::kNA], vw[G::kNB];
+#pragma unroll
+    for (int i = 0; i < G::kNA; ++i) va[i] = load16(abase + aoff[i], full * BK + achk[i], p.K);
+#pragma unroll
+    for (int i = 0; i < G::kNB; ++i) vw[i] = load16(wbase + woff[i], full * BK + wchk[i], p.K);
+    to_lds(va, vw);
+    products(0);
+  }
+
+  __syncthreads();
+  int* red = reinterpret_cast<int*>(sm);  // [wave][row][column]
+#pragma unroll
+  for (int mt = 0; mt < TM; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < TN; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<v4i*>(red + (wave * BM + mt * 32 + (lane & 31)) * G::kRow + nt * 32 + 8 * j + 4 * kh) =
+            v4i{acc[mt][nt][4 * j], acc[mt][nt][4 * j + 1], acc[mt][nt][4 * j + 2], acc[mt][nt][4 * j + 3]};
+  __syncthreads();
+  for (int i = threadIdx.x; i < BM * BN / 4; i += W * 64) {
+    const int row = i / (BN / 4), col = i % (BN / 4) * 4;
+    const int64_t m = m0 + row;
+    if (m >= p.M) continue;
+    v4i v = *reinterpret_cast<const v4i*>(red + row * G::kRow + col);
+#pragma unroll
+    for (int q = 1; q < W; ++q) v += *reinterpret_cast<const v4i*>(red + (q * BM + row) * G::kRow + col);
+    const float sa = valid_or_zero(p.a_scales[p.per_row ? m : 0]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t n = n0 + col + k;
+      if (n < p.N) put(p, m, n, scaled(sa, valid_or_zero(p.w_scales[n]), v[k], p.bias ? p.bias[n] : 0.0f));
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Rows or strides that are no multiple of 4 bytes, or K < 64: 128 x 128 tiles of y, K in steps of 64 through LDS (rows padded to 80
 // bytes: no bank conflicts), four waves with 64 x 64 each; the next step's global loads are in
 // registers during the current step's products. Rows past M or N load a valid row and are not
 // stored.
@@ -141,10 +525,50 @@ __global__ __launch_bounds__(256) void k_gemm_w8a8(GemmParams p) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int64_t m = m0 + wm * 64 + mt * 32 + 8 * (r / 4) + 4 * kh + (r % 4);
-        if (m < p.M) put(p, m, n, acc[mt][nt][r], valid_or_zero(p.a_scales[p.per_row ? m : 0]), sw, bn);
+        if (m < p.M) put(p, m, n, scaled(valid_or_zero(p.a_scales[p.per_row ? m : 0]), sw, acc[mt][nt][r], bn));
       }
   }
 }
+
+// ------------------------------------------------------------------------------------------------
+// The form for a shape. Each has its time per 64 codes of K: `alone` with few tiles on the GPU (the
+// latency of a step) and `busy` per tile and CU with all CUs at work (fitted to 1 .. 16384 tokens,
+// N = 1024 .. 18560, K = 768 .. 8192; us), and the workgroups that fit a CU. The estimate, the steps
+// times the rounds of tiles or the bytes at 4.5 TB/s, whichever is more, named the fastest form at
+// every one of 15 measured shapes, e.g. (us; tile 256x256 / 256x128 / 128x128 / 128x64 / split 64x64 /
+// 32x32): 256 x 4096 x 8192: 70 / 49 / 32 / 26 / 20 / 25; 1000 x 1536 x 768: 14 / 9.0 / 7.1 / 5.9 /
+// 10 / 13; 1024 x 4096 x 4096: 40 / 29 / 22 / 29 / 39 / 62; 4096 x 4096 x 4096: 63 / 75 / 85 / 114 /
+// 176 / 291; 64 x 4096 x 8192: split 64x64 22, 32x32 9.4.
+enum Form { TILE256, TILE256X128, TILE128, TILE128X64, SPLIT64, SPLIT32, FORMS };
+struct Cost {
+  int bm, bn, per_cu;
+  double alone, busy;
+};
+constexpr Cost kCost[FORMS] = {{256, 256, 1, 0.55, 0.94},  {256, 128, 2, 0.386, 0.59}, {128, 128, 2, 0.216, 0.335},
+                               {128, 64, 4, 0.165, 0.215}, {64, 64, 2, 0.125, 0.165},  {32, 32, 2, 0.042, 0.056}};
+
+Form choose(const GemmParams& p) {
+  constexpr double kCus = 256.0;
+  const double steps = (double)cdiv(p.K, 64);
+  const double bytes = ((double)p.M + (double)p.N) * (double)p.K + (p.yf16 ? 2.0 : 4.0) * (double)p.M * (double)p.N;
+  Form best = TILE256;
+  double least = 0.0;
+  for (int f = 0; f < FORMS; ++f) {
+    const Cost& c = kCost[f];
+    const double tiles = (double)cdiv(p.M, c.bm) * (double)cdiv(p.N, c.bn), slots = kCus * c.per_cu;
+    const double rounds = std::floor(tiles / slots), rest = tiles - rounds * slots;
+    double t = rounds * c.per_cu * c.busy;
+    if (rest > 0.0) t += std::max(c.alone, c.busy * std::ceil(rest / kCus));
+    t = std::max(steps * t, bytes / 4.5e6);
+    if (f == 0 || t < least) {
+      least = t;
+      best = (Form)f;
+    }
+  }
+  return best;
+}
+
+unsigned grid_of(const GemmParams& p, int bm, int bn) { return (unsigned)(cdiv(cdiv(p.M, bm) * cdiv(p.N, bn), 8) * 8); }
 
 }  // namespace
 
@@ -166,10 +590,30 @@ extern "C" qssm_status qssm_gemm_w8a8(const qssm_gemm_w8a8_args* a, hipStream_t 
     return fail(QSSM_ERR_INVALID_ARG, "null required pointer");
   if (((uintptr_t)a->y) % (a->y_dtype == QSSM_F16 ? 2 : 4) != 0)
     return fail(QSSM_ERR_INVALID_ARG, "y is not aligned to its type");
-  const int64_t gx = cdiv(N, kBN), gy = cdiv(M, kBM);
-  if (gy > 65535) return fail(QSSM_ERR_UNSUPPORTED, "M above 65535 * 128");
+  // 32-bit offsets inside a tile
+  if (std::max(a->a_stride, a->w_stride) > (1 << 22))
+    return fail(QSSM_ERR_UNSUPPORTED, "a_stride or w_stride above 2^22");
+  // every form's grid: the smallest tiles are 32 x 32
+  if (cdiv(M, 32) * cdiv(N, 32) > 0x7ffffff0) return fail(QSSM_ERR_UNSUPPORTED, "M * N too large");
   const GemmParams p{M, N, K, a->a_per_row != 0, a->y_dtype == QSSM_F16, a->a, a->a_stride, a->a_scales,
                      a->w, a->w_stride, a->w_scales, a->bias, a->y, a->y_stride};
-  k_gemm_w8a8<<<dim3((unsigned)gx, (unsigned)gy), 256, 0, stream>>>(p);
+  // direct loads take addresses that are multiples of 4 bytes
+  const bool direct = ((uintptr_t)a->a | (uintptr_t)a->w | (uintptr_t)a->a_stride | (uintptr_t)a->w_stride) % 4 == 0;
+  if (!direct || K < 64) {
+    if (cdiv(M, kBM) > 65535) return fail(QSSM_ERR_UNSUPPORTED, "M above 65535 * 128 with unaligned rows");
+    k_gemm_w8a8<<<dim3((unsigned)cdiv(N, kBN), (unsigned)cdiv(M, kBM)), 256, 0, stream>>>(p);
+    return launch_status("gemm_w8a8");
+  }
+  switch (choose(p)) {
+    case TILE256: k_gemm_w8a8_tile<2, 4, 4, 2, 4><<<grid_of(p, 256, 256), 512, 0, stream>>>(p); break;
+    case TILE256X128: k_gemm_w8a8_tile<4, 2, 2, 2, 3><<<grid_of(p, 256, 128), 512, 0, stream>>>(p); break;
+    case TILE128: k_gemm_w8a8_tile<2, 2, 2, 2, 4><<<grid_of(p, 128, 128), 256, 0, stream>>>(p); break;
+    case TILE128X64: k_gemm_w8a8_tile<2, 2, 2, 1, 4><<<grid_of(p, 128, 64), 256, 0, stream>>>(p); break;
+    case SPLIT64: k_gemm_w8a8_split<2, 2, 64, 4, 64, 2><<<grid_of(p, 64, 64), 256, 0, stream>>>(p); break;
+    default:
+      // up to 16 tokens load only 16 of a tile's 32 rows (8 tokens x 18560 x 4096: 18.9 us, 19.9 with all)
+      if (M <= 16) k_gemm_w8a8_split<1, 1, 128, 4, 16, 2><<<grid_of(p, 32, 32), 256, 0, stream>>>(p);
+      else k_gemm_w8a8_split<1, 1, 128, 4, 32, 2><<<grid_of(p, 32, 32), 256, 0, stream>>>(p);
+  }
   return launch_status("gemm_w8a8");
 }
