@@ -146,7 +146,7 @@ __device__ __forceinline__ float finite_abs(float v) {
 }
 
 // Codes of N values with one scale, packed little-endian: clamp(RNE(v / s), -128, 127), NaN 0, every
-// code 0 for an invalid scale (the rule above). With r = fl32(1/s), adding 1.5 * 2^23 in the fused
+// code 0 for an invalid scale (the rule above). With r ~ 1/s, adding 1.5 * 2^23 in the fused
 // multiply-add leaves c = RNE(v r) in the low bits of m. c is the nearest code when the remainder
 // e = v - c s is inside (-s/2, s/2): the fma rounds it once, rounding is monotone and s/2 is a
 // float, so |e| < s/2 after rounding implies it before. That fails only within ~2^-16 of a
@@ -156,10 +156,11 @@ __device__ __forceinline__ float finite_abs(float v) {
 template <bool IN_RANGE, int N>
 __device__ __forceinline__ void quant_row(const float (&v)[N], float s, uint32_t (&w)[N / 4]) {
   constexpr float kMagic = 12582912.0f;
-  const float r = recip_or_zero(s);
+  const bool ok = scale_ok(s);
+  const float r = __builtin_amdgcn_rcpf(s);  // 1 ulp: the remainder decides, not r
   const float half = 0.5f * s, hi = 127.0f * s, lo = -128.0f * s;
   uint32_t m[N];
-  bool bad = r == 0.0f;
+  bool bad = !ok;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float x = IN_RANGE ? v[i] : __builtin_amdgcn_fmed3f(v[i], lo, hi);
@@ -171,7 +172,7 @@ __device__ __forceinline__ void quant_row(const float (&v)[N], float s, uint32_t
   }
   if (bad) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) m[i] = (uint32_t)(int)quant8_r(v[i], s, r);
+    for (int i = 0; i < N; ++i) m[i] = (uint32_t)(int)quant8_r(v[i], s, recip_or_zero(s));
   }
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
@@ -180,6 +181,14 @@ __device__ __forceinline__ void quant_row(const float (&v)[N], float s, uint32_t
     const uint32_t hi2 = __builtin_amdgcn_perm(m[4 * i + 3], m[4 * i + 2], 0x0c0c0400u);
     w[i] = lo2 | (hi2 << 16);
   }
+}
+
+// x of the lane that differs in one bit of its number, for a reduction over 2, 4, 8 or 16 neighbouring
+// lanes in that order (the mirrored rows hold equal values by then). STEP: that bit's value.
+template <int STEP>
+__device__ __forceinline__ float dpp_partner(float x) {
+  constexpr int kCtrl = STEP == 1 ? 0xB1 : STEP == 2 ? 0x4E : STEP == 4 ? 0x141 : 0x140;
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), kCtrl, 0xF, 0xF, true));
 }
 
 // Wave-uniform value in an SGPR (so loads indexed by it can go through the scalar cache).

@@ -52,11 +52,18 @@ __device__ __forceinline__ void put(const GemmParams& p, int64_t m, int64_t n, f
 }
 
 // 16 consecutive codes of a row from k on, at any alignment (the hardware takes unaligned 16-byte
-// loads); codes at or past K read as 0 without touching memory.
+// loads); codes at or past K read as 0 without touching memory. A row's last, partial chunk is the
+// end of its last 16 codes (byte by byte, a load and a wait each, it took half of the 19 us of
+// 777 x 1001 x 1500); only rows shorter than 16 are read by bytes.
 __device__ __forceinline__ uint4 load16(const int8_t* row, int64_t k, int64_t K) {
   uint4 v = make_uint4(0u, 0u, 0u, 0u);
   if (k + 16 <= K) {
     __builtin_memcpy(&v, row + k, 16);
+  } else if (k < K && K >= 16) {
+    unsigned __int128 t;
+    __builtin_memcpy(&t, row + K - 16, 16);
+    t >>= 8 * (int)(k + 16 - K);
+    __builtin_memcpy(&v, &t, 16);
   } else if (k < K) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -160,10 +167,15 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, int8_t* sm, const 
         if (mb + row < p.M) *reinterpret_cast<uint4*>(y + (mb + row) * p.ys + nw + (lane % kLanes) * kPer) = v;
       }
     } else {
-      for (int c = lane; c < kCols; c += 64)
-        if (nw + c < p.N)
-          for (int row = 0; row < 32; ++row)
-            if (mb + row < p.M) y[(mb + row) * p.ys + nw + c] = *reinterpret_cast<const T*>(buf + row * kRowB + c * sizeof(T));
+      // 64 / kCols rows at a time, one element per lane
+      constexpr int kStep = 64 / kCols;
+      const int c = lane % kCols;
+#pragma unroll 8
+      for (int r = 0; r < 32; r += kStep) {
+        const int row = r + lane / kCols;
+        const T v = *reinterpret_cast<const T*>(buf + row * kRowB + c * sizeof(T));
+        if (mb + row < p.M && nw + c < p.N) y[(mb + row) * p.ys + nw + c] = v;
+      }
     }
     wait_vm_lds<63>();
   }
@@ -242,6 +254,9 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
     for (int nt = 0; nt < TN; ++nt) fb[ks][nt] = *reinterpret_cast<const v4i*>(base + brow + nt * 2048);
   };
 
+  if (!tail) issue(0, 0);
+#pragma unroll
+  for (int d = 1; d < NS; ++d) issue(d, d);
   if (tail) {
 #pragma unroll
     for (int i = 0; i < G::kNA; ++i)
@@ -249,11 +264,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
 #pragma unroll
     for (int i = 0; i < G::kNB; ++i)
       *reinterpret_cast<uint4*>(dst_w + i * 1024 + lane * 16) = load16(wbase + woff[i] - chunk * 16, full * 64 + chunk * 16, p.K);
-  } else {
-    issue(0, 0);
   }
-#pragma unroll
-  for (int d = 1; d < NS; ++d) issue(d, d);
   wait_vm_lds<(NS - 1) * kLd>();
   __builtin_amdgcn_s_barrier();
   fence();

@@ -26,8 +26,8 @@ constexpr int64_t kMaxDimNarrow = 8192;  // VEC = 1: 8 channels per thread
 constexpr int64_t kMaxDimWide = 32768;   // VEC = 8: 4 vectors of 8 per thread
 
 struct NormParams {
-  int64_t D, Dg;
-  int32_t Gn, dynamic;
+  int32_t D, Dg, Gn, dynamic;
+  uint32_t inv_dg;  // ceil(2^32 / Dg): c / Dg is the high word of c * inv_dg for c, Dg <= 32768
   const void* x;
   const void* res;
   void* res_out;
@@ -101,32 +101,39 @@ __device__ __forceinline__ void round_store(void* base, int64_t i, float (&v)[VE
   }
 }
 
-// silu(z) = z / (1 + e^-z), in fp64 and rounded once to fp32. e^x with x = -z clamped to +-700 (beyond
-// that silu is z or rounds to -0 either way): x = n ln2 + f, |f| <= ln2 / 2, the Taylor polynomial of
-// degree 10 in f (error f^11 / 11! < 2.2e-13). One Newton step takes the reciprocal to ~2^-47.
+// silu(z) = z / (1 + e^-z), in fp64 and rounded once to fp32. With y = -z / ln2 = n + f, |f| <= 1/2:
+// e^-z = 2^n p(f), p the polynomial of degree 9 with the least largest relative error against 2^f
+// (1.4e-14; coefficients by Remez exchange in 50 digits). Adding 1.5 * 2^52 rounds y to n, which is
+// then in the low word. Beyond |n| = 200 (an fp32 gate: |z| = 126) silu rounds to z or to -0 either
+// way, so n (z) is clamped there. An infinite gate gives a NaN, which like an infinity leaves its
+// group's codes at 0. One Newton step takes the reciprocal to ~2^-46.
+template <bool F16>
 __device__ __forceinline__ float silu_f64(float z) {
-  const double x = fmin(fmax(-(double)z, -700.0), 700.0);
-  const double n = rint(x * 1.4426950408889634);  // 1 / ln2
-  double f = fma(-n, 0x1.62e42fefa2000p-1, x);  // the leading 40 bits of ln2: n times it is exact
-  f = fma(-n, 0x1.9ef35793c7673p-41, f);          // the rest of ln2
-  double e = 1.0 / 3628800.0;
-  e = fma(e, f, 1.0 / 362880.0);
-  e = fma(e, f, 1.0 / 40320.0);
-  e = fma(e, f, 1.0 / 5040.0);
-  e = fma(e, f, 1.0 / 720.0);
-  e = fma(e, f, 1.0 / 120.0);
-  e = fma(e, f, 1.0 / 24.0);
-  e = fma(e, f, 1.0 / 6.0);
-  e = fma(e, f, 0.5);
-  e = fma(e, f, 1.0);
-  e = fma(e, f, 1.0);
-  const double d = 1.0 + ldexp(e, (int)n);
+  constexpr double kLog2e = 1.4426950408889634, kMagic = 6755399441055744.0;
+  const double x = -(double)(F16 ? z : __builtin_amdgcn_fmed3f(z, -126.0f, 126.0f));
+  const double t = fma(x, kLog2e, kMagic);
+  const double f = fma(x, kLog2e, -(t - kMagic));
+  double e = 0x1.b3f42432927dap-24;
+  e = fma(e, f, 0x1.63edf11a7df52p-20);
+  e = fma(e, f, 0x1.ffce245dbe28dp-17);
+  e = fma(e, f, 0x1.43088fca865dap-13);
+  e = fma(e, f, 0x1.5d87fd9013458p-10);
+  e = fma(e, f, 0x1.3b2ab72a10a42p-7);
+  e = fma(e, f, 0x1.c6b08d70d1ff5p-5);
+  e = fma(e, f, 0x1.ebfbdff81570dp-3);
+  e = fma(e, f, 0x1.62e42fefa3752p-1);
+  e = fma(e, f, 0x1.0000000000039p+0);
+  int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, t);
+  if (F16) n = min(max(n, -200), 200);
+  const uint64_t bits = __builtin_bit_cast(uint64_t, e);
+  const uint32_t hi = (uint32_t)(bits >> 32) + ((uint32_t)n << 20);
+  const double d = 1.0 + __builtin_bit_cast(double, ((uint64_t)hi << 32) | (uint32_t)bits);
   double r = __builtin_amdgcn_rcp(d);
   r = fma(fma(-d, r, 1.0), r, r);
-  return (float)((double)z * r);
+  return (float)((F16 ? -x : (double)z) * r);
 }
 
-__device__ __forceinline__ float group_r(double sum, int64_t Dg, float eps) {
+__device__ __forceinline__ float group_r(double sum, int Dg, float eps) {
   return (float)(1.0 / sqrt(sum / (double)Dg + (double)eps));
 }
 
@@ -143,7 +150,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
   double sum = 0.0;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    const int64_t c = (int64_t)(v * T + tid) * VEC;
+    const int c = (v * T + tid) * VEC;
 #pragma unroll
     for (int k = 0; k < VEC; ++k) t[v][k] = 0.0f;
     if (c < p.D) {
@@ -162,7 +169,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
         float z[VEC];
         load_vec<VEC, GATE == 1>(p.gate, row * p.gs + c, z);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) t[v][k] *= silu_f64(z[k]);
+        for (int k = 0; k < VEC; ++k) t[v][k] *= silu_f64<GATE == 1>(z[k]);
       }
     }
     double part = 0.0;
@@ -183,10 +190,10 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
   if (p.Gn > 1) {
     // wave k sums the groups k, k + nw, ... and leaves r in the group's first slot
     __syncthreads();
-    const int64_t per = p.Dg / VEC;
-    for (int64_t g = wave; g < p.Gn; g += nw) {
+    const int per = p.Dg / VEC;
+    for (int g = wave; g < p.Gn; g += nw) {
       double a = 0.0;
-      for (int64_t i = g * per + lane; i < (g + 1) * per; i += 64) {
+      for (int i = g * per + lane; i < (g + 1) * per; i += 64) {
         if constexpr (VEC == 1) {
           const double u = (double)reinterpret_cast<const float*>(smem)[i];
           a = fma(u, u, a);
@@ -217,11 +224,11 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
   float amax = 0.0f;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    const int64_t c = (int64_t)(v * T + tid) * VEC;
+    const int c = (v * T + tid) * VEC;
     if (c < p.D) {
       float r = r1;
       if (p.Gn > 1) {
-        const int64_t g = c / p.Dg, per = p.Dg / VEC;
+        const int g = p.Dg > 1 ? (int)__umulhi((uint32_t)c, p.inv_dg) : c, per = p.Dg / VEC;
         r = reinterpret_cast<const float*>(smem)[VEC == 1 ? g * per : 2 * g * per];
       }
       float w[VEC];
@@ -230,13 +237,20 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
       for (int k = 0; k < VEC; ++k) {
         t[v][k] *= r;
         if (p.w) t[v][k] *= w[k];
-        amax = fmaxf(amax, finite_abs(t[v][k]));
+        amax = fmaxf(amax, fabsf(t[v][k]));  // a NaN does not count
       }
     }
   }
 
   float s;
   if (p.dynamic) {
+    if (amax > 3.402823466e38f) {  // infinities do not count: the largest of the others
+      amax = 0.0f;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) amax = fmaxf(amax, finite_abs(t[v][k]));
+    }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
     if (lane == 0) red_max[wave] = amax;
@@ -250,7 +264,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
 
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    const int64_t c = (int64_t)(v * T + tid) * VEC;
+    const int c = (v * T + tid) * VEC;
     if (c < p.D) {
       int8_t* o = p.q + row * p.qs + c;
       if constexpr (VEC == 8) {
@@ -278,7 +292,11 @@ void launch_vpt(const NormParams& p, int res, int gate, unsigned rows, int threa
 template <int VEC, bool XF16>
 void launch_vec(const NormParams& p, int res, int gate, unsigned rows, hipStream_t st) {
   const int64_t nvec = p.D / VEC;
-  const int threads = (int)std::min<int64_t>(cdiv(nvec, 64) * 64, kMaxThreads);
+  // Few rows: as many threads as the row feeds (latency). Many: smaller workgroups, of which more run
+  // at once and cover each other's reductions (16384 x 8192 gated: 218 / 223 / 240 us with up to 256 /
+  // 512 / 1024 threads; 16384 x 4096 with a stream: 137 / 131 / 131; 1111 x 1543: 9.4 / 10.8 / 13.0)
+  const int cap = rows < 512 ? kMaxThreads : (gate || VEC == 1 ? 256 : 512);
+  const int threads = (int)std::min<int64_t>(cdiv(nvec, 64) * 64, std::max<int64_t>(cap, cdiv(cdiv(nvec, VEC == 8 ? 4 : 8), 64) * 64));
   const int64_t vpt = cdiv(nvec, threads);
   if (vpt == 1) launch_vpt<VEC, 1, XF16>(p, res, gate, rows, threads, st);
   else if (VEC == 8 && vpt == 2) launch_vpt<VEC, 2, XF16>(p, res, gate, rows, threads, st);
@@ -328,7 +346,8 @@ extern "C" qssm_status qssm_rmsnorm_i8(const qssm_rmsnorm_args* a, hipStream_t s
     return fail(QSSM_ERR_UNSUPPORTED, "dim above 8192 (32768 with aligned rows and groups)");
   if (M == 0) return QSSM_OK;
   if (!a->x || !a->scales || !a->q) return fail(QSSM_ERR_INVALID_ARG, "null required pointer");
-  NormParams p{D, Dg, a->norm_groups, a->compute_scales != 0, a->x, a->residual, a->residual_out,
+  NormParams p{(int32_t)D, (int32_t)Dg, a->norm_groups, a->compute_scales != 0,
+               Dg > 1 ? (uint32_t)((((uint64_t)1 << 32) + Dg - 1) / Dg) : 0u, a->x, a->residual, a->residual_out,
                a->gate, a->x_stride, a->residual_stride, a->residual_out_stride, a->gate_stride,
                a->q_stride, a->weight, a->eps, a->scales, a->q};
   const int res = !stream_on ? 0 : (a->residual_dtype == QSSM_F16 ? 1 : 2);

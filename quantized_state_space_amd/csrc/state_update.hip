@@ -18,6 +18,7 @@ using namespace qssm;
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxRows = 256;  // rows of an int8 state tile
 
 struct UpdParams {
   int64_t B, nh, P, N;
@@ -74,16 +75,15 @@ __device__ __forceinline__ void stage_inputs(const UpdParams& p, int64_t bh, flo
   __syncthreads();
 }
 
-// y of one row, fp32 or int8 codes. Persistent int8 output: fl32(y + correction term), the exact rule
+// y[i] of channel ch (= h * P + p), fp32 or int8 codes. Persistent int8 output: fl32(y + correction term), the exact rule
 // with the channel's static output scale.
-__device__ __forceinline__ void store_y(const UpdParams& p, int64_t bh, int64_t h, int64_t row, float yv) {
+__device__ __forceinline__ void store_y(const UpdParams& p, int64_t i, int64_t ch, float yv) {
   if (p.yi8) {
-    const int64_t ch = h * p.P + row;
     const float sy = p.y_scales[min((int)p.y_group_of[ch], p.Gy - 1)];
     const float yb = p.y_bias ? p.y_bias[ch] : 0.0f;
-    reinterpret_cast<int8_t*>(p.y)[bh * p.P + row] = quant8_r(yv + yb, sy, recip_or_zero(sy));
+    reinterpret_cast<int8_t*>(p.y)[i] = quant8_r(yv + yb, sy, recip_or_zero(sy));
   } else {
-    reinterpret_cast<float*>(p.y)[bh * p.P + row] = yv;
+    reinterpret_cast<float*>(p.y)[i] = yv;
   }
 }
 
@@ -166,75 +166,161 @@ __global__ __launch_bounds__(kThreads) void k_state_update(UpdParams p) {
 #pragma unroll
     for (int off = R / 2; off > 0; off >>= 1) yp += __shfl_xor(yp, off, 64);
     if (on && (lane % R) == 0) {
-      store_y(p, bh, h, row, fmaf(Dh, xs[row], yp));
+      store_y(p, bh * p.P + row, h * p.P + row, fmaf(Dh, xs[row], yp));
     }
   }
 }
 
-// int8 state: R = N / 16 lanes share one row, 16 codes (16 bytes) each, and the row's scale. The row's
-// new absmax and its readout are shuffle reductions over those lanes; the new state stays in
-// registers until its scale is known, so the codes are read and written once.
+// int8 state. A workgroup owns a tile of consecutive rows (h, p) of one (b, B/C group): it quantizes
+// the group's B and C once for all of them and leaves dA, delta x and D x of each row in LDS. R = N / 16
+// lanes share a row, 16 codes (16 bytes) each; a thread's 16 states n are the same in every row, so B and C stay
+// in its registers. The row's readout and new absmax are DPP reductions over those lanes, and the new
+// state waits in registers for its scale: the codes are read and written once. The loads of the first
+// rows are issued before the inputs are quantized, whose chain of dependent loads they cover, and
+// from then on one batch ahead.
 struct StateI8 {
   const int8_t* in;
   const float* s_in;
   int8_t* out;
   float* s_out;
+  int32_t tiles, rows;  // tiles of `rows` rows per (b, group)
 };
+
+constexpr float kMaxInRange = 0x1.fcp+106f;  // 127 * 2^100: the scale of a larger absmax is clamped
+
+template <int R>
+__device__ __forceinline__ float row_sum(float x) {
+  if constexpr (R >= 2) x += dpp_partner<1>(x);
+  if constexpr (R >= 4) x += dpp_partner<2>(x);
+  if constexpr (R >= 8) x += dpp_partner<4>(x);
+  if constexpr (R >= 16) x += dpp_partner<8>(x);
+  return x;
+}
+
+template <int R>
+__device__ __forceinline__ float row_max(float x) {
+  if constexpr (R >= 2) x = fmaxf(x, dpp_partner<1>(x));
+  if constexpr (R >= 4) x = fmaxf(x, dpp_partner<2>(x));
+  if constexpr (R >= 8) x = fmaxf(x, dpp_partner<4>(x));
+  if constexpr (R >= 16) x = fmaxf(x, dpp_partner<8>(x));
+  return x;
+}
 
 template <int R>
 __global__ __launch_bounds__(kThreads) void k_state_update_i8(UpdParams p, StateI8 st) {
-  constexpr int N = 16 * R;
-  extern __shared__ float smem[];
-  float* xs = smem;
-  float* bs = xs + ((p.P + 3) & ~3);
-  float* cs = bs + N;
-  const int64_t bh = blockIdx.x;  // b * nh + h
-  const int64_t h = bh % p.nh;
-  stage_inputs(p, bh, xs, bs, cs);
+  constexpr int N = 16 * R, kPass = kThreads / R, kBatch = 2;  // rows per pass, passes in flight
+  __shared__ __align__(16) float bs[N], cs[N];
+  __shared__ __align__(16) float4 rowc[kMaxRows];
+  const int tid = threadIdx.x;
+  const int64_t bg = blockIdx.x / st.tiles;  // b * Gbc + g
+  const int tile = (int)(blockIdx.x % st.tiles);
+  const int64_t b = bg / p.Gbc, g = bg % p.Gbc;
+  const int64_t grows = p.hpg * p.P;  // rows of the group
+  const int64_t r0 = (int64_t)tile * st.rows;
+  const int n_rows = (int)min((int64_t)st.rows, grows - r0);
+  const int64_t at0 = bg * grows + r0;  // first row in the state ([B, nh, P] = [B, Gbc, hpg P])
 
-  const float dt = p.delta[bh];
-  const float dA = (float)exp((double)(dt * p.A[h]));
-  const float Dh = p.Dskip ? p.Dskip[h] : 0.0f;
-  const int sub = threadIdx.x % R, n0 = 16 * sub;
-  for (int64_t base = 0; base < p.P; base += kThreads / R) {
-    const int64_t row = base + threadIdx.x / R;
-    const bool on = row < p.P;
-    const int64_t at = bh * p.P + row;
-    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    float s = 0.0f, x = 0.0f;
-    if (on) {
-      raw = *reinterpret_cast<const uint4*>(st.in + at * N + n0);
-      s = st.s_in[at];
-      x = xs[row];
-    }
-    const float keep = scale_ok(s) ? dA * s : 0.0f;
-    const float dtx = dt * x;
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    float v[16];
-    float yp = 0.0f, amax = 0.0f;
+  const int sub = tid % R, n0 = 16 * sub, lrow = tid / R;
+  uint4 raw[kBatch];
+  float s_in[kBatch];
+  auto load = [&](int base) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float q = (float)(int8_t)(w[k / 4] >> (8 * (k % 4)));
-      v[k] = fmaf(keep, q, dtx * bs[n0 + k]);
-      yp = fmaf(cs[n0 + k], v[k], yp);
-      amax = fmaxf(amax, finite_abs(v[k]));
+    for (int i = 0; i < kBatch; ++i) {
+      const int row = min(base + i * kPass + lrow, n_rows - 1);  // past the tile: its last row, not stored
+      raw[i] = *reinterpret_cast<const uint4*>(st.in + (at0 + row) * N + n0);
+      s_in[i] = st.s_in[at0 + row];
     }
+  };
+  load(0);
+
+  for (int k = tid; k < n_rows; k += kThreads) {
+    const int64_t ch = g * grows + r0 + k;  // h * P + p
+    const int64_t h = ch / p.P;
+    const float s = p.x_scales[min((int)p.x_group_of[ch], p.G - 1)];
+    const int8_t q = quant8(p.x[at0 + k], s);
+    if (p.xq_out) p.xq_out[at0 + k] = q;
+    const float x = scale_ok(s) ? (float)q * s : 0.0f;
+    const float dt = p.delta[b * p.nh + h];
+    rowc[k] = make_float4((float)exp((double)(dt * p.A[h])), dt * x, (p.Dskip ? p.Dskip[h] : 0.0f) * x, 0.0f);
+  }
+  const int ngs = N / p.gs;
+  for (int k = tid; k < 2 * N; k += kThreads) {
+    const int n = k % N;
+    const int64_t i = bg * N + n;
+    const float s = (k < N ? p.B_scales : p.C_scales)[g * ngs + n / p.gs];
+    const int8_t q = quant8((k < N ? p.Bm : p.Cm)[i], s);
+    int8_t* out = k < N ? p.Bq_out : p.Cq_out;
+    if (tile == 0 && out) out[i] = q;
+    (k < N ? bs : cs)[n] = scale_ok(s) ? (float)q * s : 0.0f;
+  }
+  __syncthreads();
+  float bv[16], cv[16];
 #pragma unroll
-    for (int off = R / 2; off > 0; off >>= 1) {
-      yp += __shfl_xor(yp, off, 64);
-      amax = fmaxf(amax, __shfl_xor(amax, off, 64));
+  for (int k = 0; k < 16; k += 4) {
+    const float4 b4 = *reinterpret_cast<const float4*>(bs + n0 + k), c4 = *reinterpret_cast<const float4*>(cs + n0 + k);
+    bv[k] = b4.x; bv[k + 1] = b4.y; bv[k + 2] = b4.z; bv[k + 3] = b4.w;
+    cv[k] = c4.x; cv[k + 1] = c4.y; cv[k + 2] = c4.z; cv[k + 3] = c4.w;
+  }
+
+  for (int base = 0; base < n_rows; base += kBatch * kPass) {
+    uint4 now[kBatch];
+    float s_now[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      now[i] = raw[i];
+      s_now[i] = s_in[i];
     }
-    const float sn = row_scale(amax);
-    uint32_t o[4];
-    quant_row<false, 16>(v, sn, o);
-    if (on) {
-      *reinterpret_cast<uint4*>(st.out + at * N + n0) = make_uint4(o[0], o[1], o[2], o[3]);
-      if (sub == 0) {
-        st.s_out[at] = sn;
-        store_y(p, bh, h, row, fmaf(Dh, x, yp));
+    // (in place: the rows loaded here are later ones, or the tile's last, whose value is not used)
+    if (base + kBatch * kPass < n_rows) load(base + kBatch * kPass);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int row = base + i * kPass + lrow;
+      const bool on = row < n_rows;
+      const float4 rc = rowc[on ? row : 0];
+      const float keep = scale_ok(s_now[i]) ? rc.x * s_now[i] : 0.0f;
+      const uint32_t w[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
+      float v[16];
+      float yp = 0.0f, amax = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float q = (float)(int8_t)(w[k / 4] >> (8 * (k % 4)));
+        v[k] = fmaf(keep, q, rc.y * bv[k]);
+        yp = fmaf(cv[k], v[k], yp);
+        amax = fmaxf(amax, fabsf(v[k]));
+      }
+      yp = row_sum<R>(yp);
+      amax = row_max<R>(amax);
+      uint32_t o[4];
+      float sn;
+      if (amax <= kMaxInRange && yp == yp) {
+        // every value is finite (a NaN or an infinity would show in yp or in amax)
+        sn = row_scale(amax);
+        quant_row<true, 16>(v, sn, o);
+      } else {
+        amax = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) amax = fmaxf(amax, finite_abs(v[k]));
+        sn = row_scale(row_max<R>(amax));
+        quant_row<false, 16>(v, sn, o);
+      }
+      if (on) {
+        *reinterpret_cast<uint4*>(st.out + (at0 + row) * N + n0) = make_uint4(o[0], o[1], o[2], o[3]);
+        if (sub == 0) {
+          st.s_out[at0 + row] = sn;
+          store_y(p, at0 + row, g * grows + r0 + row, rc.z + yp);
+        }
       }
     }
   }
+}
+
+template <int R>
+void launch_i8(const UpdParams& p, StateI8 st, hipStream_t stream) {
+  const int64_t grows = p.hpg * p.P;
+  // Large tiles share one quantization of B and C; small ones keep a small batch spread over the GPU.
+  st.rows = p.B * p.nh * p.P >= kMaxRows * 2048 ? kMaxRows : 64;
+  st.tiles = (int32_t)cdiv(grows, st.rows);
+  k_state_update_i8<R><<<(unsigned)(p.B * p.Gbc * st.tiles), kThreads, 0, stream>>>(p, st);
 }
 
 template <int R>
@@ -343,17 +429,17 @@ extern "C" qssm_status qssm_state_update_i8(const qssm_update_args* a, const int
   if (qssm_status st = check_rest(a)) return st;
   if ((uintptr_t)state_in % 16 != 0)
     return fail(QSSM_ERR_INVALID_ARG, "state_in must be 16-byte aligned");
+  if (a->batch * a->nheads > ((int64_t)1 << 36) / a->headdim)
+    return fail(QSSM_ERR_UNSUPPORTED, "batch * nheads * headdim above 2^36");  // grid of 64-row tiles
   const UpdParams p = params_of(a);
   int8_t* out = reinterpret_cast<int8_t*>(a->state);
-  const StateI8 st{state_in ? state_in : out, scales_in ? scales_in : state_scales, out, state_scales};
-  const size_t smem = (size_t)(((p.P + 3) & ~3) + 2 * p.N) * sizeof(float);
-  const unsigned grid = (unsigned)(p.B * p.nh);
+  const StateI8 st{state_in ? state_in : out, scales_in ? scales_in : state_scales, out, state_scales, 0, 0};
   switch (R) {
-    case 1: k_state_update_i8<1><<<grid, kThreads, smem, stream>>>(p, st); break;
-    case 2: k_state_update_i8<2><<<grid, kThreads, smem, stream>>>(p, st); break;
-    case 4: k_state_update_i8<4><<<grid, kThreads, smem, stream>>>(p, st); break;
-    case 8: k_state_update_i8<8><<<grid, kThreads, smem, stream>>>(p, st); break;
-    default: k_state_update_i8<16><<<grid, kThreads, smem, stream>>>(p, st); break;
+    case 1: launch_i8<1>(p, st, stream); break;
+    case 2: launch_i8<2>(p, st, stream); break;
+    case 4: launch_i8<4>(p, st, stream); break;
+    case 8: launch_i8<8>(p, st, stream); break;
+    default: launch_i8<16>(p, st, stream); break;
   }
   return launch_status("state_update_i8");
 }
