@@ -443,6 +443,8 @@ def update_args(x, x_group_of, x_scales, Bm, Cm, B_scales, C_scales, gs, delta, 
             if t is not None and (t.numel() != math.prod(shape) or
                                   (name == "state" and tuple(t.shape) != shape)):
                 raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        _device_of(x, x_group_of, x_scales, Bm, Cm, B_scales, C_scales, delta, A, state, y, Dskip,
+                   xq_out, Bq_out, Cq_out, y_group_of, y_scales, y_bias)
     keep = (x, x_group_of, x_scales, Bm, Cm, B_scales, C_scales, delta, A, state, y, Dskip, xq_out,
             Bq_out, Cq_out, y_group_of, y_scales, y_bias)
     ydt = {torch.float32: QSSM_F32, torch.int8: QSSM_I8}.get(y.dtype, -1)
@@ -473,36 +475,40 @@ def qssm_state_update(args, stream=None):
 # whatever the current one is; its current stream is the default.
 
 def _device_of(*tensors):
-    """The one GPU that holds every tensor given."""
+    """Index of the one GPU that holds every tensor given."""
     dev = None
     for t in tensors:
         if t is not None:
+            d = t.get_device()
             if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
+                dev = d
+            elif d != dev:
+                raise ValueError(f"tensors on devices {dev} and {d}: one GPU is needed")
     return dev
 
 
 def _call(name, dev, stream, *args, keep=()):
-    """Calls an entry point on device `dev`: on `stream`, or on that device's current stream. The
+    """Calls an entry point on GPU `dev` (an index): on `stream`, or on that GPU's current stream. The
     tensors in `keep` are marked as used by a stream that is not theirs by default."""
     torch = _t()
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        # the handle alone: a torch.cuda.Stream object costs more than the rest of this function
+        raw = torch._C._cuda_getCurrentRawStream(dev)
     else:
-        if stream.device != dev:
-            raise ValueError(f"stream of {stream.device} for tensors on {dev}")
+        if stream.device.index != dev:
+            raise ValueError(f"stream of {stream.device} for tensors on GPU {dev}")
+        raw = stream.cuda_stream
         if not torch.cuda.is_current_stream_capturing():
             for t in keep:
                 t.record_stream(stream)
     f = getattr(load(), name)
-    if torch.cuda.current_device() == dev.index:
-        status = f(*args, ctypes.c_void_p(stream.cuda_stream))
+    if torch.cuda.current_device() == dev:
+        status = f(*args, raw)
     else:
         with torch.cuda.device(dev):
-            status = f(*args, ctypes.c_void_p(stream.cuda_stream))
-    _check(name, status)
+            status = f(*args, raw)
+    if status != QSSM_OK:
+        _check(name, status)
 
 
 def _float_type(t, name):
@@ -577,16 +583,16 @@ def qssm_state_update_i8(args, state_scales, state_in=None, scales_in=None, stre
     state = args._state
     if state.dtype != torch.int8:
         raise TypeError("update_args was given a state that is not int8")
-    if state_scales.shape != state.shape[:-1] or (scales_in is not None and
-                                                  scales_in.shape != state.shape[:-1]):
+    rows = state.shape[:-1]
+    if state_scales.shape != rows or (scales_in is not None and scales_in.shape != rows):
         raise ValueError("the scales must be [B, nh, P]")
     if state_in is not None and state_in.shape != state.shape:
         raise ValueError("state_in must have the state's shape")
-    given = (state_scales, state_in, scales_in)
-    _call("qssm_state_update_i8", _device_of(state, *given), stream, ctypes.byref(args),
-          _ptr(state_in, torch.int8, "state_in", True), _ptr(scales_in, torch.float32, "scales_in", True),
-          _ptr(state_scales, torch.float32, "state_scales"),
-          keep=[t for t in given if t is not None] + args._keep)
+    keep = args._keep + [t for t in (state_scales, state_in, scales_in) if t is not None]
+    _call("qssm_state_update_i8", _device_of(state, state_scales, state_in, scales_in), stream,
+          ctypes.byref(args), _ptr(state_in, torch.int8, "state_in", True),
+          _ptr(scales_in, torch.float32, "scales_in", True),
+          _ptr(state_scales, torch.float32, "state_scales"), keep=keep)
 
 
 def rmsnorm_args(x, q, scales, weight=None, eps=1e-5, residual=None, residual_out=None, gate=None,

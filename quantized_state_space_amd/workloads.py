@@ -11,14 +11,16 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (QSSM_F16, QSSM_F32, QSSM_I16, QSSM_X_INT8, QSSM_X_SOFTEDGE, qssm_calib_block_absmax,
+from . import (QSSM_F16, QSSM_F32, QSSM_I8, QSSM_I16, QSSM_X_INT8, QSSM_X_SOFTEDGE, qssm_calib_block_absmax,
                qssm_calib_channel_absmax, qssm_calib_cluster_channels, qssm_calib_group_absmax,
                qssm_calib_s4d_state_scale, qssm_calib_scales, qssm_calib_softedge,
                qssm_softedge_track, qssm_softedge_track_workspace_size,
                qssm_quant_group_x, qssm_quant_state_group_BC, qssm_s4d_scan, qssm_scan_w8a8,
                qssm_scan_workspace_size, qssm_softedge_encode, qssm_ssd_chunk_int8,
                qssm_ssd_workspace_size, qssm_state_update, s4d_args, scan_args, ssd_args,
-               update_args, gemm_args, qssm_gemm_w4a8, qssm_quant_w4)
+               update_args, gemm_args, qssm_gemm_w4a8, qssm_quant_w4, qssm_quant_w8, rmsnorm_args,
+               qssm_rmsnorm_i8, gemm_w8a8_args, qssm_gemm_w8a8, qssm_state_quant, qssm_state_dequant,
+               qssm_state_update_i8)
 
 
 def _dev(a, device, dtype=None):
@@ -384,8 +386,9 @@ class SsdLayer:
 # Decode
 
 class DecodeLayer:
-    """Static scales from one calibration step; state [B, nh, P, N] fp32 or fp16, updated in place.
-    One step = one fused state-update call for a new token of every sequence."""
+    """Static scales from one calibration step; state [B, nh, P, N] fp32, fp16 or int8 (QSSM_I8: codes
+    with one scale a row in state_scales), updated in place. One step = one fused state-update call
+    for a new token of every sequence."""
 
     def __init__(self, params, device, gs=16, groups_per_block=8, state_dtype=QSSM_F32,
                  emit_codes=False, y_out=None):
@@ -406,8 +409,13 @@ class DecodeLayer:
         self.xs, self.bs, self.cs = _dev(xs, dev), _dev(bs, dev), _dev(cs, dev)
         self.A = _dev(params["A"], dev)
         self.D = _dev(params["D"], dev)
-        sdt = torch.float32 if state_dtype == QSSM_F32 else torch.float16
-        self.state = _dev(st0, dev, sdt)
+        self.state_scales = None
+        if state_dtype == QSSM_I8:
+            self.state = torch.empty((B, nh, P, N), dtype=torch.int8, device=dev)
+            self.state_scales = torch.empty((B, nh, P), dtype=torch.float32, device=dev)
+            self.store_state(_dev(st0, dev))
+        else:
+            self.state = _dev(st0, dev, torch.float32 if state_dtype == QSSM_F32 else torch.float16)
         yo = (None, None, None)
         if y_out is not None:
             yg, ys, yb = y_out
@@ -437,8 +445,25 @@ class DecodeLayer:
         for name, buf in (("x", self.x), ("B", self.Bm), ("C", self.Cm), ("delta", self.delta)):
             buf.copy_(torch.from_numpy(np.ascontiguousarray(step_inputs[name])))
 
+    def store_state(self, h):
+        """Writes h [B, nh, P, N] (a device tensor, e.g. a prefill's h_last) to the state."""
+        if self.state_scales is not None:
+            qssm_state_quant(h, self.state, self.state_scales)
+        else:
+            self.state.copy_(h)
+
+    def load_state(self, out):
+        """The state's values in out [B, nh, P, N] (e.g. the h0 of a following scan)."""
+        if self.state_scales is not None:
+            qssm_state_dequant(self.state, self.state_scales, out)
+        else:
+            out.copy_(self.state)
+
     def step(self):
-        qssm_state_update(self.args)
+        if self.state_scales is not None:
+            qssm_state_update_i8(self.args, self.state_scales)
+        else:
+            qssm_state_update(self.args)
         return self.y
 
 
@@ -483,3 +508,68 @@ class W4A8Linear:
         self.quantize()
         self.gemm()
         return self.y
+
+
+# ------------------------------------------------------------------------------------------------
+# W8A8 block around the recurrence
+
+class W8A8Linear:
+    """y = x W^T (+ bias) with int8 weights [N, K] quantized offline per output channel. One step reads
+    int8 codes a [M, K] with one scale a token (or one for all, as a_scales [1]) and writes y."""
+
+    def __init__(self, w, a, a_scales, y, bias=None):
+        """w: host fp32 [N, K]; a, a_scales, y: the device tensors a step reads and writes."""
+        dev = a.device
+        self.w_scales_host, self.w_host = qssm_quant_w8(w)
+        self.w, self.ws = _dev(self.w_host, dev), _dev(self.w_scales_host, dev)
+        self.bias = None if bias is None else _dev(np.asarray(bias, np.float32), dev)
+        self.y = y
+        self.args = gemm_w8a8_args(a, a_scales, self.w, self.ws, y, bias=self.bias)
+
+    def step(self):
+        qssm_gemm_w8a8(self.args)
+        return self.y
+
+
+class W8A8DecodeBlock:
+    """One token of every sequence through a W8A8 Mamba2-shaped block: the residual stream's addition
+    with the norm and its int8 output, the in-projection into the gate z, x, B and C, the state update
+    on an int8 state (by default), the gated norm over Gbc groups and the out-projection. delta
+    [B, nh] is an input, as in DecodeLayer.
+
+    params: decode parameters (state0, A, D and the calibration draws of DecodeLayer) and host fp32
+    norm_w [d], w_in [2 nh P + 2 Gbc N, d] (rows z, x, B, C), gate_w [nh P], w_out [d, nh P].
+    hidden: the block's input, and residual the stream [B, d] fp32 (updated in place)."""
+
+    def __init__(self, params, device, state_dtype=QSSM_I8, gs=16, eps=1e-5):
+        import torch
+        B, nh, P, N = params["state0"].shape
+        G = params["B_cal"].shape[1]
+        d, inner = params["w_in"].shape[1], nh * P
+        e = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=device)
+        self.core = DecodeLayer(params, device, gs=gs, state_dtype=state_dtype)
+        self.hidden, self.residual = e(B, d, dtype=torch.float16), e(B, d)
+        self.codes, self.scales = e(B, d, dtype=torch.int8), e(B)
+        self.norm_w, self.gate_w = _dev(params["norm_w"], device), _dev(params["gate_w"], device)
+        self.norm = rmsnorm_args(self.hidden, self.codes, self.scales, weight=self.norm_w, eps=eps,
+                                 residual=self.residual, residual_out=self.residual)
+        self.z = e(B, inner, dtype=torch.float16)
+        outs = (self.z, self.core.x.view(B, inner), self.core.Bm.view(B, G * N),
+                self.core.Cm.view(B, G * N))
+        rows = np.cumsum([0] + [o.shape[1] for o in outs])
+        self.proj_in = [W8A8Linear(params["w_in"][r0:r1], self.codes, self.scales, o)
+                        for r0, r1, o in zip(rows[:-1], rows[1:], outs)]
+        self.delta = self.core.delta
+        self.y_codes, self.y_scales = e(B, inner, dtype=torch.int8), e(B)
+        self.gated = rmsnorm_args(self.core.y.view(B, inner), self.y_codes, self.y_scales,
+                                  weight=self.gate_w, eps=eps, gate=self.z, norm_groups=G)
+        self.out = W8A8Linear(params["w_out"], self.y_codes, self.y_scales,
+                              e(B, d, dtype=torch.float16))
+
+    def step(self):
+        qssm_rmsnorm_i8(self.norm)
+        for p in self.proj_in:
+            p.step()
+        self.core.step()
+        qssm_rmsnorm_i8(self.gated)
+        return self.out.step()
