@@ -130,8 +130,9 @@ __device__ __forceinline__ void to_type(float v, __half& o) { o = __float2half_r
 __device__ __forceinline__ void to_type(float v, float& o) { o = v; }
 
 // The wave's TM x TN tiles: lane l holds row l % 32 and, in register 4 j + i, column
-// 8 j + 4 (l / 32) + i.
-template <int TM, int TN, typename T>
+// 8 j + 4 (l / 32) + i. STREAM (the forms for large y): stores that do not displace the operands from
+// L2 (16384 x 18560 x 4096: 1162 us, 1203 without).
+template <int TM, int TN, bool STREAM, typename T>
 __device__ __forceinline__ void epilogue(const GemmParams& p, int8_t* sm, const float* s_sw, const float* s_bias,
                                          const v16i (&acc)[TM][TN], const float (&sa)[TM], int64_t mw, int64_t nw,
                                          int wave, int lane) {
@@ -163,8 +164,12 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, int8_t* sm, const 
 #pragma unroll
       for (int r = 0; r < 32; r += 64 / kLanes) {
         const int row = r + lane / kLanes;
-        const uint4 v = *reinterpret_cast<const uint4*>(buf + row * kRowB + (lane % kLanes) * 16);
-        if (mb + row < p.M) *reinterpret_cast<uint4*>(y + (mb + row) * p.ys + nw + (lane % kLanes) * kPer) = v;
+        const v4i v = *reinterpret_cast<const v4i*>(buf + row * kRowB + (lane % kLanes) * 16);
+        v4i* dst = reinterpret_cast<v4i*>(y + (mb + row) * p.ys + nw + (lane % kLanes) * kPer);
+        if (mb + row < p.M) {
+          if (STREAM) __builtin_nontemporal_store(v, dst);
+          else *dst = v;
+        }
       }
     } else {
       // 64 / kCols rows at a time, one element per lane
@@ -309,8 +314,8 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
   wait_vm_lds<0>();  // no direct load outlives the stages it writes
   __syncthreads();   // every wave is done with them: they become the waves' output buffers
   const int64_t mw = m0 + wm * TM * 32, nw = n0 + wn * TN * 32;
-  if (p.yf16) epilogue<TM, TN, __half>(p, sm, s_sw + wn * TN * 32, s_bias + wn * TN * 32, acc, sa, mw, nw, wave, lane);
-  else epilogue<TM, TN, float>(p, sm, s_sw + wn * TN * 32, s_bias + wn * TN * 32, acc, sa, mw, nw, wave, lane);
+  if (p.yf16) epilogue<TM, TN, G::kBM == 256, __half>(p, sm, s_sw + wn * TN * 32, s_bias + wn * TN * 32, acc, sa, mw, nw, wave, lane);
+  else epilogue<TM, TN, G::kBM == 256, float>(p, sm, s_sw + wn * TN * 32, s_bias + wn * TN * 32, acc, sa, mw, nw, wave, lane);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -542,21 +547,23 @@ __global__ __launch_bounds__(256) void k_gemm_w8a8(GemmParams p) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// The form for a shape. Each has its time per 64 codes of K: `alone` with few tiles on the GPU (the
-// latency of a step) and `busy` per tile and CU with all CUs at work (fitted to 1 .. 16384 tokens,
-// N = 1024 .. 18560, K = 768 .. 8192; us), and the workgroups that fit a CU. The estimate, the steps
-// times the rounds of tiles or the bytes at 4.5 TB/s, whichever is more, named the fastest form at
-// every one of 15 measured shapes, e.g. (us; tile 256x256 / 256x128 / 128x128 / 128x64 / split 64x64 /
-// 32x32): 256 x 4096 x 8192: 70 / 49 / 32 / 26 / 20 / 25; 1000 x 1536 x 768: 14 / 9.0 / 7.1 / 5.9 /
-// 10 / 13; 1024 x 4096 x 4096: 40 / 29 / 22 / 29 / 39 / 62; 4096 x 4096 x 4096: 63 / 75 / 85 / 114 /
-// 176 / 291; 64 x 4096 x 8192: split 64x64 22, 32x32 9.4.
+// The form for a shape, by estimated time (us): a tile costs tile + step * (steps of 64 codes of K) of
+// its CU when all CUs are at work, at least tile_alone + step_alone * steps when they are not; the
+// whole at least the bytes at 4.2 TB/s. The constants are a fit (15 % rms) to 22 shapes of 1 .. 16384
+// tokens, N = 1024 .. 18560 and K = 128 .. 8192 in every form, and named the fastest form, or one within
+// 9 % of it, at all of them. Measured, e.g. (256x256 / 256x128 / 128x128 / 128x64 / split 64x64 / split 32x32):
+//   64 x 4096 x 8192      - / - / - / - / 22 / 9.4        256 x 4096 x 8192   70 / 49 / 32 / 26 / 20 / 25
+//   1000 x 1536 x 768     14 / 9.0 / 7.1 / 5.9 / 10 / 13  256 x 18560 x 4096  56 / 41 / 49 / 53 / 63 / 88
+//   1024 x 4096 x 4096    40 / 29 / 22 / 29 / 39 / 62     4096 x 4096 x 4096  63 / 75 / 85 / 114 / 176 / 291
+//   16384 x 1024 x 128    11.8 / 10.6 / 12.9 / 14.6 / 54 / 82
 enum Form { TILE256, TILE256X128, TILE128, TILE128X64, SPLIT64, SPLIT32, FORMS };
 struct Cost {
   int bm, bn, per_cu;
-  double alone, busy;
+  double tile, step, tile_alone, step_alone;
 };
-constexpr Cost kCost[FORMS] = {{256, 256, 1, 0.55, 0.94},  {256, 128, 2, 0.386, 0.59}, {128, 128, 2, 0.216, 0.335},
-                               {128, 64, 4, 0.165, 0.215}, {64, 64, 2, 0.125, 0.165},  {32, 32, 2, 0.042, 0.056}};
+constexpr Cost kCost[FORMS] = {{256, 256, 1, 10.2, 0.553, 0.0, 0.0},  {256, 128, 2, 3.94, 0.417, 6.77, 0.064},
+                               {128, 128, 2, 3.05, 0.281, 0.0, 0.0},  {128, 64, 4, 1.25, 0.201, 2.92, 0.188},
+                               {64, 64, 2, 2.79, 0.137, 5.01, 0.119}, {32, 32, 2, 1.20, 0.047, 5.18, 0.022}};
 
 Form choose(const GemmParams& p) {
   constexpr double kCus = 256.0;
@@ -567,10 +574,10 @@ Form choose(const GemmParams& p) {
   for (int f = 0; f < FORMS; ++f) {
     const Cost& c = kCost[f];
     const double tiles = (double)cdiv(p.M, c.bm) * (double)cdiv(p.N, c.bn), slots = kCus * c.per_cu;
-    const double rounds = std::floor(tiles / slots), rest = tiles - rounds * slots;
-    double t = rounds * c.per_cu * c.busy;
-    if (rest > 0.0) t += std::max(c.alone, c.busy * std::ceil(rest / kCus));
-    t = std::max(steps * t, bytes / 4.5e6);
+    const double rounds = std::floor(tiles / slots), rest = tiles - rounds * slots, busy = c.tile + c.step * steps;
+    double t = rounds * c.per_cu * busy;
+    if (rest > 0.0) t += std::max(c.tile_alone + c.step_alone * steps, busy * std::ceil(rest / kCus));
+    t = std::max(t, bytes / 4.2e6);
     if (f == 0 || t < least) {
       least = t;
       best = (Form)f;

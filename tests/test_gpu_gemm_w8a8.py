@@ -76,6 +76,27 @@ def test_against_oracle(dev, M, N, K):
     check(dev, *make(i, M, N, K, per_row=True, bias=i % 2 == 1), f16=i % 4 != 1)
 
 
+# Shapes that reach every form of the kernel with ragged edges in M, N and K: 256 x 256, 256 x 128, 128 x 128,
+# 128 x 64 tiles, K split over four waves in 64 x 64 and 32 x 32 tiles (the last with 16 or 32 token rows
+# loaded), each with K below, at and above its number of stages.
+EVERY_FORM = [(4100, 4100, 964), (4000, 4090, 4096), (2300, 4300, 132), (4097, 3000, 64), (260, 9000, 132), (1030, 4000, 2052),
+              (130, 6000, 100), (300, 4000, 700), (250, 4090, 4100), (256, 4096, 260), (70, 1000, 132), (16, 2000, 68), (9, 500, 2044),
+              (1000, 4000, 4100), (60, 1000, 4100)]
+
+
+@pytest.mark.parametrize("M,N,K", EVERY_FORM)
+def test_every_form(dev, M, N, K):
+    """Every element for short rows of y, 300 sampled token rows (first and last among them) otherwise."""
+    print(f"\n[gemm_w8a8 forms M={M} N={N} K={K}]", flush=True)
+    a, sa, w, sw, b = make(M + K, M, N, K)
+    f16 = K % 8 == 4
+    y = run(dev, a, sa, w, sw, b, f16)
+    rows = np.unique(np.concatenate([[0, M - 1, M // 2], np.random.default_rng(M).integers(0, M, 300)]))
+    yb = ow.gemm_w8a8(a[rows], sa[rows], w, sw)
+    want = yb + b.astype(np.float64)
+    assert np.all(np.abs(y[rows] - want) <= bound(want, yb, f16))
+
+
 @pytest.mark.parametrize("M,N,K,pads,offset", [
     (1, 200, 512, (16, 32, 3), 0), (40, 200, 512, (16, 16, 1), 0), (200, 300, 320, (16, 48, 5), 0),
     (40, 200, 513, (5, 1, 1), 0), (200, 300, 512, (0, 0, 0), 1), (3, 70, 256, (0, 0, 0), 8),
