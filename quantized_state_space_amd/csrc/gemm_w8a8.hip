@@ -175,14 +175,48 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, int8_t* sm, const 
       // 64 / kCols rows at a time, one element per lane
       constexpr int kStep = 64 / kCols;
       const int c = lane % kCols;
+      T* dst = y + (mb + lane / kCols) * p.ys + nw + c;
+      const T* src = reinterpret_cast<const T*>(buf + (lane / kCols) * kRowB) + c;
+      if (nw + c < p.N) {
+        if (mb + 32 <= p.M) {
 #pragma unroll 8
-      for (int r = 0; r < 32; r += kStep) {
-        const int row = r + lane / kCols;
-        const T v = *reinterpret_cast<const T*>(buf + row * kRowB + c * sizeof(T));
-        if (mb + row < p.M && nw + c < p.N) y[(mb + row) * p.ys + nw + c] = v;
+          for (int r = 0; r < 32; r += kStep) dst[r * p.ys] = src[r * (kRowB / (int)sizeof(T))];
+        } else {
+          for (int r = 0; r < 32; r += kStep)
+            if (mb + r + lane / kCols < p.M) dst[r * p.ys] = src[r * (kRowB / (int)sizeof(T))];
+        }
       }
     }
     wait_vm_lds<63>();
+  }
+}
+
+// First row and column of this workgroup's tile; false in the grid's padding (the whole workgroup).
+__device__ __forceinline__ bool tile_of(const GemmParams& p, int bm, int bn, int64_t& m0, int64_t& n0) {
+  const int64_t nm = (p.M + bm - 1) / bm, nn = (p.N + bn - 1) / bn;
+  const int64_t id = (int64_t)(blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8;
+  if (id >= nm * nn) return false;
+  constexpr int64_t kGM = 4;
+  const int64_t grp = id / (kGM * nn), fm = grp * kGM;
+  const int64_t gsz = min(nm - fm, kGM), within = id - grp * kGM * nn;
+  m0 = (fm + within % gsz) * bm;
+  n0 = (within / gsz) * bn;
+  return true;
+}
+
+// The tile's column scales and biases to LDS, and the scales of the wave's rows (from row mw).
+template <int TM>
+__device__ __forceinline__ void load_scales(const GemmParams& p, int bn, int64_t mw, int64_t n0, int lane, int tid,
+                                            int threads, float* s_sw, float* s_bias, float (&sa)[TM]) {
+  for (int i = tid; i < bn; i += threads) {
+    const int64_t n = min(n0 + i, p.N - 1);
+    s_sw[i] = valid_or_zero(p.w_scales[n]);
+    s_bias[i] = p.bias ? p.bias[n] : 0.0f;
+  }
+#pragma unroll
+  for (int mt = 0; mt < TM; ++mt) {
+    const int64_t m = min(mw + mt * 32 + (lane & 31), p.M - 1);
+    sa[mt] = valid_or_zero(p.a_scales[p.per_row ? m : 0]);
   }
 }
 
@@ -198,25 +232,10 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uniform(tid >> 6);
   const int wm = wave / WN, wn = wave % WN, kh = lane >> 5;
-  const int64_t nm = (p.M + G::kBM - 1) / G::kBM, nn = (p.N + G::kBN - 1) / G::kBN, T = nm * nn;
-  const int64_t id = (int64_t)(blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8;
-  if (id >= T) return;  // grid padding (the whole workgroup)
-  constexpr int64_t kGM = 4;
-  const int64_t grp = id / (kGM * nn), fm = grp * kGM;
-  const int64_t gsz = min(nm - fm, kGM), within = id - grp * kGM * nn;
-  const int64_t m0 = (fm + within % gsz) * G::kBM, n0 = (within / gsz) * G::kBN;
-
-  for (int i = tid; i < G::kBN; i += G::kWaves * 64) {
-    const int64_t n = min(n0 + i, p.N - 1);
-    s_sw[i] = valid_or_zero(p.w_scales[n]);
-    s_bias[i] = p.bias ? p.bias[n] : 0.0f;
-  }
+  int64_t m0, n0;
+  if (!tile_of(p, G::kBM, G::kBN, m0, n0)) return;
   float sa[TM];
-#pragma unroll
-  for (int mt = 0; mt < TM; ++mt) {
-    const int64_t m = min(m0 + (wm * TM + mt) * 32 + (lane & 31), p.M - 1);
-    sa[mt] = valid_or_zero(p.a_scales[p.per_row ? m : 0]);
-  }
+  load_scales<TM>(p, G::kBN, m0 + wm * TM * 32, n0, lane, tid, G::kWaves * 64, s_sw, s_bias, sa);
   // direct load i of this wave: 16 rows, lane l at row l / 4, slot l % 4 (32-bit offsets: host)
   const int8_t* abase = p.a + m0 * p.as;
   const int8_t* wbase = p.w + n0 * p.ws;
@@ -457,93 +476,143 @@ __global__ __launch_bounds__(W * 64, PER) void k_gemm_w8a8_split(GemmParams p) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Rows or strides that are no multiple of 4 bytes, or K < 64: 128 x 128 tiles of y, K in steps of 64 through LDS (rows padded to 80
-// bytes: no bank conflicts), four waves with 64 x 64 each; the next step's global loads are in
-// registers during the current step's products. Rows past M or N load a valid row and are not
-// stored.
-constexpr int kBM = 128, kBN = 128, kBK = 64, kRow = 80;
-
-struct GemmSmem {
-  int8_t a[2][kBM * kRow];
-  int8_t w[2][kBN * kRow];
+// Rows at any address and K of any length: the tiles of k_gemm_w8a8_tile with the operands through
+// registers. A chunk's 16 bytes are the 4 or 5 aligned words that hold them, shifted into place as they
+// go to LDS (loads of 16 unaligned bytes, one step ahead in 128 x 128 tiles, took 341 us at 4096 x 4095 x
+// 4097, this 151; 777 x 1001 x 1501: 45 and 13.5). The loads run two steps ahead of the products
+// (two register sets, named statically by unrolling the loop twice), the LDS stages one: step s + 2
+// goes into the stage that step s - 1 has left, which every wave has by the barrier of step s.
+struct Words {
+  uint4 w;
+  uint32_t w4;  // holds the last codes when there is a shift; without one the word is not read
 };
 
-__global__ __launch_bounds__(256) void k_gemm_w8a8(GemmParams p) {
-  __shared__ __align__(16) GemmSmem s;
+__device__ __forceinline__ Words load_words(const int8_t* at, uint32_t sh) {
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(at - sh);
+  return Words{make_uint4(q[0], q[1], q[2], q[3]), q[sh ? 4 : 3]};
+}
+
+__device__ __forceinline__ uint4 shifted(const Words& r, uint32_t sh) {
+  return make_uint4(__builtin_amdgcn_alignbyte(r.w.y, r.w.x, sh), __builtin_amdgcn_alignbyte(r.w.z, r.w.y, sh),
+                    __builtin_amdgcn_alignbyte(r.w.w, r.w.z, sh), __builtin_amdgcn_alignbyte(r.w4, r.w.w, sh));
+}
+
+template <int WM, int WN, int TM, int TN>
+__global__ __launch_bounds__(WM * WN * 64, 2) void k_gemm_w8a8_any(GemmParams p) {
+  constexpr int NS = 3;
+  using G = Tile<WM, WN, TM, TN, NS>;
+  static_assert(WM * WN * 32 * (TN * 32 * 4 + 16) <= NS * G::kStage, "the output buffers fit the stages");
+  __shared__ __align__(1024) int8_t sm[NS * G::kStage + 8 * G::kBN];
+  float* s_sw = reinterpret_cast<float*>(sm + NS * G::kStage);
+  float* s_bias = s_sw + G::kBN;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uniform(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1, kh = lane >> 5;
-  const int64_t m0 = (int64_t)blockIdx.y * kBM, n0 = (int64_t)blockIdx.x * kBN;
-  const int64_t nk = (p.K + kBK - 1) / kBK;
+  const int wm = wave / WN, wn = wave % WN, kh = lane >> 5;
+  int64_t m0, n0;
+  if (!tile_of(p, G::kBM, G::kBN, m0, n0)) return;
+  float sa[TM];
+  load_scales<TM>(p, G::kBN, m0 + wm * TM * 32, n0, lane, tid, G::kWaves * 64, s_sw, s_bias, sa);
 
-  v16i acc[2][2];
+  const int8_t* arow[G::kNA];
+  const int8_t* wrow[G::kNB];
+  const int lrow = lane >> 2, chunk = ((lane & 3) ^ swizzle<64>(lrow)) * 16;
 #pragma unroll
-  for (int mt = 0; mt < 2; ++mt)
+  for (int i = 0; i < G::kNA; ++i) arow[i] = p.a + min(m0 + (wave * G::kNA + i) * 16 + lrow, p.M - 1) * p.as;
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) acc[mt][nt] = v16i{};
+  for (int i = 0; i < G::kNB; ++i) wrow[i] = p.w + min(n0 + (wave * G::kNB + i) * 16 + lrow, p.N - 1) * p.ws;
+  const int full = (int)(p.K / 64), tail = (int)(p.K % 64) != 0;
+  const int nsteps = full + tail;
+  uint32_t ash[G::kNA], wsh[G::kNB];  // bytes past a word of each row (the same at every step)
+#pragma unroll
+  for (int i = 0; i < G::kNA; ++i) ash[i] = (uint32_t)(uintptr_t)arow[i] & 3u;
+#pragma unroll
+  for (int i = 0; i < G::kNB; ++i) wsh[i] = (uint32_t)(uintptr_t)wrow[i] & 3u;
+  int8_t* dst_a = sm + wave * G::kNA * 1024 + lane * 16;
+  int8_t* dst_w = sm + G::kBM * 64 + wave * G::kNB * 1024 + lane * 16;
+  struct Regs {
+    Words a[G::kNA], w[G::kNB];
+  };
+  auto load = [&](int s, Regs& r) {  // full steps only (past the last one the last again)
+    const int64_t k = (int64_t)(min(s, nsteps - 1) - tail) * 64 + chunk;
+#pragma unroll
+    for (int i = 0; i < G::kNA; ++i) r.a[i] = load_words(arow[i] + k, ash[i]);
+#pragma unroll
+    for (int i = 0; i < G::kNB; ++i) r.w[i] = load_words(wrow[i] + k, wsh[i]);
+  };
+  auto store = [&](int st, const Regs& r) {
+#pragma unroll
+    for (int i = 0; i < G::kNA; ++i) *reinterpret_cast<uint4*>(dst_a + st * G::kStage + i * 1024) = shifted(r.a[i], ash[i]);
+#pragma unroll
+    for (int i = 0; i < G::kNB; ++i) *reinterpret_cast<uint4*>(dst_w + st * G::kStage + i * 1024) = shifted(r.w[i], wsh[i]);
+  };
 
-  // thread t loads the 32 bytes at 32 (t % 2) of row t / 2 of both tiles
-  const int row = tid >> 1, half = (tid & 1) * 32;
-  const int8_t* ar = p.a + min(m0 + row, p.M - 1) * p.as;
-  const int8_t* wr = p.w + min(n0 + row, p.N - 1) * p.ws;
-  uint4 ra[2], rw[2];
-  auto load = [&](int64_t kt) {
+  v16i acc[TM][TN];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      ra[i] = load16(ar, kt * kBK + half + 16 * i, p.K);
-      rw[i] = load16(wr, kt * kBK + half + 16 * i, p.K);
-    }
-  };
-  auto store = [&](int buf) {
+  for (int mt = 0; mt < TM; ++mt)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      *reinterpret_cast<uint4*>(s.a[buf] + row * kRow + half + 16 * i) = ra[i];
-      *reinterpret_cast<uint4*>(s.w[buf] + row * kRow + half + 16 * i) = rw[i];
-    }
+    for (int nt = 0; nt < TN; ++nt) acc[mt][nt] = v16i{};
+  v4i fa[2][TM], fb[2][TN];
+  const int slot0 = (kh ^ swizzle<64>(lane & 31)) * 16;
+  const int abase = (wm * TM * 32 + (lane & 31)) * 64, bbase = (G::kBM + wn * TN * 32 + (lane & 31)) * 64;
+  auto frags = [&](int st, int ks) {
+    const int8_t* base = sm + st * G::kStage + (slot0 ^ (ks * 32));
+#pragma unroll
+    for (int mt = 0; mt < TM; ++mt) fa[ks][mt] = *reinterpret_cast<const v4i*>(base + abase + mt * 2048);
+#pragma unroll
+    for (int nt = 0; nt < TN; ++nt) fb[ks][nt] = *reinterpret_cast<const v4i*>(base + bbase + nt * 2048);
   };
-  if (nk > 0) {
-    load(0);
-    store(0);
+  auto products = [&](int ks) {
+#pragma unroll
+    for (int mt = 0; mt < TM; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < TN; ++nt)
+        acc[mt][nt] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks][nt], fa[ks][mt], acc[mt][nt], 0, 0, 0);
+  };
+
+  if (nsteps > 0) {
+    Regs r0, r1;
+    // step 0 (the partial one when there is one; rows shorter than a step have no other)
+    if (tail) {
+#pragma unroll
+      for (int i = 0; i < G::kNA; ++i) *reinterpret_cast<uint4*>(dst_a + i * 1024) = load16(arow[i], full * 64 + chunk, p.K);
+#pragma unroll
+      for (int i = 0; i < G::kNB; ++i) *reinterpret_cast<uint4*>(dst_w + i * 1024) = load16(wrow[i], full * 64 + chunk, p.K);
+    } else {
+      load(0, r0);
+      store(0, r0);
+    }
+    if (nsteps > 1) {
+      load(1, r1);
+      load(2, r0);
+      store(1, r1);
+      load(3, r1);
+    }
+    __syncthreads();
+    frags(0, 0);
+    int st = 0;
+    // step s from stage st: `next` holds step s + 2
+    auto step = [&](int s, Regs& next) {
+      const int nx = st + 1 == NS ? 0 : st + 1, nn = nx + 1 == NS ? 0 : nx + 1;
+      frags(st, 1);
+      products(0);
+      __syncthreads();  // every wave has read stage st - 1 (= nn) in full, and step s + 1 is in nx
+      frags(nx, 0);
+      if (nsteps > 1) {
+        store(nn, next);
+        load(s + 4, next);
+      }
+      products(1);
+      st = nx;
+    };
+    for (int s = 0; s < nsteps; s += 2) {
+      step(s, r0);
+      if (s + 1 < nsteps) step(s + 1, r1);
+    }
   }
   __syncthreads();
-  for (int64_t kt = 0; kt < nk; ++kt) {
-    const int buf = (int)(kt & 1);
-    if (kt + 1 < nk) load(kt + 1);
-#pragma unroll
-    for (int ks = 0; ks < kBK / 32; ++ks) {
-      v4i av[2], bv[2];
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-        av[mt] = *reinterpret_cast<const v4i*>(s.a[buf] + (wm * 64 + mt * 32 + (lane & 31)) * kRow + ks * 32 + 16 * kh);
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-        bv[nt] = *reinterpret_cast<const v4i*>(s.w[buf] + (wn * 64 + nt * 32 + (lane & 31)) * kRow + ks * 32 + 16 * kh);
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-          acc[mt][nt] = __builtin_amdgcn_mfma_i32_32x32x32_i8(av[mt], bv[nt], acc[mt][nt], 0, 0, 0);
-    }
-    if (kt + 1 < nk) {
-      store(buf ^ 1);
-      __syncthreads();
-    }
-  }
-
-  // register r of a tile holds row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
-#pragma unroll
-  for (int nt = 0; nt < 2; ++nt) {
-    const int64_t n = n0 + wn * 64 + nt * 32 + (lane & 31);
-    if (n >= p.N) continue;
-    const float sw = valid_or_zero(p.w_scales[n]), bn = p.bias ? p.bias[n] : 0.0f;
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int64_t m = m0 + wm * 64 + mt * 32 + 8 * (r / 4) + 4 * kh + (r % 4);
-        if (m < p.M) put(p, m, n, scaled(valid_or_zero(p.a_scales[p.per_row ? m : 0]), sw, acc[mt][nt][r], bn));
-      }
-  }
+  const int64_t mw = m0 + wm * TM * 32, nw = n0 + wn * TN * 32;
+  if (p.yf16) epilogue<TM, TN, false, __half>(p, sm, s_sw + wn * TN * 32, s_bias + wn * TN * 32, acc, sa, mw, nw, wave, lane);
+  else epilogue<TM, TN, false, float>(p, sm, s_sw + wn * TN * 32, s_bias + wn * TN * 32, acc, sa, mw, nw, wave, lane);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -565,14 +634,22 @@ constexpr Cost kCost[FORMS] = {{256, 256, 1, 10.2, 0.553, 0.0, 0.0},  {256, 128,
                                {128, 128, 2, 3.05, 0.281, 0.0, 0.0},  {128, 64, 4, 1.25, 0.201, 2.92, 0.188},
                                {64, 64, 2, 2.79, 0.137, 5.01, 0.119}, {32, 32, 2, 1.20, 0.047, 5.18, 0.022}};
 
-Form choose(const GemmParams& p) {
+// The same for rows at any address (k_gemm_w8a8_any; 64x64 / 128x128 / 256x128): 3 x 1001 x 1501 takes
+// 10 / 19 / 24 us, 777 x 1001 x 1501 14 / 24 / 31, 2000 x 3001 x 2001 55 / 44 / 37, 4096 x 4095 x 4097
+// 301 / 178 / 151.
+enum AnyForm { ANY64, ANY128, ANY256X128, ANY_FORMS };
+constexpr Cost kAnyCost[ANY_FORMS] = {{64, 64, 1, 0.0, 0.29, 0.0, 0.36}, {128, 128, 1, 0.0, 0.69, 0.0, 0.69},
+                                      {256, 128, 1, 0.0, 1.16, 0.0, 0.90}};
+
+// Index of the cheapest of n forms.
+int choose(const GemmParams& p, const Cost* costs, int n) {
   constexpr double kCus = 256.0;
   const double steps = (double)cdiv(p.K, 64);
   const double bytes = ((double)p.M + (double)p.N) * (double)p.K + (p.yf16 ? 2.0 : 4.0) * (double)p.M * (double)p.N;
-  Form best = TILE256;
+  int best = 0;
   double least = 0.0;
-  for (int f = 0; f < FORMS; ++f) {
-    const Cost& c = kCost[f];
+  for (int f = 0; f < n; ++f) {
+    const Cost& c = costs[f];
     const double tiles = (double)cdiv(p.M, c.bm) * (double)cdiv(p.N, c.bn), slots = kCus * c.per_cu;
     const double rounds = std::floor(tiles / slots), rest = tiles - rounds * slots, busy = c.tile + c.step * steps;
     double t = rounds * c.per_cu * busy;
@@ -580,7 +657,7 @@ Form choose(const GemmParams& p) {
     t = std::max(t, bytes / 4.2e6);
     if (f == 0 || t < least) {
       least = t;
-      best = (Form)f;
+      best = f;
     }
   }
   return best;
@@ -618,11 +695,14 @@ extern "C" qssm_status qssm_gemm_w8a8(const qssm_gemm_w8a8_args* a, hipStream_t 
   // direct loads take addresses that are multiples of 4 bytes
   const bool direct = ((uintptr_t)a->a | (uintptr_t)a->w | (uintptr_t)a->a_stride | (uintptr_t)a->w_stride) % 4 == 0;
   if (!direct || K < 64) {
-    if (cdiv(M, kBM) > 65535) return fail(QSSM_ERR_UNSUPPORTED, "M above 65535 * 128 with unaligned rows");
-    k_gemm_w8a8<<<dim3((unsigned)cdiv(N, kBN), (unsigned)cdiv(M, kBM)), 256, 0, stream>>>(p);
+    switch (choose(p, kAnyCost, ANY_FORMS)) {
+      case ANY64: k_gemm_w8a8_any<2, 2, 1, 1><<<grid_of(p, 64, 64), 256, 0, stream>>>(p); break;
+      case ANY128: k_gemm_w8a8_any<2, 2, 2, 2><<<grid_of(p, 128, 128), 256, 0, stream>>>(p); break;
+      default: k_gemm_w8a8_any<4, 2, 2, 2><<<grid_of(p, 256, 128), 512, 0, stream>>>(p); break;
+    }
     return launch_status("gemm_w8a8");
   }
-  switch (choose(p)) {
+  switch (choose(p, kCost, FORMS)) {
     case TILE256: k_gemm_w8a8_tile<2, 4, 4, 2, 4><<<grid_of(p, 256, 256), 512, 0, stream>>>(p); break;
     case TILE256X128: k_gemm_w8a8_tile<4, 2, 2, 2, 3><<<grid_of(p, 256, 128), 512, 0, stream>>>(p); break;
     case TILE128: k_gemm_w8a8_tile<2, 2, 2, 2, 4><<<grid_of(p, 128, 128), 256, 0, stream>>>(p); break;

@@ -81,7 +81,10 @@ def test_against_oracle(dev, M, N, K):
 # loaded), each with K below, at and above its number of stages.
 EVERY_FORM = [(4100, 4100, 964), (4000, 4090, 4096), (2300, 4300, 132), (4097, 3000, 64), (260, 9000, 132), (1030, 4000, 2052),
               (130, 6000, 100), (300, 4000, 700), (250, 4090, 4100), (256, 4096, 260), (70, 1000, 132), (16, 2000, 68), (9, 500, 2044),
-              (1000, 4000, 4100), (60, 1000, 4100)]
+              (1000, 4000, 4100), (60, 1000, 4100),
+              # rows at odd addresses, in each of their tile sizes; rows shorter than a step
+              (2000, 3001, 131), (4000, 1500, 2049), (1500, 1501, 197), (130, 700, 77), (200, 300, 63), (70, 70, 1),
+              (300, 200, 65), (130, 130, 62)]
 
 
 @pytest.mark.parametrize("M,N,K", EVERY_FORM)
@@ -90,7 +93,7 @@ def test_every_form(dev, M, N, K):
     print(f"\n[gemm_w8a8 forms M={M} N={N} K={K}]", flush=True)
     a, sa, w, sw, b = make(M + K, M, N, K)
     f16 = K % 8 == 4
-    y = run(dev, a, sa, w, sw, b, f16)
+    y = run(dev, a, sa, w, sw, b, f16, pads=(0, 0, 3 if M % 4 else 0))
     rows = np.unique(np.concatenate([[0, M - 1, M // 2], np.random.default_rng(M).integers(0, M, 300)]))
     yb = ow.gemm_w8a8(a[rows], sa[rows], w, sw)
     want = yb + b.astype(np.float64)
