@@ -181,9 +181,15 @@ def _ptr(t, dtype=None, name="tensor", optional=False):
     return ctypes.c_void_p(t.data_ptr())
 
 
+_torch = None
+
+
 def _t():
-    import torch
-    return torch
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
 
 
 # ------------------------------------------------------------------------------------------------
@@ -547,31 +553,46 @@ def _rows(t, dtype, name, shape, optional=False):
     return ctypes.c_void_p(t.data_ptr()), stride
 
 
-def _row_values(h, codes, scales, name):
-    """(rows, N) of state rows h [..., N] with codes of the same shape and one scale a row."""
+def _addr(t, name):
+    """Address of a contiguous GPU tensor (None for None)."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _check_rows(codes, scales):
     torch = _t()
-    if h.dim() < 1 or codes.shape != h.shape or scales.shape != h.shape[:-1]:
-        raise ValueError(f"{name} and codes must be [..., N] of one shape and scales [...]")
     if codes.dtype != torch.int8 or scales.dtype != torch.float32:
-        raise TypeError("codes must be int8 and scales float32")
-    return scales.numel(), h.shape[-1]
+        raise TypeError("state codes must be int8 and their scales float32")
+    if scales.shape != codes.shape[:-1]:
+        raise ValueError("the scales must have the codes' shape without the last dimension")
+
+
+def _state_rows(name, h, codes, scales, stream, first):
+    """The call of qssm_state_quant (h first) or qssm_state_dequant (codes first)."""
+    if h.dim() < 1 or codes.shape != h.shape:
+        raise ValueError("the values and the codes must be [..., N] of one shape")
+    _check_rows(codes, scales)
+    n = (scales.numel(), h.shape[-1])
+    hp, ht = _addr(h, "values"), _float_type(h, "values")
+    cp, sp = _addr(codes, "codes"), _addr(scales, "scales")
+    args = (hp, ht, *n, cp, sp) if first else (cp, sp, *n, hp, ht)
+    _call(name, _device_of(h, codes, scales), stream, *args, keep=(h, codes, scales))
 
 
 def qssm_state_quant(h, codes, scales, stream=None):
     """h [..., N] float32 or float16 -> codes int8 [..., N] and scales float32 [...], one a row."""
-    rows, N = _row_values(h, codes, scales, "h")
-    _call("qssm_state_quant", _device_of(h, codes, scales), stream, _ptr(h, None, "h"),
-          _float_type(h, "h"), rows, N, _ptr(codes, None, "codes"), _ptr(scales, None, "scales"),
-          keep=(h, codes, scales))
+    _state_rows("qssm_state_quant", h, codes, scales, stream, True)
     return codes, scales
 
 
 def qssm_state_dequant(codes, scales, out, stream=None):
     """out [..., N] float32 or float16 = scales * codes."""
-    rows, N = _row_values(out, codes, scales, "out")
-    _call("qssm_state_dequant", _device_of(out, codes, scales), stream, _ptr(codes, None, "codes"),
-          _ptr(scales, None, "scales"), rows, N, _ptr(out, None, "out"), _float_type(out, "out"),
-          keep=(codes, scales, out))
+    _state_rows("qssm_state_dequant", out, codes, scales, stream, False)
     return out
 
 
@@ -579,20 +600,19 @@ def qssm_state_update_i8(args, state_scales, state_in=None, scales_in=None, stre
     """The decode update on an int8 state: args from update_args with an int8 state (the codes
     written), state_scales float32 [B, nh, P] the scales written; state_in and scales_in the codes
     and scales read (both None: in place)."""
-    torch = _t()
     state = args._state
-    if state.dtype != torch.int8:
-        raise TypeError("update_args was given a state that is not int8")
-    rows = state.shape[:-1]
-    if state_scales.shape != rows or (scales_in is not None and scales_in.shape != rows):
-        raise ValueError("the scales must be [B, nh, P]")
-    if state_in is not None and state_in.shape != state.shape:
-        raise ValueError("state_in must have the state's shape")
-    keep = args._keep + [t for t in (state_scales, state_in, scales_in) if t is not None]
+    _check_rows(state, state_scales)
+    keep = [*args._keep, state_scales]
+    if state_in is not None or scales_in is not None:
+        if state_in is None or scales_in is None:
+            raise ValueError("state_in and scales_in go together")
+        if state_in.shape != state.shape:
+            raise ValueError("state_in must have the state's shape")
+        _check_rows(state_in, scales_in)
+        keep += [state_in, scales_in]
     _call("qssm_state_update_i8", _device_of(state, state_scales, state_in, scales_in), stream,
-          ctypes.byref(args), _ptr(state_in, torch.int8, "state_in", True),
-          _ptr(scales_in, torch.float32, "scales_in", True),
-          _ptr(state_scales, torch.float32, "state_scales"), keep=keep)
+          ctypes.byref(args), _addr(state_in, "state_in"), _addr(scales_in, "scales_in"),
+          _addr(state_scales, "state_scales"), keep=keep)
 
 
 def rmsnorm_args(x, q, scales, weight=None, eps=1e-5, residual=None, residual_out=None, gate=None,

@@ -149,3 +149,27 @@ def test_binding_refuses_mismatched_tensors():
                           torch.zeros(8, 32, dtype=torch.int8), torch.zeros(8), torch.zeros(4, 8))
     with pytest.raises(ValueError, match="shape"):
         qs.qssm_state_quant(x, torch.zeros(4, 32, dtype=torch.int8), torch.zeros(4))
+
+
+def test_state_binding_refusals():
+    """Shapes, types and pairs that the binding refuses before it asks for a GPU."""
+    import torch
+    i8, f = torch.int8, torch.float32
+    with pytest.raises(TypeError, match="int8"):
+        qs.qssm_state_quant(torch.zeros(4, 8), torch.zeros(4, 8), torch.zeros(4))
+    with pytest.raises(ValueError, match="scales"):
+        qs.qssm_state_dequant(torch.zeros(4, 8, dtype=i8), torch.zeros(3), torch.zeros(4, 8))
+    with pytest.raises(ValueError, match="GPU"):
+        qs.qssm_state_quant(torch.zeros(4, 8), torch.zeros(4, 8, dtype=i8), torch.zeros(4))
+    a = qs.UpdateArgs()
+    a._keep, a._state = [], torch.zeros(1, 2, 3, 16, dtype=i8)
+    sc = torch.zeros(1, 2, 3, dtype=f)
+    with pytest.raises(ValueError, match="together"):
+        qs.qssm_state_update_i8(a, sc, state_in=a._state)
+    with pytest.raises(ValueError, match="shape"):
+        qs.qssm_state_update_i8(a, sc, state_in=torch.zeros(1, 2, 3, 32, dtype=i8), scales_in=sc)
+    with pytest.raises(ValueError, match="scales"):
+        qs.qssm_state_update_i8(a, torch.zeros(1, 2, 4))
+    a._state = torch.zeros(1, 2, 3, 16)
+    with pytest.raises(TypeError, match="int8"):
+        qs.qssm_state_update_i8(a, sc)
