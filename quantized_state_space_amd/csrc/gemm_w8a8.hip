@@ -7,9 +7,9 @@
 // wave holds row (or column) l % 32 and the 16 consecutive k at 16 (l / 32). The weights go in as the
 // first operand, so a lane ends with one token and groups of 4 consecutive output channels.
 //
-// Two forms: tiles shared by a workgroup's waves with K in common steps (many tokens: bound by the
-// matrix cores and the power they draw), and small tiles with K split over the waves (few tokens,
-// few tiles: bound by the bytes of the weights and by latency). choose() picks by estimated time.
+// Tiles shared by a workgroup's waves with K in common steps (k_gemm_w8a8_tile, and k_gemm_w8a8_any for
+// rows at any address), and the smallest tiles with K split over the waves (k_gemm_w8a8_split: few tokens,
+// bound by the bytes of the weights and by latency). choose() picks by estimated time.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -108,22 +108,26 @@ __device__ __forceinline__ int swizzle(int row) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Tiles of (32 WM TM) x (32 WN TN) shared by WM x WN waves. K runs in steps of 64 bytes through NS LDS
+// Tiles of (32 WM TM) x (32 WN TN) shared by WM x WN waves. K runs in steps of BK bytes through NS LDS
 // stages that direct loads fill NS - 1 steps ahead; one barrier per step, placed where every wave has
-// the step's last fragments in registers, so that the products of half a step hide it. Fragments are
-// read half a step ahead and the reads and loads are issued between the products.
-// The partial step of a K that is no multiple of 64 is the first and goes through registers, with
+// the step's last fragments in registers, so that the last slice's products hide it. Fragments are
+// read a slice of 32 codes ahead, and reads and loads are issued between the products.
+// Steps of 128 and few stages beat steps of 64 and twice the stages (half the barriers): 256x256 tiles,
+// 16384 x 18560 x 4096: 1069 us (2.33 POPS) and 1128; 128x64 tiles, 256 x 4096 x 8192: 22 and 27.
+// The many-token forms are bound by the power the matrix cores draw: with all operands 0 the same
+// kernel runs a third faster.
+// The partial step of a K that is no multiple of BK is the first and goes through registers, with
 // zeros past K. Rows past M or N read the last row and are not stored.
 // Tile order: the tiles are cut into 8 contiguous ranges, one per XCD (workgroups are dealt to the
 // XCDs in turn), in groups of 4 row tiles, so the workgroups that run together on an XCD share rows
-// and columns in its L2 (16384 x 18560 x 4096: groups of 4 / 8 / 16 take 1151 / 1161 / 1195 us).
+// and columns in its L2 (16384 x 18560 x 4096: groups of 4 / 8 / 16 took 1151 / 1161 / 1195 us).
 // Output: each wave scales its sums and turns 32 rows at a time through LDS into whole-row stores
 // (stores straight from the registers took 23 us a tile, a third of the whole at K = 4096).
-template <int WM, int WN, int TM, int TN, int NS>
+template <int WM, int WN, int TM, int TN, int NS, int BK>
 struct Tile {
-  static constexpr int kWaves = WM * WN, kBM = WM * TM * 32, kBN = WN * TN * 32;
-  static constexpr int kNA = kBM / 16 / kWaves, kNB = kBN / 16 / kWaves;  // direct loads of a wave (16 rows each)
-  static constexpr int kStage = (kBM + kBN) * 64;
+  static constexpr int kWaves = WM * WN, kBM = WM * TM * 32, kBN = WN * TN * 32, kRpl = 1024 / BK;
+  static constexpr int kNA = kBM / kRpl / kWaves, kNB = kBN / kRpl / kWaves;  // loads of a wave, kRpl rows each
+  static constexpr int kStage = (kBM + kBN) * BK;
 };
 
 __device__ __forceinline__ void to_type(float v, __half& o) { o = __float2half_rn(v); }
@@ -220,10 +224,10 @@ __device__ __forceinline__ void load_scales(const GemmParams& p, int bn, int64_t
   }
 }
 
-template <int WM, int WN, int TM, int TN, int NS>
+template <int WM, int WN, int TM, int TN, int NS, int BK>
 __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
-  using G = Tile<WM, WN, TM, TN, NS>;
-  constexpr int kLd = G::kNA + G::kNB;
+  using G = Tile<WM, WN, TM, TN, NS, BK>;
+  constexpr int kLd = G::kNA + G::kNB, kSlots = BK / 16, kSlices = BK / 32;
   static_assert(WM * WN * 32 * (TN * 32 * 4 + 16) <= NS * G::kStage, "the output buffers fit the stages");
   // one array: with several the compiler waits for all direct loads before every LDS read
   __shared__ __align__(1024) int8_t sm[NS * G::kStage + 8 * G::kBN];
@@ -236,30 +240,36 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
   if (!tile_of(p, G::kBM, G::kBN, m0, n0)) return;
   float sa[TM];
   load_scales<TM>(p, G::kBN, m0 + wm * TM * 32, n0, lane, tid, G::kWaves * 64, s_sw, s_bias, sa);
-  // direct load i of this wave: 16 rows, lane l at row l / 4, slot l % 4 (32-bit offsets: host)
+  // load i of this wave: kRpl rows, lane l at row l / kSlots, slot l % kSlots (32-bit offsets: host)
   const int8_t* abase = p.a + m0 * p.as;
   const int8_t* wbase = p.w + n0 * p.ws;
-  const int lrow = lane >> 2, chunk = (lane & 3) ^ swizzle<64>(lrow);
-  int aoff[G::kNA], woff[G::kNB];
+  const int lrow = lane / kSlots;
+  int aoff[G::kNA], woff[G::kNB], achk[G::kNA], wchk[G::kNB];
 #pragma unroll
-  for (int i = 0; i < G::kNA; ++i)
-    aoff[i] = (int)(min((int64_t)((wave * G::kNA + i) * 16 + lrow), p.M - 1 - m0) * p.as) + chunk * 16;
+  for (int i = 0; i < G::kNA; ++i) {
+    const int row = (wave * G::kNA + i) * G::kRpl + lrow;
+    achk[i] = ((lane % kSlots) ^ swizzle<BK>(row)) * 16;
+    aoff[i] = (int)(min((int64_t)row, p.M - 1 - m0) * p.as);
+  }
 #pragma unroll
-  for (int i = 0; i < G::kNB; ++i)
-    woff[i] = (int)(min((int64_t)((wave * G::kNB + i) * 16 + lrow), p.N - 1 - n0) * p.ws) + chunk * 16;
+  for (int i = 0; i < G::kNB; ++i) {
+    const int row = (wave * G::kNB + i) * G::kRpl + lrow;
+    wchk[i] = ((lane % kSlots) ^ swizzle<BK>(row)) * 16;
+    woff[i] = (int)(min((int64_t)row, p.N - 1 - n0) * p.ws);
+  }
   const __amdgpu_buffer_rsrc_t ra = rsrc_of(abase), rw = rsrc_of(wbase);
-  const int full = (int)(p.K / 64), tail = (int)(p.K % 64) != 0;  // host: full >= 1
+  const int full = (int)(p.K / BK), tail = (int)(p.K % BK) != 0;  // host: full >= 1
   const int nsteps = full + tail;
   int8_t* dst_a = sm + wave * G::kNA * 1024;
-  int8_t* dst_w = sm + G::kBM * 64 + wave * G::kNB * 1024;
+  int8_t* dst_w = sm + G::kBM * BK + wave * G::kNB * 1024;
 
   // step s into stage st; past the last step the last one again, so that the waits stay exact
   auto issue = [&](int s, int st) {
-    const int koff = (min(s, nsteps - 1) - tail) * 64;
+    const int koff = (min(s, nsteps - 1) - tail) * BK;
 #pragma unroll
-    for (int i = 0; i < G::kNA; ++i) load_lds(ra, dst_a + st * G::kStage + i * 1024, aoff[i], koff);
+    for (int i = 0; i < G::kNA; ++i) load_lds(ra, dst_a + st * G::kStage + i * 1024, aoff[i] + achk[i], koff);
 #pragma unroll
-    for (int i = 0; i < G::kNB; ++i) load_lds(rw, dst_w + st * G::kStage + i * 1024, woff[i], koff);
+    for (int i = 0; i < G::kNB; ++i) load_lds(rw, dst_w + st * G::kStage + i * 1024, woff[i] + wchk[i], koff);
   };
 
   v16i acc[TM][TN];
@@ -268,14 +278,15 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
 #pragma unroll
     for (int nt = 0; nt < TN; ++nt) acc[mt][nt] = v16i{};
   v4i fa[2][TM], fb[2][TN];
-  const int slot0 = (kh ^ swizzle<64>(lane & 31)) * 16;
-  const int arow = (wm * TM * 32 + (lane & 31)) * 64, brow = (G::kBM + wn * TN * 32 + (lane & 31)) * 64;
+  const int slot0 = (kh ^ swizzle<BK>(lane & 31)) * 16;
+  const int arow = (wm * TM * 32 + (lane & 31)) * BK, brow = (G::kBM + wn * TN * 32 + (lane & 31)) * BK;
+  // fragments of slice ks of stage st into set ks % 2
   auto frags = [&](int st, int ks) {
     const int8_t* base = sm + st * G::kStage + (slot0 ^ (ks * 32));
 #pragma unroll
-    for (int mt = 0; mt < TM; ++mt) fa[ks][mt] = *reinterpret_cast<const v4i*>(base + arow + mt * 2048);
+    for (int mt = 0; mt < TM; ++mt) fa[ks & 1][mt] = *reinterpret_cast<const v4i*>(base + arow + mt * 32 * BK);
 #pragma unroll
-    for (int nt = 0; nt < TN; ++nt) fb[ks][nt] = *reinterpret_cast<const v4i*>(base + brow + nt * 2048);
+    for (int nt = 0; nt < TN; ++nt) fb[ks & 1][nt] = *reinterpret_cast<const v4i*>(base + brow + nt * 32 * BK);
   };
 
   if (!tail) issue(0, 0);
@@ -284,10 +295,10 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
   if (tail) {
 #pragma unroll
     for (int i = 0; i < G::kNA; ++i)
-      *reinterpret_cast<uint4*>(dst_a + i * 1024 + lane * 16) = load16(abase + aoff[i] - chunk * 16, full * 64 + chunk * 16, p.K);
+      *reinterpret_cast<uint4*>(dst_a + i * 1024 + lane * 16) = load16(abase + aoff[i], full * BK + achk[i], p.K);
 #pragma unroll
     for (int i = 0; i < G::kNB; ++i)
-      *reinterpret_cast<uint4*>(dst_w + i * 1024 + lane * 16) = load16(wbase + woff[i] - chunk * 16, full * 64 + chunk * 16, p.K);
+      *reinterpret_cast<uint4*>(dst_w + i * 1024 + lane * 16) = load16(wbase + woff[i], full * BK + wchk[i], p.K);
   }
   wait_vm_lds<(NS - 1) * kLd>();
   __builtin_amdgcn_s_barrier();
@@ -297,19 +308,31 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
   constexpr int kMf = TM * TN, kDs = TM + TN;
   for (int s = 0; s < nsteps; ++s) {
     const int nx = st + 1 == NS ? 0 : st + 1;
-    auto products = [&](int ks) {
+#pragma unroll
+    for (int ks = 0; ks < kSlices; ++ks) {
+      const bool last = ks == kSlices - 1;
+      if (!last) {
+        frags(st, ks + 1);
+      } else {
+        // every wave has the last fragments of stage st in registers, and step s + 1 has landed
+        wait_vm_lds<(NS - 2) * kLd>();
+        __builtin_amdgcn_s_barrier();
+        fence();
+        frags(nx, 0);
+        issue(s + NS, st);
+      }
 #pragma unroll
       for (int mt = 0; mt < TM; ++mt)
 #pragma unroll
         for (int nt = 0; nt < TN; ++nt)
-          acc[mt][nt] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks][nt], fa[ks][mt], acc[mt][nt], 0, 0, 0);
-      // issue order: a product, two fragment reads, ... (second half: then a product, a load, ...)
+          acc[mt][nt] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks & 1][nt], fa[ks & 1][mt], acc[mt][nt], 0, 0, 0);
+      // issue order: a product, two fragment reads, ... (last slice: then a product, a load, ...)
 #pragma unroll
       for (int i = 0; i < kDs / 2; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
       }
-      if (ks == 1) {
+      if (last) {
 #pragma unroll
         for (int i = 0; i < kLd; ++i) {
           __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
@@ -318,16 +341,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
       }
       __builtin_amdgcn_sched_group_barrier(0x8, kMf, 0);
       __builtin_amdgcn_sched_barrier(0);
-    };
-    frags(st, 1);
-    products(0);
-    // every wave has the last fragments of stage st in registers, and step s + 1 has landed
-    wait_vm_lds<(NS - 2) * kLd>();
-    __builtin_amdgcn_s_barrier();
-    fence();
-    frags(nx, 0);
-    issue(s + NS, st);
-    products(1);
+    }
     st = nx;
   }
   wait_vm_lds<0>();  // no direct load outlives the stages it writes
@@ -339,22 +353,22 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
 
 // ------------------------------------------------------------------------------------------------
 // Tiles of (32 TM) x (32 TN) with K split over the W waves of a workgroup: wave k takes the units
-// k, k + W, ... of BK bytes, each through two LDS stages of its own that it fills and reads alone, so
+// k, k + W, ... of BK bytes, each through NS LDS stages of its own that it fills and reads alone, so
 // no barrier is needed until the waves' integer sums are joined (exactly, in any order) in LDS.
 // ROWS: token rows that are loaded (a multiple of 1024 / BK; tokens past M up to ROWS read the last
 // row, those past ROWS are whatever the LDS held: their sums are not stored).
-template <int TM, int TN, int BK, int W, int ROWS>
+template <int TM, int TN, int BK, int W, int ROWS, int NS>
 struct Split {
   static constexpr int kBM = TM * 32, kBN = TN * 32, kRpl = 1024 / BK;  // rows per load instruction
-  static constexpr int kNA = ROWS / kRpl, kNB = kBN / kRpl, kStages = 2;
+  static constexpr int kNA = ROWS / kRpl, kNB = kBN / kRpl;
   static constexpr int kStage = (kBM + kBN) * BK, kRow = kBN + 4;
-  static constexpr int kMain = kStages * W * kStage, kEnd = W * kBM * kRow * 4;
+  static constexpr int kMain = NS * W * kStage, kEnd = W * kBM * kRow * 4;
   static constexpr int kLds = kMain > kEnd ? kMain : kEnd;
 };
 
-template <int TM, int TN, int BK, int W, int ROWS, int PER>
-__global__ __launch_bounds__(W * 64, PER) void k_gemm_w8a8_split(GemmParams p) {
-  using G = Split<TM, TN, BK, W, ROWS>;
+template <int TM, int TN, int BK, int W, int ROWS, int NS>
+__global__ __launch_bounds__(W * 64, 2) void k_gemm_w8a8_split(GemmParams p) {
+  using G = Split<TM, TN, BK, W, ROWS, NS>;
   constexpr int BM = G::kBM, BN = G::kBN, kSlots = BK / 16, kLd = G::kNA + G::kNB;
   __shared__ __align__(1024) int8_t sm[G::kLds];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), kh = lane >> 5;
@@ -379,7 +393,7 @@ __global__ __launch_bounds__(W * 64, PER) void k_gemm_w8a8_split(GemmParams p) {
     wchk[i] = ((lane % kSlots) ^ swizzle<BK>(row)) * 16;
     woff[i] = (int)(min((int64_t)row, p.N - 1 - n0) * p.ws);
   }
-  int8_t* mine = sm + wave * G::kStages * G::kStage;
+  int8_t* mine = sm + wave * NS * G::kStage;
   const int full = (int)(p.K / BK);
 
   v16i acc[TM][TN];
@@ -425,15 +439,15 @@ __global__ __launch_bounds__(W * 64, PER) void k_gemm_w8a8_split(GemmParams p) {
     for (int i = 0; i < G::kNB; ++i) load_lds(rw, mine + st * G::kStage + BM * BK + i * 1024, woff[i] + wchk[i], koff);
   };
   if (wave < full) {
-    issue(wave, 0);
-    issue(wave + W, 1);
+#pragma unroll
+    for (int d = 0; d < NS; ++d) issue(wave + d * W, d);
     int st = 0;
     for (int u = wave; u < full; u += W) {
-      wait_vm_lds<kLd>();
+      wait_vm_lds<(NS - 1) * kLd>();
       products(st);
       wait_vm_lds<63>();  // the stage's fragments are in registers
-      issue(u + 2 * W, st);
-      st ^= 1;
+      issue(u + NS * W, st);
+      st = st + 1 == NS ? 0 : st + 1;
     }
     wait_vm_lds<0>();
   }
@@ -500,7 +514,7 @@ __device__ __forceinline__ uint4 shifted(const Words& r, uint32_t sh) {
 template <int WM, int WN, int TM, int TN>
 __global__ __launch_bounds__(WM * WN * 64, 2) void k_gemm_w8a8_any(GemmParams p) {
   constexpr int NS = 3;
-  using G = Tile<WM, WN, TM, TN, NS>;
+  using G = Tile<WM, WN, TM, TN, NS, 64>;
   static_assert(WM * WN * 32 * (TN * 32 * 4 + 16) <= NS * G::kStage, "the output buffers fit the stages");
   __shared__ __align__(1024) int8_t sm[NS * G::kStage + 8 * G::kBN];
   float* s_sw = reinterpret_cast<float*>(sm + NS * G::kStage);
@@ -618,21 +632,21 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void k_gemm_w8a8_any(GemmParams p)
 // ------------------------------------------------------------------------------------------------
 // The form for a shape, by estimated time (us): a tile costs tile + step * (steps of 64 codes of K) of
 // its CU when all CUs are at work, at least tile_alone + step_alone * steps when they are not; the
-// whole at least the bytes at 4.2 TB/s. The constants are a fit (15 % rms) to 22 shapes of 1 .. 16384
-// tokens, N = 1024 .. 18560 and K = 128 .. 8192 in every form, and named the fastest form, or one within
-// 9 % of it, at all of them. Measured, e.g. (256x256 / 256x128 / 128x128 / 128x64 / split 64x64 / split 32x32):
-//   64 x 4096 x 8192      - / - / - / - / 22 / 9.4        256 x 4096 x 8192   70 / 49 / 32 / 26 / 20 / 25
-//   1000 x 1536 x 768     14 / 9.0 / 7.1 / 5.9 / 10 / 13  256 x 18560 x 4096  56 / 41 / 49 / 53 / 63 / 88
-//   1024 x 4096 x 4096    40 / 29 / 22 / 29 / 39 / 62     4096 x 4096 x 4096  63 / 75 / 85 / 114 / 176 / 291
-//   16384 x 1024 x 128    11.8 / 10.6 / 12.9 / 14.6 / 54 / 82
-enum Form { TILE256, TILE256X128, TILE128, TILE128X64, SPLIT64, SPLIT32, FORMS };
+// whole at least the bytes at 4.3 TB/s. The constants follow a fit (16 % rms) to 30 shapes of 1 .. 16384
+// tokens, N = 1024 .. 18560 and K = 128 .. 8192 in every form; they named the fastest form at 27 of them
+// and one within 3 to 14 % of it at the others. Measured, e.g. (256x256 / 256x128 / 128x128 / 128x64 /
+// 64x64 / split 32x32):
+//   64 x 4096 x 8192      69 / 38 / 30 / 21 / 18 / 9.3      256 x 4096 x 8192   72 / 40 / 31 / 22 / 18 / 25
+//   1000 x 1536 x 768     13 / 8.8 / 7.4 / 5.8 / 5.7 / 13   256 x 18560 x 4096  56 / 33 / 47 / 45 / 46 / 88
+//   1024 x 4096 x 4096    40 / 24 / 21 / 24 / 30 / 62       4096 x 4096 x 4096  58 / 66 / 82 / 90 / 111 / 294
+enum Form { TILE256, TILE256X128, TILE128, TILE128X64, TILE64, SPLIT32, FORMS };
 struct Cost {
   int bm, bn, per_cu;
   double tile, step, tile_alone, step_alone;
 };
-constexpr Cost kCost[FORMS] = {{256, 256, 1, 10.2, 0.553, 0.0, 0.0},  {256, 128, 2, 3.94, 0.417, 6.77, 0.064},
-                               {128, 128, 2, 3.05, 0.281, 0.0, 0.0},  {128, 64, 4, 1.25, 0.201, 2.92, 0.188},
-                               {64, 64, 2, 2.79, 0.137, 5.01, 0.119}, {32, 32, 2, 1.20, 0.047, 5.18, 0.022}};
+constexpr Cost kCost[FORMS] = {{256, 256, 1, 0.0, 0.68, 6.0, 0.591},  {256, 128, 1, 4.31, 0.321, 0.0, 0.0},
+                               {128, 128, 1, 3.93, 0.231, 0.0, 0.0},  {128, 64, 2, 1.48, 0.164, 2.56, 0.156},
+                               {64, 64, 3, 0.87, 0.104, 1.65, 0.111}, {32, 32, 2, 1.26, 0.048, 0.0, 0.0}};
 
 // The same for rows at any address (k_gemm_w8a8_any; 64x64 / 128x128 / 256x128): 3 x 1001 x 1501 takes
 // 10 / 19 / 24 us, 777 x 1001 x 1501 14 / 24 / 31, 2000 x 3001 x 2001 55 / 44 / 37, 4096 x 4095 x 4097
@@ -654,7 +668,7 @@ int choose(const GemmParams& p, const Cost* costs, int n) {
     const double rounds = std::floor(tiles / slots), rest = tiles - rounds * slots, busy = c.tile + c.step * steps;
     double t = rounds * c.per_cu * busy;
     if (rest > 0.0) t += std::max(c.tile_alone + c.step_alone * steps, busy * std::ceil(rest / kCus));
-    t = std::max(t, bytes / 4.2e6);
+    t = std::max(t, bytes / 4.3e6);
     if (f == 0 || t < least) {
       least = t;
       best = f;
@@ -694,7 +708,7 @@ extern "C" qssm_status qssm_gemm_w8a8(const qssm_gemm_w8a8_args* a, hipStream_t 
                      a->w, a->w_stride, a->w_scales, a->bias, a->y, a->y_stride};
   // direct loads take addresses that are multiples of 4 bytes
   const bool direct = ((uintptr_t)a->a | (uintptr_t)a->w | (uintptr_t)a->a_stride | (uintptr_t)a->w_stride) % 4 == 0;
-  if (!direct || K < 64) {
+  if (!direct || K < 128) {
     switch (choose(p, kAnyCost, ANY_FORMS)) {
       case ANY64: k_gemm_w8a8_any<2, 2, 1, 1><<<grid_of(p, 64, 64), 256, 0, stream>>>(p); break;
       case ANY128: k_gemm_w8a8_any<2, 2, 2, 2><<<grid_of(p, 128, 128), 256, 0, stream>>>(p); break;
@@ -703,11 +717,11 @@ extern "C" qssm_status qssm_gemm_w8a8(const qssm_gemm_w8a8_args* a, hipStream_t 
     return launch_status("gemm_w8a8");
   }
   switch (choose(p, kCost, FORMS)) {
-    case TILE256: k_gemm_w8a8_tile<2, 4, 4, 2, 4><<<grid_of(p, 256, 256), 512, 0, stream>>>(p); break;
-    case TILE256X128: k_gemm_w8a8_tile<4, 2, 2, 2, 3><<<grid_of(p, 256, 128), 512, 0, stream>>>(p); break;
-    case TILE128: k_gemm_w8a8_tile<2, 2, 2, 2, 4><<<grid_of(p, 128, 128), 256, 0, stream>>>(p); break;
-    case TILE128X64: k_gemm_w8a8_tile<2, 2, 2, 1, 4><<<grid_of(p, 128, 64), 256, 0, stream>>>(p); break;
-    case SPLIT64: k_gemm_w8a8_split<2, 2, 64, 4, 64, 2><<<grid_of(p, 64, 64), 256, 0, stream>>>(p); break;
+    case TILE256: k_gemm_w8a8_tile<2, 4, 4, 2, 2, 128><<<grid_of(p, 256, 256), 512, 0, stream>>>(p); break;
+    case TILE256X128: k_gemm_w8a8_tile<4, 2, 2, 2, 3, 128><<<grid_of(p, 256, 128), 512, 0, stream>>>(p); break;
+    case TILE128: k_gemm_w8a8_tile<2, 2, 2, 2, 3, 128><<<grid_of(p, 128, 128), 256, 0, stream>>>(p); break;
+    case TILE128X64: k_gemm_w8a8_tile<2, 2, 2, 1, 3, 128><<<grid_of(p, 128, 64), 256, 0, stream>>>(p); break;
+    case TILE64: k_gemm_w8a8_tile<2, 2, 1, 1, 3, 128><<<grid_of(p, 64, 64), 256, 0, stream>>>(p); break;
     default:
       // up to 16 tokens load only 16 of a tile's 32 rows (8 tokens x 18560 x 4096: 18.9 us, 19.9 with all)
       if (M <= 16) k_gemm_w8a8_split<1, 1, 128, 4, 16, 2><<<grid_of(p, 32, 32), 256, 0, stream>>>(p);

@@ -77,11 +77,11 @@ def test_against_oracle(dev, M, N, K):
 
 
 # Shapes that reach every form of the kernel with ragged edges in M, N and K: 256 x 256, 256 x 128, 128 x 128,
-# 128 x 64 tiles, K split over four waves in 64 x 64 and 32 x 32 tiles (the last with 16 or 32 token rows
-# loaded), each with K below, at and above its number of stages.
+# 128 x 64 and 64 x 64 tiles, K split over four waves in 32 x 32 tiles (with 16 or 32 token rows loaded),
+# each with few steps of K and many, whole and partial.
 EVERY_FORM = [(4100, 4100, 964), (4000, 4090, 4096), (2300, 4300, 132), (4097, 3000, 64), (260, 9000, 132), (1030, 4000, 2052),
               (130, 6000, 100), (300, 4000, 700), (250, 4090, 4100), (256, 4096, 260), (70, 1000, 132), (16, 2000, 68), (9, 500, 2044),
-              (1000, 4000, 4100), (60, 1000, 4100),
+              (1000, 4000, 4100), (60, 1000, 4100), (2000, 8000, 2000), (4000, 4000, 384), (250, 4000, 256), (50, 500, 128),
               # rows at odd addresses, in each of their tile sizes; rows shorter than a step
               (2000, 3001, 131), (4000, 1500, 2049), (1500, 1501, 197), (130, 700, 77), (200, 300, 63), (70, 70, 1),
               (300, 200, 65), (130, 130, 62)]
