@@ -395,7 +395,7 @@ typedef struct qssm_update_args {
   const float* delta;                     /* [B, nh] */
   const float* A;                         /* [nh] */
   const float* Dskip;                     /* [nh] or NULL */
-  int32_t state_dtype;                    /* QSSM_F32 or QSSM_F16 */
+  int32_t state_dtype;                    /* QSSM_F32 or QSSM_F16 (QSSM_I8: qssm_state_update_i8) */
   void* state;                            /* [B, nh, P, N] in/out */
   void* y;                                /* [B, nh, P], fp32 or int8 codes (y_dtype) */
   int8_t* xq_out;                         /* [B, nh, P] or NULL */
@@ -503,7 +503,7 @@ qssm_status qssm_rmsnorm_i8(const qssm_rmsnorm_args* a, hipStream_t stream);
  * else QSSM_ERR_UNSUPPORTED), is rounded once to fp32, and one fused multiply-add scales it and
  * adds the bias; an fp16 y is rounded once more. K == 0 gives y = bias. Any M, N >= 0, any
  * alignment of a and w (addresses and strides that are multiples of 4 bytes take the fast forms);
- * a_stride and w_stride at most 2^22.
+ * a_stride and w_stride at most 2^22, M and N at most 2^27.
  */
 typedef struct qssm_gemm_w8a8_args {
   int64_t M, N, K;

@@ -655,21 +655,24 @@ enum AnyForm { ANY64, ANY128, ANY256X128, ANY_FORMS };
 constexpr Cost kAnyCost[ANY_FORMS] = {{64, 64, 1, 0.0, 0.29, 0.0, 0.36}, {128, 128, 1, 0.0, 0.69, 0.0, 0.69},
                                       {256, 128, 1, 0.0, 1.16, 0.0, 0.90}};
 
+constexpr int64_t kMaxTiles = ((int64_t)1 << 23) - 8;
+
 // Index of the cheapest of n forms.
 int choose(const GemmParams& p, const Cost* costs, int n) {
   constexpr double kCus = 256.0;
   const double steps = (double)cdiv(p.K, 64);
   const double bytes = ((double)p.M + (double)p.N) * (double)p.K + (p.yf16 ? 2.0 : 4.0) * (double)p.M * (double)p.N;
-  int best = 0;
+  int best = -1;
   double least = 0.0;
   for (int f = 0; f < n; ++f) {
     const Cost& c = costs[f];
     const double tiles = (double)cdiv(p.M, c.bm) * (double)cdiv(p.N, c.bn), slots = kCus * c.per_cu;
+    if (tiles >= (double)kMaxTiles) continue;
     const double rounds = std::floor(tiles / slots), rest = tiles - rounds * slots, busy = c.tile + c.step * steps;
     double t = rounds * c.per_cu * busy;
     if (rest > 0.0) t += std::max(c.tile_alone + c.step_alone * steps, busy * std::ceil(rest / kCus));
     t = std::max(t, bytes / 4.3e6);
-    if (f == 0 || t < least) {
+    if (best < 0 || t < least) {
       least = t;
       best = f;
     }
@@ -692,8 +695,8 @@ extern "C" qssm_status qssm_gemm_w8a8(const qssm_gemm_w8a8_args* a, hipStream_t 
   if (a->a_stride < K || a->w_stride < K || a->y_stride < N)
     return fail(QSSM_ERR_INVALID_ARG, "a row stride is smaller than the row");
   const int64_t lim = (int64_t)1 << 40;  // row offsets stay far inside 64 bits
-  if (a->a_stride > lim || a->w_stride > lim || a->y_stride > lim || M > 0x7fffffff || N > 0x7fffffff)
-    return fail(QSSM_ERR_UNSUPPORTED, "M or N above 2^31 - 1 or a stride above 2^40");
+  if (a->a_stride > lim || a->w_stride > lim || a->y_stride > lim || M > (1 << 27) || N > (1 << 27))
+    return fail(QSSM_ERR_UNSUPPORTED, "M or N above 2^27 or a stride above 2^40");
   if (M == 0 || N == 0) return QSSM_OK;
   if (!a->a_scales || !a->w_scales || !a->y || (K > 0 && (!a->a || !a->w)))
     return fail(QSSM_ERR_INVALID_ARG, "null required pointer");
@@ -702,8 +705,8 @@ extern "C" qssm_status qssm_gemm_w8a8(const qssm_gemm_w8a8_args* a, hipStream_t 
   // 32-bit offsets inside a tile
   if (std::max(a->a_stride, a->w_stride) > (1 << 22))
     return fail(QSSM_ERR_UNSUPPORTED, "a_stride or w_stride above 2^22");
-  // every form's grid: the smallest tiles are 32 x 32
-  if (cdiv(M, 32) * cdiv(N, 32) > 0x7ffffff0) return fail(QSSM_ERR_UNSUPPORTED, "M * N too large");
+  // a grid holds fewer than 2^32 threads, 512 a workgroup
+  if (cdiv(M, 256) * cdiv(N, 128) >= kMaxTiles) return fail(QSSM_ERR_UNSUPPORTED, "M * N too large");
   const GemmParams p{M, N, K, a->a_per_row != 0, a->y_dtype == QSSM_F16, a->a, a->a_stride, a->a_scales,
                      a->w, a->w_stride, a->w_scales, a->bias, a->y, a->y_stride};
   // direct loads take addresses that are multiples of 4 bytes

@@ -26,6 +26,7 @@ constexpr int64_t kMaxDimNarrow = 8192;  // VEC = 1: 8 channels per thread
 constexpr int64_t kMaxDimWide = 32768;   // VEC = 8: 4 vectors of 8 per thread
 
 struct NormParams {
+  int64_t M;
   int32_t D, Dg, Gn, dynamic;
   uint32_t inv_dg;  // ceil(2^32 / Dg): c / Dg is the high word of c * inv_dg for c, Dg <= 32768
   const void* x;
@@ -143,7 +144,8 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
   extern __shared__ __align__(16) unsigned char smem[];  // several groups: one partial per vector
   __shared__ double red_sum[kMaxWaves];
   __shared__ float red_max[kMaxWaves];
-  const int64_t row = blockIdx.x;
+  const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (row >= p.M) return;  // grid padding (the whole workgroup)
   const int tid = threadIdx.x, T = blockDim.x, lane = tid & 63, wave = tid >> 6, nw = T >> 6;
 
   float t[VPT][VEC];
@@ -279,7 +281,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
 }
 
 template <int VEC, int VPT, bool XF16>
-void launch_vpt(const NormParams& p, int res, int gate, unsigned rows, int threads, hipStream_t st) {
+void launch_vpt(const NormParams& p, int res, int gate, dim3 rows, int threads, hipStream_t st) {
   size_t smem = 0;
   if (p.Gn > 1) smem = VEC == 1 ? (size_t)p.D * 4 : (size_t)(p.D / VEC) * 8;
   if (gate == 1) k_rmsnorm_i8<VEC, VPT, XF16, 0, 1><<<rows, threads, smem, st>>>(p);
@@ -290,17 +292,20 @@ void launch_vpt(const NormParams& p, int res, int gate, unsigned rows, int threa
 }
 
 template <int VEC, bool XF16>
-void launch_vec(const NormParams& p, int res, int gate, unsigned rows, hipStream_t st) {
+void launch_vec(const NormParams& p, int res, int gate, hipStream_t st) {
   const int64_t nvec = p.D / VEC;
   // Few rows: as many threads as the row feeds (latency). Many: smaller workgroups, of which more run
   // at once and cover each other's reductions (16384 x 8192 gated: 218 / 223 / 240 us with up to 256 /
   // 512 / 1024 threads; 16384 x 4096 with a stream: 137 / 131 / 131; 1111 x 1543: 9.4 / 10.8 / 13.0)
-  const int cap = rows < 512 ? kMaxThreads : (gate || VEC == 1 ? 256 : 512);
+  const int cap = p.M < 512 ? kMaxThreads : (gate || VEC == 1 ? 256 : 512);
   const int threads = (int)std::min<int64_t>(cdiv(nvec, 64) * 64, std::max<int64_t>(cap, cdiv(cdiv(nvec, VEC == 8 ? 4 : 8), 64) * 64));
   const int64_t vpt = cdiv(nvec, threads);
-  if (vpt == 1) launch_vpt<VEC, 1, XF16>(p, res, gate, rows, threads, st);
-  else if (VEC == 8 && vpt == 2) launch_vpt<VEC, 2, XF16>(p, res, gate, rows, threads, st);
-  else launch_vpt<VEC, VEC == 8 ? 4 : 8, XF16>(p, res, gate, rows, threads, st);
+  // a grid dimension holds fewer than 2^32 threads
+  const int64_t gx = std::min<int64_t>(p.M, (int64_t)1 << 21);
+  const dim3 grid((unsigned)gx, (unsigned)cdiv(p.M, gx));
+  if (vpt == 1) launch_vpt<VEC, 1, XF16>(p, res, gate, grid, threads, st);
+  else if (VEC == 8 && vpt == 2) launch_vpt<VEC, 2, XF16>(p, res, gate, grid, threads, st);
+  else launch_vpt<VEC, VEC == 8 ? 4 : 8, XF16>(p, res, gate, grid, threads, st);
 }
 
 bool dtype_ok(int32_t t) { return t == QSSM_F32 || t == QSSM_F16; }
@@ -346,7 +351,7 @@ extern "C" qssm_status qssm_rmsnorm_i8(const qssm_rmsnorm_args* a, hipStream_t s
     return fail(QSSM_ERR_UNSUPPORTED, "dim above 8192 (32768 with aligned rows and groups)");
   if (M == 0) return QSSM_OK;
   if (!a->x || !a->scales || !a->q) return fail(QSSM_ERR_INVALID_ARG, "null required pointer");
-  NormParams p{(int32_t)D, (int32_t)Dg, a->norm_groups, a->compute_scales != 0,
+  NormParams p{M, (int32_t)D, (int32_t)Dg, a->norm_groups, a->compute_scales != 0,
                Dg > 1 ? (uint32_t)((((uint64_t)1 << 32) + Dg - 1) / Dg) : 0u, a->x, a->residual, a->residual_out,
                a->gate, a->x_stride, a->residual_stride, a->residual_out_stride, a->gate_stride,
                a->q_stride, a->weight, a->eps, a->scales, a->q};
@@ -354,11 +359,11 @@ extern "C" qssm_status qssm_rmsnorm_i8(const qssm_rmsnorm_args* a, hipStream_t s
   const int gate = !a->gate ? 0 : (a->gate_dtype == QSSM_F16 ? 1 : 2);
   const bool xf16 = a->x_dtype == QSSM_F16;
   if (wide) {
-    if (xf16) launch_vec<8, true>(p, res, gate, (unsigned)M, stream);
-    else launch_vec<8, false>(p, res, gate, (unsigned)M, stream);
+    if (xf16) launch_vec<8, true>(p, res, gate, stream);
+    else launch_vec<8, false>(p, res, gate, stream);
   } else {
-    if (xf16) launch_vec<1, true>(p, res, gate, (unsigned)M, stream);
-    else launch_vec<1, false>(p, res, gate, (unsigned)M, stream);
+    if (xf16) launch_vec<1, true>(p, res, gate, stream);
+    else launch_vec<1, false>(p, res, gate, stream);
   }
   return launch_status("rmsnorm_i8");
 }

@@ -180,7 +180,8 @@ int lanes_of(int64_t rows, int64_t N, const void* values, int32_t dtype, const i
     return 0;
   int L = 1;
   while (4 * L < N) L *= 2;
-  return cdiv(rows, kRows * (64 / L) * (kThreads / 64)) <= 0x7fffffff ? L : 0;
+  // a grid holds fewer than 2^32 threads
+  return cdiv(rows, kRows * (64 / L) * (kThreads / 64)) < ((int64_t)1 << 24) ? L : 0;
 }
 
 // Calls f(std::integral_constant L) for L lanes per row.

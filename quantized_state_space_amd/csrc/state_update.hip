@@ -11,6 +11,8 @@
 // accesses, and the readout sum over n is a shuffle reduction among the lanes sharing a row.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "common.hpp"
 
 using namespace qssm;
@@ -183,7 +185,8 @@ struct StateI8 {
   const float* s_in;
   int8_t* out;
   float* s_out;
-  int32_t tiles, rows;  // tiles of `rows` rows per (b, group)
+  int64_t tiles;  // of `rows` rows per (b, group)
+  int32_t rows;
 };
 
 constexpr float kMaxInRange = 0x1.fcp+106f;  // 127 * 2^100: the scale of a larger absmax is clamped
@@ -212,11 +215,13 @@ __global__ __launch_bounds__(kThreads) void k_state_update_i8(UpdParams p, State
   __shared__ __align__(16) float bs[N], cs[N];
   __shared__ __align__(16) float4 rowc[kMaxRows];
   const int tid = threadIdx.x;
-  const int64_t bg = blockIdx.x / st.tiles;  // b * Gbc + g
-  const int tile = (int)(blockIdx.x % st.tiles);
+  const int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const int64_t bg = id / st.tiles;  // b * Gbc + g
+  if (bg >= p.B * p.Gbc) return;     // grid padding (the whole workgroup)
+  const int64_t tile = id % st.tiles;
   const int64_t b = bg / p.Gbc, g = bg % p.Gbc;
   const int64_t grows = p.hpg * p.P;  // rows of the group
-  const int64_t r0 = (int64_t)tile * st.rows;
+  const int64_t r0 = tile * st.rows;
   const int n_rows = (int)min((int64_t)st.rows, grows - r0);
   const int64_t at0 = bg * grows + r0;  // first row in the state ([B, nh, P] = [B, Gbc, hpg P])
 
@@ -226,9 +231,13 @@ __global__ __launch_bounds__(kThreads) void k_state_update_i8(UpdParams p, State
   auto load = [&](int base) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int row = min(base + i * kPass + lrow, n_rows - 1);  // past the tile: its last row, not stored
-      raw[i] = *reinterpret_cast<const uint4*>(st.in + (at0 + row) * N + n0);
-      s_in[i] = st.s_in[at0 + row];
+      const int row = base + i * kPass + lrow;
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      s_in[i] = 0.0f;
+      if (row < n_rows) {
+        raw[i] = *reinterpret_cast<const uint4*>(st.in + (at0 + row) * N + n0);
+        s_in[i] = st.s_in[at0 + row];
+      }
     }
   };
   load(0);
@@ -270,7 +279,6 @@ __global__ __launch_bounds__(kThreads) void k_state_update_i8(UpdParams p, State
       now[i] = raw[i];
       s_now[i] = s_in[i];
     }
-    // (in place: the rows loaded here are later ones, or the tile's last, whose value is not used)
     if (base + kBatch * kPass < n_rows) load(base + kBatch * kPass);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -319,8 +327,10 @@ void launch_i8(const UpdParams& p, StateI8 st, hipStream_t stream) {
   const int64_t grows = p.hpg * p.P;
   // Large tiles share one quantization of B and C; small ones keep a small batch spread over the GPU.
   st.rows = p.B * p.nh * p.P >= kMaxRows * 2048 ? kMaxRows : 64;
-  st.tiles = (int32_t)cdiv(grows, st.rows);
-  k_state_update_i8<R><<<(unsigned)(p.B * p.Gbc * st.tiles), kThreads, 0, stream>>>(p, st);
+  st.tiles = cdiv(grows, st.rows);
+  // a grid dimension holds fewer than 2^32 threads
+  const int64_t n = p.B * p.Gbc * st.tiles, gx = std::min<int64_t>(n, (int64_t)1 << 23);
+  k_state_update_i8<R><<<dim3((unsigned)gx, (unsigned)cdiv(n, gx)), kThreads, 0, stream>>>(p, st);
 }
 
 template <int R>
@@ -429,8 +439,8 @@ extern "C" qssm_status qssm_state_update_i8(const qssm_update_args* a, const int
   if (qssm_status st = check_rest(a)) return st;
   if ((uintptr_t)state_in % 16 != 0)
     return fail(QSSM_ERR_INVALID_ARG, "state_in must be 16-byte aligned");
-  if (a->batch * a->nheads > ((int64_t)1 << 36) / a->headdim)
-    return fail(QSSM_ERR_UNSUPPORTED, "batch * nheads * headdim above 2^36");  // grid of 64-row tiles
+  if (a->batch * a->nheads > ((int64_t)1 << 38) / a->headdim)
+    return fail(QSSM_ERR_UNSUPPORTED, "batch * nheads * headdim above 2^38");
   const UpdParams p = params_of(a);
   int8_t* out = reinterpret_cast<int8_t*>(a->state);
   const StateI8 st{state_in ? state_in : out, scales_in ? scales_in : state_scales, out, state_scales, 0, 0};

@@ -71,7 +71,8 @@ def gemm(**kw):
     (dict(y_dtype=qs.QSSM_I8), INV, "y_dtype"),
     (dict(K=131072, a_stride=131072, w_stride=131072), UNS, "131071"),
     (dict(a_stride=63), INV, "stride"), (dict(w_stride=63), INV, "stride"), (dict(y_stride=7), INV, "stride"),
-    (dict(a_stride=2 ** 41), UNS, "stride"), (dict(w_stride=2 ** 22 + 64), UNS, "2^22"), (dict(M=2 ** 31), UNS, "2^31"),
+    (dict(a_stride=2 ** 41), UNS, "stride"), (dict(w_stride=2 ** 22 + 64), UNS, "2^22"), (dict(M=2 ** 31), UNS, "2^27"), (dict(N=2 ** 27 + 1, y_stride=2 ** 27 + 1), UNS, "2^27"),
+    (dict(M=2 ** 27, N=2 ** 27, y_stride=2 ** 27), UNS, "M * N"),
     (dict(a=None), INV, "null"), (dict(w=None), INV, "null"), (dict(y=None), INV, "null"),
     (dict(a_scales=None), INV, "null"), (dict(w_scales=None), INV, "null"),
     (dict(y=ctypes.c_void_p(4098)), INV, "aligned")])

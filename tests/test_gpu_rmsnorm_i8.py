@@ -168,3 +168,18 @@ def test_another_stream_and_replay(dev):
         oq, os_, oh = ow.rmsnorm_i8(xk, w, residual=res, residual_dtype=np.float32)
         assert np.array_equal(q.cpu().numpy(), oq) and np.array_equal(sc.cpu().numpy(), os_), k
         assert np.array_equal(ro.cpu().numpy(), oh), k
+
+
+def test_more_rows_than_a_grid_dimension(dev):
+    """2^21 + 3 rows: the grid's second dimension (a dimension holds fewer than 2^32 threads)."""
+    print("\n[rmsnorm 2^21 + 3 rows]", flush=True)
+    import torch
+    import quantized_state_space_amd as qs
+    M, D = 2 ** 21 + 3, 8
+    x = torch.randn(M, D, device=dev)
+    q, sc = torch.full((M, D), -77, dtype=torch.int8, device=dev), torch.full((M,), float("nan"), device=dev)
+    qs.qssm_rmsnorm_i8(qs.rmsnorm_args(x, q, sc))
+    rows = torch.cat([torch.arange(5), torch.arange(M // 2 - 4, M // 2 + 4), torch.arange(2 ** 21 - 4, M)]).to(dev)
+    oq, os_, _ = ow.rmsnorm_i8(x[rows].cpu().numpy())
+    assert np.array_equal(q[rows].cpu().numpy(), oq) and np.array_equal(sc[rows].cpu().numpy(), os_)
+    assert not bool(torch.isnan(sc).any())

@@ -237,3 +237,31 @@ def test_steps_replay_and_drift(dev):
         real = dA * real + (d["delta"].astype(np.float64)[:, :, None] * xh)[..., None] * Bh[:, :, None, :]
         drift = dA * drift + 0.5 * s[..., None] * (1 + 1e-5) + 1e-5 * np.abs(real).max()
         assert np.all(np.abs(q * s[..., None].astype(np.float64) - real) <= drift), k
+
+
+def test_more_tiles_than_a_grid_dimension(dev):
+    """2^23 + 5 sequences of one row each: the grid's second dimension."""
+    print("\n[state_update_i8 2^23 + 5 sequences]", flush=True)
+    import torch
+    import quantized_state_space_amd as qs
+    B, N = 2 ** 23 + 5, 16
+    g = torch.Generator(device=dev).manual_seed(3)
+    rn = lambda *s: torch.randn(*s, generator=g, device=dev)  # noqa: E731
+    x, Bm, Cm = rn(B, 1, 1), rn(B, 1, N), rn(B, 1, N)
+    one = lambda v, n=1: torch.full((n,), v, device=dev)  # noqa: E731
+    delta = torch.rand(B, 1, generator=g, device=dev)
+    codes = torch.randint(-127, 128, (B, 1, 1, N), dtype=torch.int8, generator=g, device=dev)
+    sc = 0.01 + torch.rand(B, 1, 1, generator=g, device=dev)
+    out, s_out, y = torch.empty_like(codes), torch.full_like(sc, float("nan")), torch.empty(B, 1, 1, device=dev)
+    args = qs.update_args(x, torch.zeros(1, dtype=torch.uint8, device=dev), one(0.03), Bm, Cm, one(0.03), one(0.03), N,
+                          delta, one(-0.7), out, y)
+    qs.qssm_state_update_i8(args, s_out, state_in=codes, scales_in=sc)
+    rows = torch.cat([torch.arange(4), torch.arange(2 ** 22 - 2, 2 ** 22 + 2), torch.arange(2 ** 23 - 3, B)]).to(dev)
+    n = lambda t: t[rows].cpu().numpy()  # noqa: E731
+    s3 = np.float32(0.03)
+    xh, Bh, Ch = (ow.quant(n(t), s3) * s3 for t in (x, Bm, Cm))
+    yr, q, s, h = ow.state_update(n(codes), n(sc), xh[:, :, 0][:, :, None], Bh, Ch, n(delta), np.float32([-0.7]))
+    assert np.array_equal(n(out), q) and np.array_equal(n(s_out), s)
+    err = (N + 2) * 2.0 ** -24 * (np.abs(h.astype(np.float64)) * np.abs(Ch[:, :, None, :])).sum(3)
+    assert np.all(np.abs(n(y) - yr) <= err)
+    assert not bool(torch.isnan(s_out).any())
