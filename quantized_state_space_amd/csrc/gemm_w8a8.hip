@@ -99,6 +99,14 @@ __device__ __forceinline__ void wait_vm_lds() {
   fence();
 }
 
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N <= 63, "vmcnt has 6 bits");
+  fence();
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0xF70);
+  fence();
+}
+
 // LDS rows of BK bytes; the 16-byte chunk c of row r is in slot c ^ swizzle(r), which spreads the rows
 // that a 16-byte read serves together over all 64 banks (measured: no conflicts; 4 of 8 cycles of
 // every read without it).
@@ -111,11 +119,15 @@ __device__ __forceinline__ int swizzle(int row) {
 // Tiles of (32 WM TM) x (32 WN TN) shared by WM x WN waves. K runs in steps of BK bytes through NS LDS
 // stages that direct loads fill NS - 1 steps ahead; one barrier per step, placed where every wave has
 // the step's last fragments in registers, so that the last slice's products hide it. Fragments are
-// read a slice of 32 codes ahead, and reads and loads are issued between the products.
+// read AHEAD slices of 32 codes ahead, and reads and loads are issued between the products.
+// AHEAD > 1 (small tiles, whose products are too few to cover an LDS read): the barrier then stands
+// where the fragments pass to the next step, and its step refills the stage before last; it pays with
+// many stages, which leave room for one tile per CU (256 x 4096 x 8192 in 64x64 tiles: 18.4 us with 3
+// stages, 18.0 with 6, 16.4 with 6 and AHEAD 3).
 // Steps of 128 and few stages beat steps of 64 and twice the stages (half the barriers): 256x256 tiles,
 // 16384 x 18560 x 4096: 1069 us (2.33 POPS) and 1128; 128x64 tiles, 256 x 4096 x 8192: 22 and 27.
 // The many-token forms are bound by the power the matrix cores draw: with all operands 0 the same
-// kernel runs a third faster.
+// kernel takes 0.71 of the time (4096 x 4096 x 16384), and its clock under load is 1.4 GHz.
 // The partial step of a K that is no multiple of BK is the first and goes through registers, with
 // zeros past K. Rows past M or N read the last row and are not stored.
 // Tile order: the tiles are cut into 8 contiguous ranges, one per XCD (workgroups are dealt to the
@@ -224,7 +236,7 @@ __device__ __forceinline__ void load_scales(const GemmParams& p, int bn, int64_t
   }
 }
 
-template <int WM, int WN, int TM, int TN, int NS, int BK>
+template <int WM, int WN, int TM, int TN, int NS, int BK, int AHEAD>
 __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
   using G = Tile<WM, WN, TM, TN, NS, BK>;
   constexpr int kLd = G::kNA + G::kNB, kSlots = BK / 16, kSlices = BK / 32;
@@ -277,21 +289,23 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
   for (int mt = 0; mt < TM; ++mt)
 #pragma unroll
     for (int nt = 0; nt < TN; ++nt) acc[mt][nt] = v16i{};
-  v4i fa[2][TM], fb[2][TN];
+  constexpr int kSets = AHEAD == 1 ? 2 : kSlices;
+  v4i fa[kSets][TM], fb[kSets][TN];
   const int slot0 = (kh ^ swizzle<BK>(lane & 31)) * 16;
   const int arow = (wm * TM * 32 + (lane & 31)) * BK, brow = (G::kBM + wn * TN * 32 + (lane & 31)) * BK;
-  // fragments of slice ks of stage st into set ks % 2
+  // fragments of slice ks of stage st into set ks % kSets
   auto frags = [&](int st, int ks) {
     const int8_t* base = sm + st * G::kStage + (slot0 ^ (ks * 32));
 #pragma unroll
-    for (int mt = 0; mt < TM; ++mt) fa[ks & 1][mt] = *reinterpret_cast<const v4i*>(base + arow + mt * 32 * BK);
+    for (int mt = 0; mt < TM; ++mt) fa[ks % kSets][mt] = *reinterpret_cast<const v4i*>(base + arow + mt * 32 * BK);
 #pragma unroll
-    for (int nt = 0; nt < TN; ++nt) fb[ks & 1][nt] = *reinterpret_cast<const v4i*>(base + brow + nt * 32 * BK);
+    for (int nt = 0; nt < TN; ++nt) fb[ks % kSets][nt] = *reinterpret_cast<const v4i*>(base + brow + nt * 32 * BK);
   };
 
+  constexpr int kFirst = AHEAD == 1 ? NS : NS - 1;  // steps issued before the loop
   if (!tail) issue(0, 0);
 #pragma unroll
-  for (int d = 1; d < NS; ++d) issue(d, d);
+  for (int d = 1; d < kFirst; ++d) issue(d, d);
   if (tail) {
 #pragma unroll
     for (int i = 0; i < G::kNA; ++i)
@@ -300,39 +314,46 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
     for (int i = 0; i < G::kNB; ++i)
       *reinterpret_cast<uint4*>(dst_w + i * 1024 + lane * 16) = load16(wbase + woff[i], full * BK + wchk[i], p.K);
   }
-  wait_vm_lds<(NS - 1) * kLd>();
+  wait_vm_lds<(kFirst - 1) * kLd>();
   __builtin_amdgcn_s_barrier();
   fence();
-  frags(0, 0);
+#pragma unroll
+  for (int d = 0; d < AHEAD; ++d) frags(0, d);
   int st = 0;
   constexpr int kMf = TM * TN, kDs = TM + TN;
   for (int s = 0; s < nsteps; ++s) {
     const int nx = st + 1 == NS ? 0 : st + 1;
 #pragma unroll
     for (int ks = 0; ks < kSlices; ++ks) {
-      const bool last = ks == kSlices - 1;
-      if (!last) {
-        frags(st, ks + 1);
-      } else {
-        // every wave has the last fragments of stage st in registers, and step s + 1 has landed
-        wait_vm_lds<(NS - 2) * kLd>();
+      const bool cross = ks == kSlices - AHEAD;  // the next fragments are the next step's first
+      if (cross) {
+        if constexpr (AHEAD == 1) {
+          // every wave has the last fragments of stage st in registers, and step s + 1 has landed
+          wait_vm_lds<(NS - 2) * kLd>();
+        } else {
+          // step s + 1 has landed, and every wave has used all of step s - 1
+          wait_vm<(NS - 3) * kLd>();
+        }
         __builtin_amdgcn_s_barrier();
         fence();
-        frags(nx, 0);
-        issue(s + NS, st);
+      }
+      frags(ks + AHEAD < kSlices ? st : nx, (ks + AHEAD) % kSlices);
+      if (cross) {
+        if constexpr (AHEAD == 1) issue(s + NS, st);
+        else issue(s + NS - 1, st == 0 ? NS - 1 : st - 1);
       }
 #pragma unroll
       for (int mt = 0; mt < TM; ++mt)
 #pragma unroll
         for (int nt = 0; nt < TN; ++nt)
-          acc[mt][nt] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks & 1][nt], fa[ks & 1][mt], acc[mt][nt], 0, 0, 0);
-      // issue order: a product, two fragment reads, ... (last slice: then a product, a load, ...)
+          acc[mt][nt] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks % kSets][nt], fa[ks % kSets][mt], acc[mt][nt], 0, 0, 0);
+      // issue order: a product, two fragment reads, ... (after the barrier: then a product, a load, ...)
 #pragma unroll
       for (int i = 0; i < kDs / 2; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
       }
-      if (last) {
+      if (cross) {
 #pragma unroll
         for (int i = 0; i < kLd; ++i) {
           __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
@@ -631,22 +652,23 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void k_gemm_w8a8_any(GemmParams p)
 
 // ------------------------------------------------------------------------------------------------
 // The form for a shape, by estimated time (us): a tile costs tile + step * (steps of 64 codes of K) of
-// its CU when all CUs are at work, at least tile_alone + step_alone * steps when they are not; the
-// whole at least the bytes at 4.3 TB/s. The constants follow a fit (16 % rms) to 30 shapes of 1 .. 16384
+// its CU when it shares it, tile_alone + step_alone * steps when the last round leaves it alone there;
+// the whole at least the bytes at 4.3 TB/s. The constants follow a fit (16 % rms) to 30 shapes of 1 .. 16384
 // tokens, N = 1024 .. 18560 and K = 128 .. 8192 in every form; they named the fastest form at 27 of them
 // and one within 3 to 14 % of it at the others. Measured, e.g. (256x256 / 256x128 / 128x128 / 128x64 /
 // 64x64 / split 32x32):
-//   64 x 4096 x 8192      69 / 38 / 30 / 21 / 18 / 9.3      256 x 4096 x 8192   72 / 40 / 31 / 22 / 18 / 25
+//   64 x 4096 x 8192      69 / 38 / 30 / 21 / 18 / 9.3      256 x 4096 x 8192   72 / 40 / 31 / 22 / 18 / 25 (deep 64x64: 16.4)
 //   1000 x 1536 x 768     13 / 8.8 / 7.4 / 5.8 / 5.7 / 13   256 x 18560 x 4096  56 / 33 / 47 / 45 / 46 / 88
 //   1024 x 4096 x 4096    40 / 24 / 21 / 24 / 30 / 62       4096 x 4096 x 4096  58 / 66 / 82 / 90 / 111 / 294
-enum Form { TILE256, TILE256X128, TILE128, TILE128X64, TILE64, SPLIT32, FORMS };
+enum Form { TILE256, TILE256X128, TILE128, TILE128X64, TILE64, TILE64DEEP, SPLIT32, FORMS };
 struct Cost {
   int bm, bn, per_cu;
   double tile, step, tile_alone, step_alone;
 };
-constexpr Cost kCost[FORMS] = {{256, 256, 1, 0.0, 0.68, 6.0, 0.591},  {256, 128, 1, 4.31, 0.321, 0.0, 0.0},
-                               {128, 128, 1, 3.93, 0.231, 0.0, 0.0},  {128, 64, 2, 1.48, 0.164, 2.56, 0.156},
-                               {64, 64, 3, 0.87, 0.104, 1.65, 0.111}, {32, 32, 2, 1.26, 0.048, 0.0, 0.0}};
+constexpr Cost kCost[FORMS] = {{256, 256, 1, 0.0, 0.68, 6.0, 0.591},    {256, 128, 1, 4.31, 0.321, 4.31, 0.321},
+                               {128, 128, 1, 3.93, 0.231, 3.93, 0.231}, {128, 64, 2, 1.48, 0.164, 2.56, 0.156},
+                               {64, 64, 3, 0.87, 0.104, 1.65, 0.111},   {64, 64, 1, 1.0, 0.132, 1.0, 0.101},
+                               {32, 32, 2, 1.26, 0.048, 1.26, 0.048}};
 
 // The same for rows at any address (k_gemm_w8a8_any; 64x64 / 128x128 / 256x128): 3 x 1001 x 1501 takes
 // 10 / 19 / 24 us, 777 x 1001 x 1501 14 / 24 / 31, 2000 x 3001 x 2001 55 / 44 / 37, 4096 x 4095 x 4097
@@ -668,10 +690,10 @@ int choose(const GemmParams& p, const Cost* costs, int n) {
     const Cost& c = costs[f];
     const double tiles = (double)cdiv(p.M, c.bm) * (double)cdiv(p.N, c.bn), slots = kCus * c.per_cu;
     if (tiles >= (double)kMaxTiles) continue;
-    const double rounds = std::floor(tiles / slots), rest = tiles - rounds * slots, busy = c.tile + c.step * steps;
-    double t = rounds * c.per_cu * busy;
-    if (rest > 0.0) t += std::max(c.tile_alone + c.step_alone * steps, busy * std::ceil(rest / kCus));
-    t = std::max(t, bytes / 4.3e6);
+    const double busy = c.tile + c.step * steps, alone = c.tile_alone + c.step_alone * steps;
+    const double rounds = std::ceil(tiles / slots) - 1.0, on_cu = std::ceil((tiles - rounds * slots) / kCus);
+    const double last = on_cu <= 1.0 ? alone : std::max(alone, busy * on_cu);
+    const double t = std::max(rounds * c.per_cu * busy + last, bytes / 4.3e6);
     if (best < 0 || t < least) {
       least = t;
       best = f;
@@ -720,11 +742,12 @@ extern "C" qssm_status qssm_gemm_w8a8(const qssm_gemm_w8a8_args* a, hipStream_t 
     return launch_status("gemm_w8a8");
   }
   switch (choose(p, kCost, FORMS)) {
-    case TILE256: k_gemm_w8a8_tile<2, 4, 4, 2, 2, 128><<<grid_of(p, 256, 256), 512, 0, stream>>>(p); break;
-    case TILE256X128: k_gemm_w8a8_tile<4, 2, 2, 2, 3, 128><<<grid_of(p, 256, 128), 512, 0, stream>>>(p); break;
-    case TILE128: k_gemm_w8a8_tile<2, 2, 2, 2, 3, 128><<<grid_of(p, 128, 128), 256, 0, stream>>>(p); break;
-    case TILE128X64: k_gemm_w8a8_tile<2, 2, 2, 1, 3, 128><<<grid_of(p, 128, 64), 256, 0, stream>>>(p); break;
-    case TILE64: k_gemm_w8a8_tile<2, 2, 1, 1, 3, 128><<<grid_of(p, 64, 64), 256, 0, stream>>>(p); break;
+    case TILE256: k_gemm_w8a8_tile<2, 4, 4, 2, 2, 128, 1><<<grid_of(p, 256, 256), 512, 0, stream>>>(p); break;
+    case TILE256X128: k_gemm_w8a8_tile<4, 2, 2, 2, 3, 128, 1><<<grid_of(p, 256, 128), 512, 0, stream>>>(p); break;
+    case TILE128: k_gemm_w8a8_tile<2, 2, 2, 2, 3, 128, 1><<<grid_of(p, 128, 128), 256, 0, stream>>>(p); break;
+    case TILE128X64: k_gemm_w8a8_tile<2, 2, 2, 1, 3, 128, 1><<<grid_of(p, 128, 64), 256, 0, stream>>>(p); break;
+    case TILE64: k_gemm_w8a8_tile<2, 2, 1, 1, 3, 128, 1><<<grid_of(p, 64, 64), 256, 0, stream>>>(p); break;
+    case TILE64DEEP: k_gemm_w8a8_tile<2, 2, 1, 1, 6, 128, 3><<<grid_of(p, 64, 64), 256, 0, stream>>>(p); break;
     default:
       // up to 16 tokens load only 16 of a tile's 32 rows (8 tokens x 18560 x 4096: 18.9 us, 19.9 with all)
       if (M <= 16) k_gemm_w8a8_split<1, 1, 128, 4, 16, 2><<<grid_of(p, 32, 32), 256, 0, stream>>>(p);
