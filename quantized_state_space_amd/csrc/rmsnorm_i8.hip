@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kMaxThreads = 1024;
 constexpr int kMaxWaves = kMaxThreads / 64;
-constexpr int64_t kMaxDimNarrow = 8192;  // VEC = 1: 8 channels per thread
+constexpr int64_t kMaxDimNarrow = 8192;  // VEC = 1: 8 channels per thread (16 with many long rows)
 constexpr int64_t kMaxDimWide = 32768;   // VEC = 8: 4 vectors of 8 per thread
 
 struct NormParams {
@@ -40,64 +40,71 @@ struct NormParams {
   int8_t* q;
 };
 
-// VEC consecutive elements of row data as fp32 (VEC = 8: 16-byte aligned)
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+constexpr int kBufferWord3 = 0x00020000;  // buffer resource word 3 for raw 32-bit access (gfx9)
+
+// Raw buffer over `n` bytes of a row (n = 0: nothing). Loads past them give 0 and stores past them are
+// dropped, so a thread's accesses need no branches and all its loads are in flight together (with a
+// branch around each vector's loads they waited one after the other: 8192 x 5001 fp16, 141 us for 82).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void* p, int64_t byte, int n) {
+  const char* q = reinterpret_cast<const char*>(p) + (p ? byte : 0);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(q), (short)0, p ? n : 0, kBufferWord3);
+}
+
+// VEC consecutive elements (16-byte aligned when VEC = 8) as they lie in memory
 template <int VEC, bool F16>
-__device__ __forceinline__ void load_vec(const void* base, int64_t i, float (&o)[VEC]) {
-  if constexpr (F16) {
-    const __half* p = reinterpret_cast<const __half*>(base) + i;
-    if constexpr (VEC == 8) {
-      const uint4 raw = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const __half2 v = *reinterpret_cast<const __half2*>(&w[k]);
-        o[2 * k] = __low2float(v);
-        o[2 * k + 1] = __high2float(v);
-      }
-    } else {
-      o[0] = __half2float(p[0]);
-    }
+struct Raw {
+  v4i w[VEC == 8 ? (F16 ? 1 : 2) : 1];
+};
+
+template <int VEC, bool F16>
+__device__ __forceinline__ Raw<VEC, F16> load_raw(__amdgpu_buffer_rsrc_t r, int c) {
+  Raw<VEC, F16> o;
+  if constexpr (VEC == 8) {
+    o.w[0] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, c * (F16 ? 2 : 4), 0, 0));
+    if constexpr (!F16) o.w[1] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, c * 4 + 16, 0, 0));
+  } else if constexpr (F16) {
+    o.w[0][0] = (int)(unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, c * 2, 0, 0);
   } else {
-    const float* p = reinterpret_cast<const float*>(base) + i;
-    if constexpr (VEC == 8) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-      o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-      o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+    o.w[0][0] = (int)__builtin_amdgcn_raw_buffer_load_b32(r, c * 4, 0, 0);
+  }
+  return o;
+}
+
+template <int VEC, bool F16>
+__device__ __forceinline__ void to_float(const Raw<VEC, F16>& r, float (&o)[VEC]) {
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) {
+    if constexpr (F16) {
+      const uint32_t w = (uint32_t)r.w[0][k / 2];
+      o[k] = __half2float(__ushort_as_half((unsigned short)(k % 2 ? w >> 16 : w & 0xFFFFu)));
     } else {
-      o[0] = p[0];
+      o[k] = __builtin_bit_cast(float, (int)r.w[k / 4][k % 4]);
     }
   }
 }
 
 // Rounds v to the stream's type and stores it; v becomes the stored value.
 template <int VEC, bool F16>
-__device__ __forceinline__ void round_store(void* base, int64_t i, float (&v)[VEC]) {
+__device__ __forceinline__ void round_store(__amdgpu_buffer_rsrc_t r, int c, float (&v)[VEC]) {
   if constexpr (F16) {
-    __half h[VEC];
+    uint32_t w[(VEC + 1) / 2] = {};
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      h[k] = __float2half_rn(v[k]);
-      v[k] = __half2float(h[k]);
+      const __half h = __float2half_rn(v[k]);
+      v[k] = __half2float(h);
+      w[k / 2] |= (uint32_t)__half_as_ushort(h) << (16 * (k % 2));
     }
-    if (!base) return;
-    __half* p = reinterpret_cast<__half*>(base) + i;
-    if constexpr (VEC == 8) {
-      uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = (uint32_t)__half_as_ushort(h[2 * k]) | ((uint32_t)__half_as_ushort(h[2 * k + 1]) << 16);
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      p[0] = h[0];
-    }
+    if constexpr (VEC == 8) __builtin_amdgcn_raw_buffer_store_b128(v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]}, r, c * 2, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b16((unsigned short)w[0], r, c * 2, 0, 0);
   } else {
-    if (!base) return;
-    float* p = reinterpret_cast<float*>(base) + i;
     if constexpr (VEC == 8) {
-      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      const int* w = reinterpret_cast<const int*>(v);
+      __builtin_amdgcn_raw_buffer_store_b128(v4i{w[0], w[1], w[2], w[3]}, r, c * 4, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(v4i{w[4], w[5], w[6], w[7]}, r, c * 4 + 16, 0, 0);
     } else {
-      p[0] = v[0];
+      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, v[0]), r, c * 4, 0, 0);
     }
   }
 }
@@ -148,31 +155,47 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
   if (row >= p.M) return;  // grid padding (the whole workgroup)
   const int tid = threadIdx.x, T = blockDim.x, lane = tid & 63, wave = tid >> 6, nw = T >> 6;
 
+  constexpr int kXB = XF16 ? 2 : 4, kRB = RES == 1 ? 2 : 4, kZB = GATE == 1 ? 2 : 4;
+  const __amdgpu_buffer_rsrc_t rx = row_rsrc(p.x, row * p.xs * kXB, p.D * kXB);
+  Raw<VEC, XF16> xr[VPT];
+  Raw<VEC, RES == 1> rr[RES ? VPT : 1];
+  Raw<VEC, GATE == 1> zr[GATE ? VPT : 1];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) xr[v] = load_raw<VEC, XF16>(rx, (v * T + tid) * VEC);
+  if constexpr (RES != 0) {
+    const __amdgpu_buffer_rsrc_t r = row_rsrc(p.res, row * p.rs * kRB, p.D * kRB);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) rr[v] = load_raw<VEC, RES == 1>(r, (v * T + tid) * VEC);
+  }
+  if constexpr (GATE != 0) {
+    const __amdgpu_buffer_rsrc_t r = row_rsrc(p.gate, row * p.gs * kZB, p.D * kZB);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) zr[v] = load_raw<VEC, GATE == 1>(r, (v * T + tid) * VEC);
+  }
+
+  // channels past D hold 0 from here on (or NaN after r, which no reduction counts)
   float t[VPT][VEC];
   double sum = 0.0;
+  [[maybe_unused]] const __amdgpu_buffer_rsrc_t ro = row_rsrc(p.res_out, row * p.ros * kRB, p.D * kRB);
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int c = (v * T + tid) * VEC;
+    to_float<VEC, XF16>(xr[v], t[v]);
+    if constexpr (RES != 0) {
+      if (p.res) {
+        float o[VEC];
+        to_float<VEC, RES == 1>(rr[v], o);
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) t[v][k] = 0.0f;
-    if (c < p.D) {
-      load_vec<VEC, XF16>(p.x, row * p.xs + c, t[v]);
-      if constexpr (RES != 0) {
-        if (p.res) {
-          float o[VEC];
-          load_vec<VEC, RES == 1>(p.res, row * p.rs + c, o);
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) t[v][k] += o[k];
-        }
-        // res_out may be res: each element is read above by the thread that writes it here
-        round_store<VEC, RES == 1>(p.res_out, row * p.ros + c, t[v]);
+        for (int k = 0; k < VEC; ++k) t[v][k] += o[k];
       }
-      if constexpr (GATE != 0) {
-        float z[VEC];
-        load_vec<VEC, GATE == 1>(p.gate, row * p.gs + c, z);
+      // res_out may be res: each element was read above by the thread that writes it here
+      round_store<VEC, RES == 1>(ro, c, t[v]);
+    }
+    if constexpr (GATE != 0) {
+      float z[VEC];
+      to_float<VEC, GATE == 1>(zr[v], z);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) t[v][k] *= silu_f64<GATE == 1>(z[k]);
-      }
+      for (int k = 0; k < VEC; ++k) t[v][k] *= silu_f64<GATE == 1>(z[k]);
     }
     double part = 0.0;
 #pragma unroll
@@ -223,25 +246,27 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
     r1 = group_r(a, p.Dg, p.eps);
   }
 
+  const __amdgpu_buffer_rsrc_t rw = row_rsrc(p.w, 0, p.D * 4);
   float amax = 0.0f;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int c = (v * T + tid) * VEC;
-    if (c < p.D) {
-      float r = r1;
-      if (p.Gn > 1) {
-        const int g = p.Dg > 1 ? (int)__umulhi((uint32_t)c, p.inv_dg) : c, per = p.Dg / VEC;
-        r = reinterpret_cast<const float*>(smem)[VEC == 1 ? g * per : 2 * g * per];
-      }
-      float w[VEC];
-      if (p.w) load_vec<VEC, false>(p.w, c, w);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        t[v][k] *= r;
-        if (p.w) t[v][k] *= w[k];
-        amax = fmaxf(amax, fabsf(t[v][k]));  // a NaN does not count
-      }
+    float r = r1;
+    if (p.Gn > 1) {
+      const int cc = min(c, p.D - VEC);  // (past D: any group's)
+      const int g = p.Dg > 1 ? (int)__umulhi((uint32_t)cc, p.inv_dg) : cc, per = p.Dg / VEC;
+      r = reinterpret_cast<const float*>(smem)[VEC == 1 ? g * per : 2 * g * per];
     }
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) t[v][k] *= r;
+    if (p.w) {
+      float w[VEC];
+      to_float<VEC, false>(load_raw<VEC, false>(rw, c), w);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) t[v][k] *= w[k];
+    }
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) amax = fmaxf(amax, fabsf(t[v][k]));  // a NaN does not count
   }
 
   float s;
@@ -264,19 +289,24 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
     s = p.scales[0];
   }
 
+  const __amdgpu_buffer_rsrc_t rq = row_rsrc(p.q, row * p.qs, p.D);
+  if constexpr (VEC == 8) {
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    const int c = (v * T + tid) * VEC;
-    if (c < p.D) {
-      int8_t* o = p.q + row * p.qs + c;
-      if constexpr (VEC == 8) {
-        uint32_t w[2];
-        quant_row<false, 8>(t[v], s, w);
-        *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
-      } else {
-        *o = quant8_r(t[v][0], s, recip_or_zero(s));
-      }
+    for (int v = 0; v < VPT; ++v) {
+      uint32_t w[2];
+      quant_row<false, 8>(t[v], s, w);
+      __builtin_amdgcn_raw_buffer_store_b64(v2i{(int)w[0], (int)w[1]}, rq, (v * T + tid) * 8, 0, 0);
     }
+  } else {
+    constexpr int kN = (VPT + 3) / 4 * 4;
+    float u[kN];
+    uint32_t w[kN / 4];
+#pragma unroll
+    for (int v = 0; v < kN; ++v) u[v] = v < VPT ? t[v < VPT ? v : 0][0] : 0.0f;
+    quant_row<false, kN>(u, s, w);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+      __builtin_amdgcn_raw_buffer_store_b8((unsigned char)(w[v / 4] >> (8 * (v % 4))), rq, v * T + tid, 0, 0);
   }
 }
 
@@ -295,17 +325,25 @@ template <int VEC, bool XF16>
 void launch_vec(const NormParams& p, int res, int gate, hipStream_t st) {
   const int64_t nvec = p.D / VEC;
   // Few rows: as many threads as the row feeds (latency). Many: smaller workgroups, of which more run
-  // at once and cover each other's reductions (16384 x 8192 gated: 218 / 223 / 240 us with up to 256 /
-  // 512 / 1024 threads; 16384 x 4096 with a stream: 137 / 131 / 131; 1111 x 1543: 9.4 / 10.8 / 13.0)
-  const int cap = p.M < 512 ? kMaxThreads : (gate || VEC == 1 ? 256 : 512);
-  const int threads = (int)std::min<int64_t>(cdiv(nvec, 64) * 64, std::max<int64_t>(cap, cdiv(cdiv(nvec, VEC == 8 ? 4 : 8), 64) * 64));
+  // at once and cover each other's reductions. Wide, up to 256 / 512 threads: 16384 x 8192 gated 196 /
+  // 203 us, 16384 x 4096 with a stream 132 / 128. Narrow, up to 64 / 256: 16000 x 130 11.7 / 21.7,
+  // 8192 x 1001 21.9 / 23.8; 8 / 16 channels per thread: 8192 x 5001 fp16 82 / 54, fp32 84 / 71 (with
+  // an fp32 stream 123 / 130), 8192 x 8001 fp16 with a stream 139 / 122, but 1111 x 1543 8.1 / 10.0.
+  const bool few = p.M < 512;
+  const int cap = few ? kMaxThreads : (VEC == 1 ? 64 : gate ? 256 : 512);
+  const int most = VEC == 8 ? 4 : (few || p.D <= 2048 ? 8 : 16);  // vectors per thread
+  const int threads = (int)std::min<int64_t>(cdiv(nvec, 64) * 64, std::max<int64_t>(cap, cdiv(cdiv(nvec, most), 64) * 64));
   const int64_t vpt = cdiv(nvec, threads);
   // a grid dimension holds fewer than 2^32 threads
   const int64_t gx = std::min<int64_t>(p.M, (int64_t)1 << 21);
   const dim3 grid((unsigned)gx, (unsigned)cdiv(p.M, gx));
-  if (vpt == 1) launch_vpt<VEC, 1, XF16>(p, res, gate, grid, threads, st);
-  else if (VEC == 8 && vpt == 2) launch_vpt<VEC, 2, XF16>(p, res, gate, grid, threads, st);
-  else launch_vpt<VEC, VEC == 8 ? 4 : 8, XF16>(p, res, gate, grid, threads, st);
+  if (vpt == 1) return launch_vpt<VEC, 1, XF16>(p, res, gate, grid, threads, st);
+  if (vpt == 2) return launch_vpt<VEC, 2, XF16>(p, res, gate, grid, threads, st);
+  if (vpt <= 4) return launch_vpt<VEC, 4, XF16>(p, res, gate, grid, threads, st);
+  if constexpr (VEC == 1) {
+    if (vpt <= 8) return launch_vpt<VEC, 8, XF16>(p, res, gate, grid, threads, st);
+    launch_vpt<VEC, 16, XF16>(p, res, gate, grid, threads, st);
+  }
 }
 
 bool dtype_ok(int32_t t) { return t == QSSM_F32 || t == QSSM_F16; }

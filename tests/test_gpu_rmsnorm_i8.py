@@ -91,6 +91,23 @@ def test_against_oracle(dev, M, D, groups, xt, rt, gt, static, pad):
     check(dev, *make(M * 31 + D, M, D, xt, rt, gt), groups=groups, static=static, pad=pad)
 
 
+@pytest.mark.parametrize("M,D,groups,xt,rt,gt,static,pad", [
+    (512, 5001, 1, "f16", None, None, None, 0),
+    (515, 8191, 1, "f32", "f32", None, None, 1),
+    (513, 2050, 2, "f16", None, "f32", None, 0),
+    (600, 2048, 64, "f32", None, "f16", None, 3),
+    (700, 130, 1, "f16", "f32", None, 0.05, 0),
+    (1000, 1001, 7, "f32", "f16", None, None, 0),
+    (520, 8192, 8, "f16", None, "f16", None, 0),
+    (520, 4104, 1, "f16", "f32", None, None, 8),
+    (530, 24576, 1, "f32", None, "f32", None, 0),
+])
+def test_many_rows(dev, M, D, groups, xt, rt, gt, static, pad):
+    """The launch shapes taken from 512 rows on."""
+    print(f"\n[rmsnorm M={M} D={D} groups={groups} x={xt} residual={rt} gate={gt} static={static} pad={pad}]", flush=True)
+    check(dev, *make(M * 31 + D, M, D, xt, rt, gt), groups=groups, static=static, pad=pad)
+
+
 def test_stream_in_place_and_absent(dev):
     print("\n[rmsnorm residual in place, without an output, starting from x, no weight]", flush=True)
     import torch
