@@ -173,6 +173,13 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
     for (int v = 0; v < VPT; ++v) zr[v] = load_raw<VEC, GATE == 1>(r, (v * T + tid) * VEC);
   }
 
+  // the weight too, ahead of the reduction: 8192 x 5001 with an fp32 stream 129 -> 113 us, 1111 x 1543
+  // 8.1 -> 7.3, aligned rows alike
+  const __amdgpu_buffer_rsrc_t rw = row_rsrc(p.w, 0, p.D * 4);
+  Raw<VEC, false> wr[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) wr[v] = load_raw<VEC, false>(rw, (v * T + tid) * VEC);
+
   // channels past D hold 0 from here on (or NaN after r, which no reduction counts)
   float t[VPT][VEC];
   double sum = 0.0;
@@ -246,7 +253,6 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
     r1 = group_r(a, p.Dg, p.eps);
   }
 
-  const __amdgpu_buffer_rsrc_t rw = row_rsrc(p.w, 0, p.D * 4);
   float amax = 0.0f;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
@@ -261,7 +267,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
     for (int k = 0; k < VEC; ++k) t[v][k] *= r;
     if (p.w) {
       float w[VEC];
-      to_float<VEC, false>(load_raw<VEC, false>(rw, c), w);
+      to_float<VEC, false>(wr[v], w);
 #pragma unroll
       for (int k = 0; k < VEC; ++k) t[v][k] *= w[k];
     }
