@@ -465,7 +465,8 @@ qssm_status qssm_state_update_i8(const qssm_update_args* a, const int8_t* state_
  * x and residual are fp32 or fp16, the gate too; rows of each tensor lie `*_stride` elements apart
  * (>= D), so a slice of a wider tensor's columns can be given.
  * Supported: D <= 8192; up to 32768 when D / norm_groups is a multiple of 8, every stride a multiple
- * of 8, q 8-byte aligned and the other tensors 16-byte aligned (the form with wide loads).
+ * of 8, q 8-byte aligned and the other tensors 16-byte aligned (the form with wide loads). Every tensor
+ * is aligned to its type, and q overlaps no input.
  */
 typedef struct qssm_rmsnorm_args {
   int64_t rows, dim;

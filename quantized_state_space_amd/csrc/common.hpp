@@ -150,7 +150,7 @@ __device__ __forceinline__ float finite_abs(float v) {
 // multiply-add leaves c = RNE(v r) in the low bits of m. c is the nearest code when the remainder
 // e = v - c s is inside (-s/2, s/2): the fma rounds it once, rounding is monotone and s/2 is a
 // float, so |e| < s/2 after rounding implies it before. That fails only within ~2^-16 of a
-// half-integer (or for a NaN); a wave with such a lane decides all its codes by quant8_r. Values are
+// half-integer (or for a NaN); a lane with such a value decides all its codes by quant8_r. Values are
 // clamped to [-128 s, 127 s] first (fl(127 s) / s still rounds to 127). IN_RANGE: the caller knows
 // that every value is finite and |v| <= 127.4 s, as with the scale of the row's own absmax.
 template <bool IN_RANGE, int N>

@@ -395,6 +395,11 @@ extern "C" qssm_status qssm_rmsnorm_i8(const qssm_rmsnorm_args* a, hipStream_t s
     return fail(QSSM_ERR_UNSUPPORTED, "dim above 8192 (32768 with aligned rows and groups)");
   if (M == 0) return QSSM_OK;
   if (!a->x || !a->scales || !a->q) return fail(QSSM_ERR_INVALID_ARG, "null required pointer");
+  const auto off_type = [](const void* t, int32_t type) { return (uintptr_t)t % (type == QSSM_F16 ? 2 : 4) != 0; };
+  if (off_type(a->x, a->x_dtype) || off_type(a->weight, QSSM_F32) || off_type(a->scales, QSSM_F32) ||
+      (stream_on && (off_type(a->residual, a->residual_dtype) || off_type(a->residual_out, a->residual_dtype))) ||
+      (a->gate && off_type(a->gate, a->gate_dtype)))
+    return fail(QSSM_ERR_INVALID_ARG, "a tensor is not aligned to its type");
   NormParams p{M, (int32_t)D, (int32_t)Dg, a->norm_groups, a->compute_scales != 0,
                Dg > 1 ? (uint32_t)((((uint64_t)1 << 32) + Dg - 1) / Dg) : 0u, a->x, a->residual, a->residual_out,
                a->gate, a->x_stride, a->residual_stride, a->residual_out_stride, a->gate_stride,

@@ -159,6 +159,14 @@ __global__ __launch_bounds__(kThreads) void k_state_dequant(const int8_t* codes,
   }
 }
 
+// The pointers of a call with rows: none null, the values and the scales aligned to their types.
+qssm_status check_tensors(const void* values, int32_t dtype, const int8_t* codes, const float* scales) {
+  if (!values || !codes || !scales) return fail(QSSM_ERR_INVALID_ARG, "null required pointer");
+  if ((uintptr_t)values % (dtype == QSSM_F16 ? 2 : 4) != 0 || (uintptr_t)scales % 4 != 0)
+    return fail(QSSM_ERR_INVALID_ARG, "a tensor is not aligned to its type");
+  return QSSM_OK;
+}
+
 qssm_status check(int32_t dtype, int64_t rows, int64_t N) {
   if (dtype != QSSM_F32 && dtype != QSSM_F16)
     return fail(QSSM_ERR_INVALID_ARG, "the values must be QSSM_F32 or QSSM_F16");
@@ -205,7 +213,7 @@ extern "C" qssm_status qssm_state_quant(const void* h, int32_t h_dtype, int64_t 
   clear_error();
   if (qssm_status st = check(h_dtype, rows, N)) return st;
   if (rows == 0) return QSSM_OK;
-  if (!h || !codes || !scales) return fail(QSSM_ERR_INVALID_ARG, "null required pointer");
+  if (qssm_status st = check_tensors(h, h_dtype, codes, scales)) return st;
   const bool f16 = h_dtype == QSSM_F16;
   if (const int L = lanes_of(rows, N, h, h_dtype, codes)) {
     with_lanes(L, [&](auto l) {
@@ -226,7 +234,7 @@ extern "C" qssm_status qssm_state_dequant(const int8_t* codes, const float* scal
   clear_error();
   if (qssm_status st = check(out_dtype, rows, N)) return st;
   if (rows == 0) return QSSM_OK;
-  if (!codes || !scales || !out) return fail(QSSM_ERR_INVALID_ARG, "null required pointer");
+  if (qssm_status st = check_tensors(out, out_dtype, codes, scales)) return st;
   const bool f16 = out_dtype == QSSM_F16;
   if (const int L = lanes_of(rows, N, out, out_dtype, codes)) {
     with_lanes(L, [&](auto l) {

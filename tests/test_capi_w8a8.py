@@ -46,6 +46,23 @@ def test_norm_refusals(kw, status, word):
     assert word in message()
 
 
+@pytest.mark.parametrize("kw", [
+    dict(x=ctypes.c_void_p(4098)), dict(x=ctypes.c_void_p(4097), x_dtype=qs.QSSM_F16),
+    dict(residual=ctypes.c_void_p(4098), residual_stride=64), dict(weight=ctypes.c_void_p(4097)),
+    dict(residual_out=ctypes.c_void_p(4097), residual_dtype=qs.QSSM_F16, residual_out_stride=64),
+    dict(gate=ctypes.c_void_p(4098), gate_stride=64), dict(scales=ctypes.c_void_p(4098))])
+def test_norm_refuses_misaligned_tensors(kw):
+    assert norm(**kw) == INV
+    assert "aligned" in message()
+
+
+def test_state_rows_refuse_misaligned_tensors():
+    lib, odd, half = qs.load(), ctypes.c_void_p(4097), ctypes.c_void_p(4098)
+    for h, t, s in ((half, qs.QSSM_F32, P), (odd, qs.QSSM_F16, P), (P, qs.QSSM_F16, half)):
+        assert lib.qssm_state_quant(h, t, 4, 16, P, s, None) == INV and "aligned" in message()
+        assert lib.qssm_state_dequant(P, s, 4, 16, h, t, None) == INV and "aligned" in message()
+
+
 def test_empty_calls_launch_nothing():
     lib = qs.load()
     assert norm(rows=0, x=None, q=None, scales=None) == qs.QSSM_OK
@@ -104,6 +121,15 @@ def test_state_update_i8_refusals(kw, status, word):
     assert word in message()
     lib = qs.load()
     assert lib.qssm_state_update_i8(None, None, None, None, None) == INV
+
+
+def test_state_update_i8_refuses_partly_overlapping_states():
+    """16 rows of 16 codes: 256 bytes of codes and 64 of scales."""
+    at = ctypes.c_void_p
+    for off in (-240, -16, 16, 240):
+        assert update(state_in=at(4096 + off), scales_in=P) == INV and "overlap" in message()
+    for off in (-60, -4, 4, 60):
+        assert update(state_in=P, scales_in=at(4096 + off)) == INV and "overlap" in message()
 
 
 def test_fp_update_still_refuses_an_int8_state():

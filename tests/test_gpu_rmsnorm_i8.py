@@ -108,6 +108,23 @@ def test_many_rows(dev, M, D, groups, xt, rt, gt, static, pad):
     check(dev, *make(M * 31 + D, M, D, xt, rt, gt), groups=groups, static=static, pad=pad)
 
 
+@pytest.mark.parametrize("D,rt", [(1001, "f16"), (1001, "f32"), (1000, "f16")])
+def test_columns_behind_the_stream_are_left(dev, D, rt):
+    """residual_out as a slice of a wider tensor, whose other columns keep what they hold."""
+    print(f"\n[rmsnorm residual_out in a wider tensor D={D} residual={rt}]", flush=True)
+    import torch
+    import quantized_state_space_amd as qs
+    x, w, res, _ = make(8, 600, D, "f16", rt, None)
+    wide = torch.full((600, 1008), -7.0, dtype=torch.from_numpy(res).dtype, device=dev)
+    q, sc = torch.empty(600, D, dtype=torch.int8, device=dev), torch.empty(600, device=dev)
+    qs.qssm_rmsnorm_i8(qs.rmsnorm_args(to(x, dev), q, sc, weight=to(w, dev), residual=to(res, dev),
+                                       residual_out=wide[:, :D]))
+    oq, os_, oh = ow.rmsnorm_i8(x, w, residual=res, residual_dtype=res.dtype)
+    assert np.array_equal(q.cpu().numpy(), oq) and np.array_equal(sc.cpu().numpy(), os_)
+    assert np.array_equal(wide[:, :D].cpu().numpy(), oh)
+    assert bool((wide[:, D:] == -7.0).all())
+
+
 def test_stream_in_place_and_absent(dev):
     print("\n[rmsnorm residual in place, without an output, starting from x, no weight]", flush=True)
     import torch
