@@ -7,8 +7,8 @@
 // wave holds row (or column) l % 32 and the 16 consecutive k at 16 (l / 32). The weights go in as the
 // first operand, so a lane ends with one token and groups of 4 consecutive output channels.
 //
-// Tiles shared by a workgroup's waves with K in common steps (k_gemm_w8a8_tile, and k_gemm_w8a8_any for
-// rows at any address), and the smallest tiles with K split over the waves (k_gemm_w8a8_split: few tokens,
+// Tiles shared by a workgroup's waves with K in common steps (k_gemm_w8a8_tile, with a variant for rows
+// at any address), and the smallest tiles with K split over the waves (k_gemm_w8a8_split: few tokens,
 // bound by the bytes of the weights and by latency). choose() picks by estimated time.
 #include <hip/hip_runtime.h>
 
@@ -51,27 +51,32 @@ __device__ __forceinline__ void put(const GemmParams& p, int64_t m, int64_t n, f
   else reinterpret_cast<float*>(p.y)[m * p.ys + n] = v;
 }
 
-// 16 consecutive codes of a row from k on, at any alignment (the hardware takes unaligned 16-byte
-// loads); codes at or past K read as 0 without touching memory. A row's last, partial chunk is the
-// end of its last 16 codes (byte by byte, a load and a wait each, it took half of the 19 us of
-// 777 x 1001 x 1500); only rows shorter than 16 are read by bytes.
+// 16 consecutive codes of a row of K from k on, at any alignment (the hardware takes unaligned 16-byte
+// loads); codes at or past K are 0 and not read. A chunk that reaches past K is the end of the row's last
+// 16 codes, shifted into place without a branch, so that a thread's loads are in flight together; K >= 16
+// (load16_short: any K, byte by byte, a load and a wait each).
 __device__ __forceinline__ uint4 load16(const int8_t* row, int64_t k, int64_t K) {
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (k + 16 <= K) {
-    __builtin_memcpy(&v, row + k, 16);
-  } else if (k < K && K >= 16) {
-    unsigned __int128 t;
-    __builtin_memcpy(&t, row + K - 16, 16);
-    t >>= 8 * (int)(k + 16 - K);
-    __builtin_memcpy(&v, &t, 16);
-  } else if (k < K) {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
+  const int64_t at = min(k, K - 16);
+  uint32_t w[4];
+  __builtin_memcpy(w, row + at, 16);
+  const int n = (int)min(k - at, (int64_t)16);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (k + i < K) w[i / 4] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i % 4));
-    v = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  return v;
+  for (int i = 0; i < 4; ++i) w[i] = (n & 16) ? 0u : w[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (n & 8) ? (i < 2 ? w[(i + 2) & 3] : 0u) : w[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (n & 4) ? (i < 3 ? w[(i + 1) & 3] : 0u) : w[i];
+  const uint32_t b = n & 3;
+  return make_uint4(__builtin_amdgcn_alignbyte(w[1], w[0], b), __builtin_amdgcn_alignbyte(w[2], w[1], b),
+                    __builtin_amdgcn_alignbyte(w[3], w[2], b), __builtin_amdgcn_alignbyte(0u, w[3], b));
+}
+
+__device__ __forceinline__ uint4 load16_short(const int8_t* row, int64_t k, int64_t K) {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (k + i < K) w[i / 4] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i % 4));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
@@ -82,8 +87,19 @@ __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, int8_t* dst, 
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)dst, 16, voff, soff, 0, 0);
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const int8_t* p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p), (short)0, 0x7fffffff, kBufferWord3);
+// 4 bytes per lane, at dst + 4 lane
+__device__ __forceinline__ void load_lds_word(__amdgpu_buffer_rsrc_t r, int8_t* dst, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)dst, 4, voff, soff, 0, 0);
+}
+
+// The 16 codes from byte sh on of v and the word behind it.
+__device__ __forceinline__ v4i shifted(const v4i& v, uint32_t next, uint32_t sh) {
+  return v4i{(int)__builtin_amdgcn_alignbyte(v[1], v[0], sh), (int)__builtin_amdgcn_alignbyte(v[2], v[1], sh),
+             (int)__builtin_amdgcn_alignbyte(v[3], v[2], sh), (int)__builtin_amdgcn_alignbyte(next, v[3], sh)};
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const int8_t* p, int bytes = 0x7fffffff) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p), (short)0, bytes, kBufferWord3);
 }
 
 // Keeps the compiler's LDS accesses on their side (the direct loads are not its accesses).
@@ -107,13 +123,10 @@ __device__ __forceinline__ void wait_vm() {
   fence();
 }
 
-// LDS rows of BK bytes; the 16-byte chunk c of row r is in slot c ^ swizzle(r), which spreads the rows
+// LDS rows of 128 bytes; the 16-byte chunk c of row r is in slot c ^ swizzle(r), which spreads the rows
 // that a 16-byte read serves together over all 64 banks (measured: no conflicts; 4 of 8 cycles of
 // every read without it).
-template <int BK>
-__device__ __forceinline__ int swizzle(int row) {
-  return BK == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
-}
+__device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
 
 // ------------------------------------------------------------------------------------------------
 // Tiles of (32 WM TM) x (32 WN TN) shared by WM x WN waves. K runs in steps of BK bytes through NS LDS
@@ -133,13 +146,19 @@ __device__ __forceinline__ int swizzle(int row) {
 // Tile order: the tiles are cut into 8 contiguous ranges, one per XCD (workgroups are dealt to the
 // XCDs in turn), in groups of 4 row tiles, so the workgroups that run together on an XCD share rows
 // and columns in its L2 (16384 x 18560 x 4096: groups of 4 / 8 / 16 took 1151 / 1161 / 1195 us).
+// SHIFT: rows at any address, K of any length. Direct loads take multiples of 4 bytes, so a row lies in
+// LDS from the word on that holds its first code, 0 to 3 codes late, with the word behind each step's
+// BK bytes beside the stage; a fragment is its 16 bytes and the next word shifted into place (the sums
+// pair codes of the same k). 4096 x 4095 x 4097, fp32 y: 93 us, 77 with K = 4100 and no shift; fp16 y: 88, and 123
+// with the operands through registers in place of direct loads (16384 x 9001 x 4001: 762 and 1048).
 // Output: each wave scales its sums and turns 32 rows at a time through LDS into whole-row stores
 // (stores straight from the registers took 23 us a tile, a third of the whole at K = 4096).
-template <int WM, int WN, int TM, int TN, int NS, int BK>
+template <int WM, int WN, int TM, int TN, int NS, int BK, bool SHIFT = false>
 struct Tile {
   static constexpr int kWaves = WM * WN, kBM = WM * TM * 32, kBN = WN * TN * 32, kRpl = 1024 / BK;
   static constexpr int kNA = kBM / kRpl / kWaves, kNB = kBN / kRpl / kWaves;  // loads of a wave, kRpl rows each
-  static constexpr int kStage = (kBM + kBN) * BK;
+  static constexpr int kRows = kBM + kBN, kStage = kRows * (BK + (SHIFT ? 4 : 0));
+  static constexpr int kNX = SHIFT ? (kRows / 64 + kWaves - 1) / kWaves : 0;  // loads of next words, 64 rows each
 };
 
 __device__ __forceinline__ void to_type(float v, __half& o) { o = __float2half_rn(v); }
@@ -236,10 +255,10 @@ __device__ __forceinline__ void load_scales(const GemmParams& p, int bn, int64_t
   }
 }
 
-template <int WM, int WN, int TM, int TN, int NS, int BK, int AHEAD>
+template <int WM, int WN, int TM, int TN, int NS, int BK, int AHEAD, bool SHIFT>
 __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
-  using G = Tile<WM, WN, TM, TN, NS, BK>;
-  constexpr int kLd = G::kNA + G::kNB, kSlots = BK / 16, kSlices = BK / 32;
+  using G = Tile<WM, WN, TM, TN, NS, BK, SHIFT>;
+  constexpr int kLd = G::kNA + G::kNB + G::kNX, kSlots = BK / 16, kSlices = BK / 32;
   static_assert(WM * WN * 32 * (TN * 32 * 4 + 16) <= NS * G::kStage, "the output buffers fit the stages");
   // one array: with several the compiler waits for all direct loads before every LDS read
   __shared__ __align__(1024) int8_t sm[NS * G::kStage + 8 * G::kBN];
@@ -253,35 +272,62 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
   float sa[TM];
   load_scales<TM>(p, G::kBN, m0 + wm * TM * 32, n0, lane, tid, G::kWaves * 64, s_sw, s_bias, sa);
   // load i of this wave: kRpl rows, lane l at row l / kSlots, slot l % kSlots (32-bit offsets: host)
+  // (SHIFT: from the word that holds the row's first code on)
   const int8_t* abase = p.a + m0 * p.as;
   const int8_t* wbase = p.w + n0 * p.ws;
+  const int apre = SHIFT ? (int)((uintptr_t)abase & 3) : 0, wpre = SHIFT ? (int)((uintptr_t)wbase & 3) : 0;
+  abase -= apre;
+  wbase -= wpre;
+  constexpr int kWord = SHIFT ? ~3 : ~0;
+  const int alast = (int)min(p.M - 1 - m0, (int64_t)G::kBM), wlast = (int)min(p.N - 1 - n0, (int64_t)G::kBN);
+  const int as = (int)p.as, ws = (int)p.ws;
+  const auto a_at = [&](int row) { return min(row, alast) * as + apre; };
+  const auto w_at = [&](int row) { return min(row, wlast) * ws + wpre; };
   const int lrow = lane / kSlots;
   int aoff[G::kNA], woff[G::kNB], achk[G::kNA], wchk[G::kNB];
+  uint32_t atail[G::kNA], wtail[G::kNB];  // codes before the row's first
 #pragma unroll
   for (int i = 0; i < G::kNA; ++i) {
     const int row = (wave * G::kNA + i) * G::kRpl + lrow;
-    achk[i] = ((lane % kSlots) ^ swizzle<BK>(row)) * 16;
-    aoff[i] = (int)(min((int64_t)row, p.M - 1 - m0) * p.as);
+    achk[i] = ((lane % kSlots) ^ swizzle(row)) * 16;
+    aoff[i] = a_at(row) & kWord;
+    atail[i] = a_at(row) & ~kWord;
   }
 #pragma unroll
   for (int i = 0; i < G::kNB; ++i) {
     const int row = (wave * G::kNB + i) * G::kRpl + lrow;
-    wchk[i] = ((lane % kSlots) ^ swizzle<BK>(row)) * 16;
-    woff[i] = (int)(min((int64_t)row, p.N - 1 - n0) * p.ws);
+    wchk[i] = ((lane % kSlots) ^ swizzle(row)) * 16;
+    woff[i] = w_at(row) & kWord;
+    wtail[i] = w_at(row) & ~kWord;
   }
-  const __amdgpu_buffer_rsrc_t ra = rsrc_of(abase), rw = rsrc_of(wbase);
-  const int full = (int)(p.K / BK), tail = (int)(p.K % BK) != 0;  // host: full >= 1
+  // SHIFT: the word behind each row's BK bytes of a step; of rows that need none, the last one before
+  int xoff[G::kNX + 1], xrow[G::kNX + 1];
+  uint32_t xsh[G::kNX + 1];
+#pragma unroll
+  for (int i = 0; i < G::kNX; ++i) {
+    xrow[i] = (wave * G::kNX + i) % (G::kRows / 64) * 64;
+    const int row = xrow[i] + lane, at = xrow[i] < G::kBM ? a_at(row) : w_at(row - G::kBM);
+    xsh[i] = at & 3;
+    xoff[i] = (at & ~3) + BK - (xsh[i] ? 0 : 4);
+  }
+  const int full = (int)(p.K / BK), tail = (int)(p.K % BK) != 0;  // host: full >= 1 without SHIFT
+  // without a full step every direct load is out of range: it reads nothing
+  const int bytes = SHIFT && full == 0 ? 0 : 0x7fffffff;
+  const __amdgpu_buffer_rsrc_t ra = rsrc_of(abase, bytes), rw = rsrc_of(wbase, bytes);
   const int nsteps = full + tail;
   int8_t* dst_a = sm + wave * G::kNA * 1024;
   int8_t* dst_w = sm + G::kBM * BK + wave * G::kNB * 1024;
 
   // step s into stage st; past the last step the last one again, so that the waits stay exact
   auto issue = [&](int s, int st) {
-    const int koff = (min(s, nsteps - 1) - tail) * BK;
+    const int koff = (SHIFT ? max(min(s, nsteps - 1) - tail, 0) : min(s, nsteps - 1) - tail) * BK;
 #pragma unroll
     for (int i = 0; i < G::kNA; ++i) load_lds(ra, dst_a + st * G::kStage + i * 1024, aoff[i] + achk[i], koff);
 #pragma unroll
     for (int i = 0; i < G::kNB; ++i) load_lds(rw, dst_w + st * G::kStage + i * 1024, woff[i] + wchk[i], koff);
+#pragma unroll
+    for (int i = 0; i < G::kNX; ++i)
+      load_lds_word(xrow[i] < G::kBM ? ra : rw, sm + st * G::kStage + G::kRows * BK + xrow[i] * 4, xoff[i], koff);
   };
 
   v16i acc[TM][TN];
@@ -291,8 +337,15 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
     for (int nt = 0; nt < TN; ++nt) acc[mt][nt] = v16i{};
   constexpr int kSets = AHEAD == 1 ? 2 : kSlices;
   v4i fa[kSets][TM], fb[kSets][TN];
-  const int slot0 = (kh ^ swizzle<BK>(lane & 31)) * 16;
+  const int slot0 = (kh ^ swizzle(lane & 31)) * 16;
   const int arow = (wm * TM * 32 + (lane & 31)) * BK, brow = (G::kBM + wn * TN * 32 + (lane & 31)) * BK;
+  [[maybe_unused]] uint32_t na[kSets][TM], nb[kSets][TN], sha[TM], shb[TN];
+  if constexpr (SHIFT) {
+#pragma unroll
+    for (int mt = 0; mt < TM; ++mt) sha[mt] = a_at((wm * TM + mt) * 32 + (lane & 31)) & 3;
+#pragma unroll
+    for (int nt = 0; nt < TN; ++nt) shb[nt] = w_at((wn * TN + nt) * 32 + (lane & 31)) & 3;
+  }
   // fragments of slice ks of stage st into set ks % kSets
   auto frags = [&](int st, int ks) {
     const int8_t* base = sm + st * G::kStage + (slot0 ^ (ks * 32));
@@ -300,6 +353,22 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
     for (int mt = 0; mt < TM; ++mt) fa[ks % kSets][mt] = *reinterpret_cast<const v4i*>(base + arow + mt * 32 * BK);
 #pragma unroll
     for (int nt = 0; nt < TN; ++nt) fb[ks % kSets][nt] = *reinterpret_cast<const v4i*>(base + brow + nt * 32 * BK);
+    if constexpr (SHIFT) {
+      // the word behind the fragment: the next chunk's first, or behind the last chunk the row's next word
+      const bool last = ks == kSlices - 1;
+      const int chunk = 2 * ks + kh + 1, slot = (chunk ^ swizzle(lane & 31)) * 16;
+      const int8_t* stage = sm + st * G::kStage;
+#pragma unroll
+      for (int mt = 0; mt < TM; ++mt) {
+        const int in = arow + mt * 32 * BK + slot, behind = G::kRows * BK + (wm * TM * 32 + mt * 32 + (lane & 31)) * 4;
+        na[ks % kSets][mt] = *reinterpret_cast<const uint32_t*>(stage + (last && kh ? behind : in));
+      }
+#pragma unroll
+      for (int nt = 0; nt < TN; ++nt) {
+        const int in = brow + nt * 32 * BK + slot, behind = G::kRows * BK + (G::kBM + wn * TN * 32 + nt * 32 + (lane & 31)) * 4;
+        nb[ks % kSets][nt] = *reinterpret_cast<const uint32_t*>(stage + (last && kh ? behind : in));
+      }
+    }
   };
 
   constexpr int kFirst = AHEAD == 1 ? NS : NS - 1;  // steps issued before the loop
@@ -307,12 +376,34 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
 #pragma unroll
   for (int d = 1; d < kFirst; ++d) issue(d, d);
   if (tail) {
+    uint4 va[G::kNA], vw[G::kNB];
+    // at most three codes lie behind the step, in a word that holds codes (else the row's first word)
+    uint32_t xw[G::kNX + 1];
+    int xleft[G::kNX + 1];
 #pragma unroll
-    for (int i = 0; i < G::kNA; ++i)
-      *reinterpret_cast<uint4*>(dst_a + i * 1024 + lane * 16) = load16(abase + aoff[i], full * BK + achk[i], p.K);
+    for (int i = 0; i < G::kNX; ++i) {
+      xleft[i] = (int)(p.K + xsh[i]) - (full + 1) * BK;
+      const int first = xoff[i] - BK + (xsh[i] ? 0 : 4), at = xleft[i] > 0 ? xoff[i] + full * BK : first;
+      xw[i] = *reinterpret_cast<const uint32_t*>((xrow[i] < G::kBM ? abase : wbase) + at);
+    }
+    if (!SHIFT || p.K >= 16) {
 #pragma unroll
-    for (int i = 0; i < G::kNB; ++i)
-      *reinterpret_cast<uint4*>(dst_w + i * 1024 + lane * 16) = load16(wbase + woff[i], full * BK + wchk[i], p.K);
+      for (int i = 0; i < G::kNA; ++i) va[i] = load16(abase + aoff[i], full * BK + achk[i], p.K + atail[i]);
+#pragma unroll
+      for (int i = 0; i < G::kNB; ++i) vw[i] = load16(wbase + woff[i], full * BK + wchk[i], p.K + wtail[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < G::kNA; ++i) va[i] = load16_short(abase + aoff[i], achk[i], p.K + atail[i]);
+#pragma unroll
+      for (int i = 0; i < G::kNB; ++i) vw[i] = load16_short(wbase + woff[i], wchk[i], p.K + wtail[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < G::kNA; ++i) *reinterpret_cast<uint4*>(dst_a + i * 1024 + lane * 16) = va[i];
+#pragma unroll
+    for (int i = 0; i < G::kNB; ++i) *reinterpret_cast<uint4*>(dst_w + i * 1024 + lane * 16) = vw[i];
+#pragma unroll
+    for (int i = 0; i < G::kNX; ++i)
+      *reinterpret_cast<uint32_t*>(sm + G::kRows * BK + (xrow[i] + lane) * 4) = xleft[i] > 0 ? xw[i] & ((1u << (8 * xleft[i])) - 1u) : 0u;
   }
   wait_vm_lds<(kFirst - 1) * kLd>();
   __builtin_amdgcn_s_barrier();
@@ -342,6 +433,12 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
         if constexpr (AHEAD == 1) issue(s + NS, st);
         else issue(s + NS - 1, st == 0 ? NS - 1 : st - 1);
       }
+      if constexpr (SHIFT) {
+#pragma unroll
+        for (int mt = 0; mt < TM; ++mt) fa[ks % kSets][mt] = shifted(fa[ks % kSets][mt], na[ks % kSets][mt], sha[mt]);
+#pragma unroll
+        for (int nt = 0; nt < TN; ++nt) fb[ks % kSets][nt] = shifted(fb[ks % kSets][nt], nb[ks % kSets][nt], shb[nt]);
+      }
 #pragma unroll
       for (int mt = 0; mt < TM; ++mt)
 #pragma unroll
@@ -351,7 +448,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
 #pragma unroll
       for (int i = 0; i < kDs / 2; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, SHIFT ? 4 : 2, 0);
       }
       if (cross) {
 #pragma unroll
@@ -405,13 +502,13 @@ __global__ __launch_bounds__(W * 64, 2) void k_gemm_w8a8_split(GemmParams p) {
 #pragma unroll
   for (int i = 0; i < G::kNA; ++i) {
     const int row = i * G::kRpl + lrow;
-    achk[i] = ((lane % kSlots) ^ swizzle<BK>(row)) * 16;
+    achk[i] = ((lane % kSlots) ^ swizzle(row)) * 16;
     aoff[i] = (int)(min((int64_t)row, p.M - 1 - m0) * p.as);
   }
 #pragma unroll
   for (int i = 0; i < G::kNB; ++i) {
     const int row = i * G::kRpl + lrow;
-    wchk[i] = ((lane % kSlots) ^ swizzle<BK>(row)) * 16;
+    wchk[i] = ((lane % kSlots) ^ swizzle(row)) * 16;
     woff[i] = (int)(min((int64_t)row, p.N - 1 - n0) * p.ws);
   }
   int8_t* mine = sm + wave * NS * G::kStage;
@@ -427,7 +524,7 @@ __global__ __launch_bounds__(W * 64, 2) void k_gemm_w8a8_split(GemmParams p) {
     v4i fa[BK / 32][TM], fb[BK / 32][TN];
 #pragma unroll
     for (int ks = 0; ks < BK / 32; ++ks) {
-      const int slot = ((2 * ks + kh) ^ swizzle<BK>(lane & 31)) * 16;
+      const int slot = ((2 * ks + kh) ^ swizzle(lane & 31)) * 16;
 #pragma unroll
       for (int mt = 0; mt < TM; ++mt) fa[ks][mt] = *reinterpret_cast<const v4i*>(base + (mt * 32 + (lane & 31)) * BK + slot);
 #pragma unroll
@@ -511,146 +608,6 @@ __global__ __launch_bounds__(W * 64, 2) void k_gemm_w8a8_split(GemmParams p) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Rows at any address and K of any length: the tiles of k_gemm_w8a8_tile with the operands through
-// registers. A chunk's 16 bytes are the 4 or 5 aligned words that hold them, shifted into place as they
-// go to LDS (loads of 16 unaligned bytes, one step ahead in 128 x 128 tiles, took 341 us at 4096 x 4095 x
-// 4097, this 151; 777 x 1001 x 1501: 45 and 13.5). The loads run two steps ahead of the products
-// (two register sets, named statically by unrolling the loop twice), the LDS stages one: step s + 2
-// goes into the stage that step s - 1 has left, which every wave has by the barrier of step s.
-struct Words {
-  uint4 w;
-  uint32_t w4;  // holds the last codes when there is a shift; without one the word is not read
-};
-
-__device__ __forceinline__ Words load_words(const int8_t* at, uint32_t sh) {
-  const uint32_t* q = reinterpret_cast<const uint32_t*>(at - sh);
-  return Words{make_uint4(q[0], q[1], q[2], q[3]), q[sh ? 4 : 3]};
-}
-
-__device__ __forceinline__ uint4 shifted(const Words& r, uint32_t sh) {
-  return make_uint4(__builtin_amdgcn_alignbyte(r.w.y, r.w.x, sh), __builtin_amdgcn_alignbyte(r.w.z, r.w.y, sh),
-                    __builtin_amdgcn_alignbyte(r.w.w, r.w.z, sh), __builtin_amdgcn_alignbyte(r.w4, r.w.w, sh));
-}
-
-template <int WM, int WN, int TM, int TN>
-__global__ __launch_bounds__(WM * WN * 64, 2) void k_gemm_w8a8_any(GemmParams p) {
-  constexpr int NS = 3;
-  using G = Tile<WM, WN, TM, TN, NS, 64>;
-  static_assert(WM * WN * 32 * (TN * 32 * 4 + 16) <= NS * G::kStage, "the output buffers fit the stages");
-  __shared__ __align__(1024) int8_t sm[NS * G::kStage + 8 * G::kBN];
-  float* s_sw = reinterpret_cast<float*>(sm + NS * G::kStage);
-  float* s_bias = s_sw + G::kBN;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = uniform(tid >> 6);
-  const int wm = wave / WN, wn = wave % WN, kh = lane >> 5;
-  int64_t m0, n0;
-  if (!tile_of(p, G::kBM, G::kBN, m0, n0)) return;
-  float sa[TM];
-  load_scales<TM>(p, G::kBN, m0 + wm * TM * 32, n0, lane, tid, G::kWaves * 64, s_sw, s_bias, sa);
-
-  const int8_t* arow[G::kNA];
-  const int8_t* wrow[G::kNB];
-  const int lrow = lane >> 2, chunk = ((lane & 3) ^ swizzle<64>(lrow)) * 16;
-#pragma unroll
-  for (int i = 0; i < G::kNA; ++i) arow[i] = p.a + min(m0 + (wave * G::kNA + i) * 16 + lrow, p.M - 1) * p.as;
-#pragma unroll
-  for (int i = 0; i < G::kNB; ++i) wrow[i] = p.w + min(n0 + (wave * G::kNB + i) * 16 + lrow, p.N - 1) * p.ws;
-  const int full = (int)(p.K / 64), tail = (int)(p.K % 64) != 0;
-  const int nsteps = full + tail;
-  uint32_t ash[G::kNA], wsh[G::kNB];  // bytes past a word of each row (the same at every step)
-#pragma unroll
-  for (int i = 0; i < G::kNA; ++i) ash[i] = (uint32_t)(uintptr_t)arow[i] & 3u;
-#pragma unroll
-  for (int i = 0; i < G::kNB; ++i) wsh[i] = (uint32_t)(uintptr_t)wrow[i] & 3u;
-  int8_t* dst_a = sm + wave * G::kNA * 1024 + lane * 16;
-  int8_t* dst_w = sm + G::kBM * 64 + wave * G::kNB * 1024 + lane * 16;
-  struct Regs {
-    Words a[G::kNA], w[G::kNB];
-  };
-  auto load = [&](int s, Regs& r) {  // full steps only (past the last one the last again)
-    const int64_t k = (int64_t)(min(s, nsteps - 1) - tail) * 64 + chunk;
-#pragma unroll
-    for (int i = 0; i < G::kNA; ++i) r.a[i] = load_words(arow[i] + k, ash[i]);
-#pragma unroll
-    for (int i = 0; i < G::kNB; ++i) r.w[i] = load_words(wrow[i] + k, wsh[i]);
-  };
-  auto store = [&](int st, const Regs& r) {
-#pragma unroll
-    for (int i = 0; i < G::kNA; ++i) *reinterpret_cast<uint4*>(dst_a + st * G::kStage + i * 1024) = shifted(r.a[i], ash[i]);
-#pragma unroll
-    for (int i = 0; i < G::kNB; ++i) *reinterpret_cast<uint4*>(dst_w + st * G::kStage + i * 1024) = shifted(r.w[i], wsh[i]);
-  };
-
-  v16i acc[TM][TN];
-#pragma unroll
-  for (int mt = 0; mt < TM; ++mt)
-#pragma unroll
-    for (int nt = 0; nt < TN; ++nt) acc[mt][nt] = v16i{};
-  v4i fa[2][TM], fb[2][TN];
-  const int slot0 = (kh ^ swizzle<64>(lane & 31)) * 16;
-  const int abase = (wm * TM * 32 + (lane & 31)) * 64, bbase = (G::kBM + wn * TN * 32 + (lane & 31)) * 64;
-  auto frags = [&](int st, int ks) {
-    const int8_t* base = sm + st * G::kStage + (slot0 ^ (ks * 32));
-#pragma unroll
-    for (int mt = 0; mt < TM; ++mt) fa[ks][mt] = *reinterpret_cast<const v4i*>(base + abase + mt * 2048);
-#pragma unroll
-    for (int nt = 0; nt < TN; ++nt) fb[ks][nt] = *reinterpret_cast<const v4i*>(base + bbase + nt * 2048);
-  };
-  auto products = [&](int ks) {
-#pragma unroll
-    for (int mt = 0; mt < TM; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < TN; ++nt)
-        acc[mt][nt] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks][nt], fa[ks][mt], acc[mt][nt], 0, 0, 0);
-  };
-
-  if (nsteps > 0) {
-    Regs r0, r1;
-    // step 0 (the partial one when there is one; rows shorter than a step have no other)
-    if (tail) {
-#pragma unroll
-      for (int i = 0; i < G::kNA; ++i) *reinterpret_cast<uint4*>(dst_a + i * 1024) = load16(arow[i], full * 64 + chunk, p.K);
-#pragma unroll
-      for (int i = 0; i < G::kNB; ++i) *reinterpret_cast<uint4*>(dst_w + i * 1024) = load16(wrow[i], full * 64 + chunk, p.K);
-    } else {
-      load(0, r0);
-      store(0, r0);
-    }
-    if (nsteps > 1) {
-      load(1, r1);
-      load(2, r0);
-      store(1, r1);
-      load(3, r1);
-    }
-    __syncthreads();
-    frags(0, 0);
-    int st = 0;
-    // step s from stage st: `next` holds step s + 2
-    auto step = [&](int s, Regs& next) {
-      const int nx = st + 1 == NS ? 0 : st + 1, nn = nx + 1 == NS ? 0 : nx + 1;
-      frags(st, 1);
-      products(0);
-      __syncthreads();  // every wave has read stage st - 1 (= nn) in full, and step s + 1 is in nx
-      frags(nx, 0);
-      if (nsteps > 1) {
-        store(nn, next);
-        load(s + 4, next);
-      }
-      products(1);
-      st = nx;
-    };
-    for (int s = 0; s < nsteps; s += 2) {
-      step(s, r0);
-      if (s + 1 < nsteps) step(s + 1, r1);
-    }
-  }
-  __syncthreads();
-  const int64_t mw = m0 + wm * TM * 32, nw = n0 + wn * TN * 32;
-  if (p.yf16) epilogue<TM, TN, false, __half>(p, sm, s_sw + wn * TN * 32, s_bias + wn * TN * 32, acc, sa, mw, nw, wave, lane);
-  else epilogue<TM, TN, false, float>(p, sm, s_sw + wn * TN * 32, s_bias + wn * TN * 32, acc, sa, mw, nw, wave, lane);
-}
-
-// ------------------------------------------------------------------------------------------------
 // The form for a shape, by estimated time (us): a tile costs tile + step * (steps of 64 codes of K) of
 // its CU when it shares it, tile_alone + step_alone * steps when the last round leaves it alone there;
 // the whole at least the bytes at 4.3 TB/s. The constants follow a fit (16 % rms) to 30 shapes of 1 .. 16384
@@ -660,34 +617,27 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void k_gemm_w8a8_any(GemmParams p)
 //   64 x 4096 x 8192      69 / 38 / 30 / 21 / 18 / 9.3      256 x 4096 x 8192   72 / 40 / 31 / 22 / 18 / 25 (deep 64x64: 16.4)
 //   1000 x 1536 x 768     13 / 8.8 / 7.4 / 5.8 / 5.7 / 13   256 x 18560 x 4096  56 / 33 / 47 / 45 / 46 / 88
 //   1024 x 4096 x 4096    40 / 24 / 21 / 24 / 30 / 62       4096 x 4096 x 4096  58 / 66 / 82 / 90 / 111 / 294
-enum Form { TILE256, TILE256X128, TILE128, TILE128X64, TILE64, TILE64DEEP, SPLIT32, FORMS };
+enum Form { TILE256, TILE256X128, TILE128, TILE128X64, TILE64, SPLIT32, TILE64DEEP, FORMS };
 struct Cost {
   int bm, bn, per_cu;
   double tile, step, tile_alone, step_alone;
 };
 constexpr Cost kCost[FORMS] = {{256, 256, 1, 0.0, 0.68, 6.0, 0.591},    {256, 128, 1, 4.31, 0.321, 4.31, 0.321},
                                {128, 128, 1, 3.93, 0.231, 3.93, 0.231}, {128, 64, 2, 1.48, 0.164, 2.56, 0.156},
-                               {64, 64, 3, 0.87, 0.104, 1.65, 0.111},   {64, 64, 1, 1.0, 0.132, 1.0, 0.101},
-                               {32, 32, 2, 1.26, 0.048, 1.26, 0.048}};
-
-// The same for rows at any address (k_gemm_w8a8_any; 64x64 / 128x128 / 256x128): 3 x 1001 x 1501 takes
-// 10 / 19 / 24 us, 777 x 1001 x 1501 14 / 24 / 31, 2000 x 3001 x 2001 55 / 44 / 37, 4096 x 4095 x 4097
-// 301 / 178 / 151.
-enum AnyForm { ANY64, ANY128, ANY256X128, ANY_FORMS };
-constexpr Cost kAnyCost[ANY_FORMS] = {{64, 64, 1, 0.0, 0.29, 0.0, 0.36}, {128, 128, 1, 0.0, 0.69, 0.0, 0.69},
-                                      {256, 128, 1, 0.0, 1.16, 0.0, 0.90}};
+                               {64, 64, 3, 0.87, 0.104, 1.65, 0.111},   {32, 32, 2, 1.26, 0.048, 1.26, 0.048},
+                               {64, 64, 1, 1.0, 0.132, 1.0, 0.101}};
 
 constexpr int64_t kMaxTiles = ((int64_t)1 << 23) - 8;
 
-// Index of the cheapest of n forms.
-int choose(const GemmParams& p, const Cost* costs, int n) {
+// The cheapest of the first n forms.
+Form choose(const GemmParams& p, int n) {
   constexpr double kCus = 256.0;
   const double steps = (double)cdiv(p.K, 64);
   const double bytes = ((double)p.M + (double)p.N) * (double)p.K + (p.yf16 ? 2.0 : 4.0) * (double)p.M * (double)p.N;
   int best = -1;
   double least = 0.0;
   for (int f = 0; f < n; ++f) {
-    const Cost& c = costs[f];
+    const Cost& c = kCost[f];
     const double tiles = (double)cdiv(p.M, c.bm) * (double)cdiv(p.N, c.bn), slots = kCus * c.per_cu;
     if (tiles >= (double)kMaxTiles) continue;
     const double busy = c.tile + c.step * steps, alone = c.tile_alone + c.step_alone * steps;
@@ -699,10 +649,23 @@ int choose(const GemmParams& p, const Cost* costs, int n) {
       best = f;
     }
   }
-  return best;
+  return (Form)best;
 }
 
 unsigned grid_of(const GemmParams& p, int bm, int bn) { return (unsigned)(cdiv(cdiv(p.M, bm) * cdiv(p.N, bn), 8) * 8); }
+
+template <bool SHIFT>
+void launch_tile(Form form, const GemmParams& p, hipStream_t stream) {
+  switch (form) {
+    case TILE256: k_gemm_w8a8_tile<2, 4, 4, 2, 2, 128, 1, SHIFT><<<grid_of(p, 256, 256), 512, 0, stream>>>(p); break;
+    case TILE256X128: k_gemm_w8a8_tile<4, 2, 2, 2, 3, 128, 1, SHIFT><<<grid_of(p, 256, 128), 512, 0, stream>>>(p); break;
+    case TILE128: k_gemm_w8a8_tile<2, 2, 2, 2, 3, 128, 1, SHIFT><<<grid_of(p, 128, 128), 256, 0, stream>>>(p); break;
+    case TILE128X64: k_gemm_w8a8_tile<2, 2, 2, 1, 3, 128, 1, SHIFT><<<grid_of(p, 128, 64), 256, 0, stream>>>(p); break;
+    case TILE64: k_gemm_w8a8_tile<2, 2, 1, 1, 3, 128, 1, SHIFT><<<grid_of(p, 64, 64), 256, 0, stream>>>(p); break;
+    default:
+      if constexpr (!SHIFT) k_gemm_w8a8_tile<2, 2, 1, 1, 6, 128, 3, false><<<grid_of(p, 64, 64), 256, 0, stream>>>(p);
+  }
+}
 
 }  // namespace
 
@@ -731,27 +694,19 @@ extern "C" qssm_status qssm_gemm_w8a8(const qssm_gemm_w8a8_args* a, hipStream_t 
   if (cdiv(M, 256) * cdiv(N, 128) >= kMaxTiles) return fail(QSSM_ERR_UNSUPPORTED, "M * N too large");
   const GemmParams p{M, N, K, a->a_per_row != 0, a->y_dtype == QSSM_F16, a->a, a->a_stride, a->a_scales,
                      a->w, a->w_stride, a->w_scales, a->bias, a->y, a->y_stride};
-  // direct loads take addresses that are multiples of 4 bytes
+  // Direct loads take addresses that are multiples of 4 bytes. The split form then takes any K >= 16, the
+  // tiles without SHIFT a K that holds a full step. (1 x 1000 x 64: the split form 3.8 us, a shifted tile 4.5.)
   const bool direct = ((uintptr_t)a->a | (uintptr_t)a->w | (uintptr_t)a->a_stride | (uintptr_t)a->w_stride) % 4 == 0;
-  if (!direct || K < 128) {
-    switch (choose(p, kAnyCost, ANY_FORMS)) {
-      case ANY64: k_gemm_w8a8_any<2, 2, 1, 1><<<grid_of(p, 64, 64), 256, 0, stream>>>(p); break;
-      case ANY128: k_gemm_w8a8_any<2, 2, 2, 2><<<grid_of(p, 128, 128), 256, 0, stream>>>(p); break;
-      default: k_gemm_w8a8_any<4, 2, 2, 2><<<grid_of(p, 256, 128), 512, 0, stream>>>(p); break;
-    }
-    return launch_status("gemm_w8a8");
-  }
-  switch (choose(p, kCost, FORMS)) {
-    case TILE256: k_gemm_w8a8_tile<2, 4, 4, 2, 2, 128, 1><<<grid_of(p, 256, 256), 512, 0, stream>>>(p); break;
-    case TILE256X128: k_gemm_w8a8_tile<4, 2, 2, 2, 3, 128, 1><<<grid_of(p, 256, 128), 512, 0, stream>>>(p); break;
-    case TILE128: k_gemm_w8a8_tile<2, 2, 2, 2, 3, 128, 1><<<grid_of(p, 128, 128), 256, 0, stream>>>(p); break;
-    case TILE128X64: k_gemm_w8a8_tile<2, 2, 2, 1, 3, 128, 1><<<grid_of(p, 128, 64), 256, 0, stream>>>(p); break;
-    case TILE64: k_gemm_w8a8_tile<2, 2, 1, 1, 3, 128, 1><<<grid_of(p, 64, 64), 256, 0, stream>>>(p); break;
-    case TILE64DEEP: k_gemm_w8a8_tile<2, 2, 1, 1, 6, 128, 3><<<grid_of(p, 64, 64), 256, 0, stream>>>(p); break;
-    default:
-      // up to 16 tokens load only 16 of a tile's 32 rows (8 tokens x 18560 x 4096: 18.9 us, 19.9 with all)
-      if (M <= 16) k_gemm_w8a8_split<1, 1, 128, 4, 16, 2><<<grid_of(p, 32, 32), 256, 0, stream>>>(p);
-      else k_gemm_w8a8_split<1, 1, 128, 4, 32, 2><<<grid_of(p, 32, 32), 256, 0, stream>>>(p);
+  const Form form = choose(p, direct && K >= 128 ? FORMS : direct && K >= 16 ? TILE64DEEP : SPLIT32);
+  if (form == SPLIT32) {
+    // up to 16 tokens load only 16 of a tile's 32 rows (8 tokens x 18560 x 4096: 18.9 us, 19.9 with all)
+    if (M <= 16) k_gemm_w8a8_split<1, 1, 128, 4, 16, 2><<<grid_of(p, 32, 32), 256, 0, stream>>>(p);
+    else k_gemm_w8a8_split<1, 1, 128, 4, 32, 2><<<grid_of(p, 32, 32), 256, 0, stream>>>(p);
+  } else if (!direct || K < 128) {
+    // the shifted tiles at the same estimates: the fastest or within 6 % of it in 12 shapes of 1 .. 16384 tokens
+    launch_tile<true>(form, p, stream);
+  } else {
+    launch_tile<false>(form, p, stream);
   }
   return launch_status("gemm_w8a8");
 }

@@ -100,6 +100,39 @@ def test_every_form(dev, M, N, K):
     assert np.all(np.abs(y[rows] - want) <= bound(want, yb, f16))
 
 
+# The tiles of 256 x 256, 256 x 128, 128 x 128, 128 x 64 and 64 x 64 (two shapes each) with rows of every alignment,
+# and the shortest rows: (pads of a and w, offsets of a and w)
+ROWS_ANYWHERE = [(4100, 4100, 965), (2300, 4300, 131), (1300, 4000, 513), (2048, 2049, 255), (521, 5536, 1021), (540, 5500, 2047),
+                 (1281, 2309, 129), (521, 5463, 135), (300, 4000, 703), (70, 1000, 133), (3, 130, 1023), (4000, 700, 127), (65, 300, 126), (130, 70, 3),
+                 (9, 33, 2), (1, 1, 125), (130, 130, 16), (66, 65, 15)]
+
+
+@pytest.mark.parametrize("M,N,K", ROWS_ANYWHERE)
+def test_rows_at_any_address(dev, M, N, K):
+    """Rows 1 or 3 bytes further apart than a multiple of 4, and tensors that start at any byte; the bytes
+    around and between the rows are 99."""
+    import torch
+    import quantized_state_space_amd as qs
+    a, sa, w, sw, b = make(M + 2 * K, M, N, K)
+    rows = np.unique(np.concatenate([[0, M - 1, M // 2], np.random.default_rng(M).integers(0, M, 150)]))
+    yb = ow.gemm_w8a8(a[rows], sa[rows], w, sw)
+    want = yb + b.astype(np.float64)
+    for pa, pw, oa, ob in ((-K % 4 + 1, -K % 4 + 3, 0, 1), (-K % 4 + 3, -K % 4 + 4, 2, 3), (-K % 4, -K % 4 + 1, 1, 2), (-K % 4, -K % 4, 3, 3)):
+        print(f"\n[gemm_w8a8 rows anywhere M={M} N={N} K={K} pads={pa, pw} offsets={oa, ob}]", flush=True)
+
+        def place(t, pad, off):
+            flat = torch.full((t.shape[0] * (K + pad) + off,), 99, dtype=torch.int8, device=dev)
+            v = flat[off:].view(t.shape[0], K + pad)[:, :K]
+            v.copy_(torch.from_numpy(t))
+            return v
+        y = torch.full((M, N), float("nan"), device=dev)
+        dv = lambda v: torch.from_numpy(v).to(dev)  # noqa: E731
+        qs.qssm_gemm_w8a8(qs.gemm_w8a8_args(place(a, pa, oa), dv(sa), place(w, pw, ob), dv(sw), y, bias=dv(b)))
+        got = y[torch.from_numpy(rows).to(dev)].cpu().numpy().astype(np.float64)
+        assert np.all(np.abs(got - want) <= bound(want, yb, False))
+        assert bool(torch.isfinite(y).all())
+
+
 @pytest.mark.parametrize("M,N,K,pads,offset", [
     (1, 200, 512, (16, 32, 3), 0), (40, 200, 512, (16, 16, 1), 0), (200, 300, 320, (16, 48, 5), 0),
     (40, 200, 513, (5, 1, 1), 0), (200, 300, 512, (0, 0, 0), 1), (3, 70, 256, (0, 0, 0), 8),
