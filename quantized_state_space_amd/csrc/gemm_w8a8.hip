@@ -98,6 +98,15 @@ __device__ __forceinline__ v4i shifted(const v4i& v, uint32_t next, uint32_t sh)
              (int)__builtin_amdgcn_alignbyte(v[3], v[2], sh), (int)__builtin_amdgcn_alignbyte(next, v[3], sh)};
 }
 
+// The word behind the partial step that follows `full` steps of BK bytes, of K bytes from `row` (a
+// multiple of 4) on: it holds at most three codes, and is read where it holds any (else the row's first).
+template <int BK>
+__device__ __forceinline__ uint32_t word_behind(const int8_t* row, int full, int64_t K) {
+  const int left = (int)K - (full + 1) * BK;
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(row + (left > 0 ? (full + 1) * BK : 0));
+  return left > 0 ? w & ((1u << (8 * left)) - 1u) : 0u;
+}
+
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const int8_t* p, int bytes = 0x7fffffff) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p), (short)0, bytes, kBufferWord3);
 }
@@ -377,15 +386,10 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
   for (int d = 1; d < kFirst; ++d) issue(d, d);
   if (tail) {
     uint4 va[G::kNA], vw[G::kNB];
-    // at most three codes lie behind the step, in a word that holds codes (else the row's first word)
     uint32_t xw[G::kNX + 1];
-    int xleft[G::kNX + 1];
 #pragma unroll
-    for (int i = 0; i < G::kNX; ++i) {
-      xleft[i] = (int)(p.K + xsh[i]) - (full + 1) * BK;
-      const int first = xoff[i] - BK + (xsh[i] ? 0 : 4), at = xleft[i] > 0 ? xoff[i] + full * BK : first;
-      xw[i] = *reinterpret_cast<const uint32_t*>((xrow[i] < G::kBM ? abase : wbase) + at);
-    }
+    for (int i = 0; i < G::kNX; ++i)
+      xw[i] = word_behind<BK>((xrow[i] < G::kBM ? abase : wbase) + (xoff[i] - BK + (xsh[i] ? 0 : 4)), full, p.K + xsh[i]);
     if (!SHIFT || p.K >= 16) {
 #pragma unroll
       for (int i = 0; i < G::kNA; ++i) va[i] = load16(abase + aoff[i], full * BK + achk[i], p.K + atail[i]);
@@ -403,7 +407,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
     for (int i = 0; i < G::kNB; ++i) *reinterpret_cast<uint4*>(dst_w + i * 1024 + lane * 16) = vw[i];
 #pragma unroll
     for (int i = 0; i < G::kNX; ++i)
-      *reinterpret_cast<uint32_t*>(sm + G::kRows * BK + (xrow[i] + lane) * 4) = xleft[i] > 0 ? xw[i] & ((1u << (8 * xleft[i])) - 1u) : 0u;
+      *reinterpret_cast<uint32_t*>(sm + G::kRows * BK + (xrow[i] + lane) * 4) = xw[i];
   }
   wait_vm_lds<(kFirst - 1) * kLd>();
   __builtin_amdgcn_s_barrier();
@@ -474,20 +478,22 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
 // k, k + W, ... of BK bytes, each through NS LDS stages of its own that it fills and reads alone, so
 // no barrier is needed until the waves' integer sums are joined (exactly, in any order) in LDS.
 // ROWS: token rows that are loaded (a multiple of 1024 / BK; tokens past M up to ROWS read the last
-// row, those past ROWS are whatever the LDS held: their sums are not stored).
-template <int TM, int TN, int BK, int W, int ROWS, int NS>
+// row, those past ROWS are whatever the LDS held: their sums are not stored). SHIFT: as in the shared tiles.
+template <int TM, int TN, int BK, int W, int ROWS, int NS, bool SHIFT>
 struct Split {
   static constexpr int kBM = TM * 32, kBN = TN * 32, kRpl = 1024 / BK;  // rows per load instruction
   static constexpr int kNA = ROWS / kRpl, kNB = kBN / kRpl;
-  static constexpr int kStage = (kBM + kBN) * BK, kRow = kBN + 4;
+  static constexpr int kNX = SHIFT ? 2 : 0;  // loads of the next words of 64 rows, half of them twice
+  static constexpr int kStage = (kBM + kBN) * BK + kNX * 256, kRow = kBN + 4;
   static constexpr int kMain = NS * W * kStage, kEnd = W * kBM * kRow * 4;
   static constexpr int kLds = kMain > kEnd ? kMain : kEnd;
 };
 
-template <int TM, int TN, int BK, int W, int ROWS, int NS>
+template <int TM, int TN, int BK, int W, int ROWS, int NS, bool SHIFT>
 __global__ __launch_bounds__(W * 64, 2) void k_gemm_w8a8_split(GemmParams p) {
-  using G = Split<TM, TN, BK, W, ROWS, NS>;
-  constexpr int BM = G::kBM, BN = G::kBN, kSlots = BK / 16, kLd = G::kNA + G::kNB;
+  using G = Split<TM, TN, BK, W, ROWS, NS, SHIFT>;
+  constexpr int BM = G::kBM, BN = G::kBN, kSlots = BK / 16, kLd = G::kNA + G::kNB + G::kNX;
+  static_assert(!SHIFT || (TM == 1 && TN == 1), "a lane's next words are of one row of each operand");
   __shared__ __align__(1024) int8_t sm[G::kLds];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), kh = lane >> 5;
   const int64_t nm = (p.M + BM - 1) / BM, nn = (p.N + BN - 1) / BN;
@@ -496,21 +502,36 @@ __global__ __launch_bounds__(W * 64, 2) void k_gemm_w8a8_split(GemmParams p) {
   const int64_t m0 = id % nm * BM, n0 = id / nm * BN;
   const int8_t* abase = p.a + m0 * p.as;
   const int8_t* wbase = p.w + n0 * p.ws;
+  const int apre = SHIFT ? (int)((uintptr_t)abase & 3) : 0, wpre = SHIFT ? (int)((uintptr_t)wbase & 3) : 0;
+  abase -= apre;
+  wbase -= wpre;
+  constexpr int kWord = SHIFT ? ~3 : ~0;
+  const int alast = (int)min(p.M - 1 - m0, (int64_t)BM), wlast = (int)min(p.N - 1 - n0, (int64_t)BN);
+  const int as = (int)p.as, ws = (int)p.ws;
+  const auto a_at = [&](int row) { return min(row, alast) * as + apre; };
+  const auto w_at = [&](int row) { return min(row, wlast) * ws + wpre; };
   const int lrow = lane / kSlots;
   // load i: rows i kRpl ..., lane l at row l / kSlots, slot l % kSlots; byte offset of its chunk
   int aoff[G::kNA], woff[G::kNB], achk[G::kNA], wchk[G::kNB];
+  uint32_t atail[G::kNA], wtail[G::kNB];  // codes before the row's first
 #pragma unroll
   for (int i = 0; i < G::kNA; ++i) {
     const int row = i * G::kRpl + lrow;
     achk[i] = ((lane % kSlots) ^ swizzle(row)) * 16;
-    aoff[i] = (int)(min((int64_t)row, p.M - 1 - m0) * p.as);
+    aoff[i] = a_at(row) & kWord;
+    atail[i] = a_at(row) & ~kWord;
   }
 #pragma unroll
   for (int i = 0; i < G::kNB; ++i) {
     const int row = i * G::kRpl + lrow;
     wchk[i] = ((lane % kSlots) ^ swizzle(row)) * 16;
-    woff[i] = (int)(min((int64_t)row, p.N - 1 - n0) * p.ws);
+    woff[i] = w_at(row) & kWord;
+    wtail[i] = w_at(row) & ~kWord;
   }
+  // SHIFT: the lane's rows' codes before the first, and where the words behind a step lie
+  const int ax = a_at(lane & 31), wx = w_at(lane & 31);
+  const uint32_t sha = ax & 3, shb = wx & 3;
+  const int axoff = (ax & ~3) + BK - (sha ? 0 : 4), wxoff = (wx & ~3) + BK - (shb ? 0 : 4);
   int8_t* mine = sm + wave * NS * G::kStage;
   const int full = (int)(p.K / BK);
 
@@ -530,6 +551,15 @@ __global__ __launch_bounds__(W * 64, 2) void k_gemm_w8a8_split(GemmParams p) {
 #pragma unroll
       for (int nt = 0; nt < TN; ++nt) fb[ks][nt] = *reinterpret_cast<const v4i*>(base + (BM + nt * 32 + (lane & 31)) * BK + slot);
     }
+#pragma unroll
+    for (int ks = 0; ks < BK / 32; ++ks)
+      if constexpr (SHIFT) {
+        const int slot = ((2 * ks + kh + 1) ^ swizzle(lane & 31)) * 16, row = lane & 31;
+        const bool behind = ks == BK / 32 - 1 && kh;
+        const int8_t* words = base + (BM + BN) * BK;
+        fa[ks][0] = shifted(fa[ks][0], *reinterpret_cast<const uint32_t*>(behind ? words + row * 4 : base + row * BK + slot), sha);
+        fb[ks][0] = shifted(fb[ks][0], *reinterpret_cast<const uint32_t*>(behind ? words + 256 + row * 4 : base + (BM + row) * BK + slot), shb);
+      }
 #pragma unroll
     for (int ks = 0; ks < BK / 32; ++ks)
 #pragma unroll
@@ -555,6 +585,10 @@ __global__ __launch_bounds__(W * 64, 2) void k_gemm_w8a8_split(GemmParams p) {
     for (int i = 0; i < G::kNA; ++i) load_lds(ra, mine + st * G::kStage + i * 1024, aoff[i] + achk[i], koff);
 #pragma unroll
     for (int i = 0; i < G::kNB; ++i) load_lds(rw, mine + st * G::kStage + BM * BK + i * 1024, woff[i] + wchk[i], koff);
+    if constexpr (SHIFT) {
+      load_lds_word(ra, mine + st * G::kStage + (BM + BN) * BK, axoff, koff);
+      load_lds_word(rw, mine + st * G::kStage + (BM + BN) * BK + 256, wxoff, koff);
+    }
   };
   if (wave < full) {
 #pragma unroll
@@ -572,10 +606,19 @@ __global__ __launch_bounds__(W * 64, 2) void k_gemm_w8a8_split(GemmParams p) {
   // the last K % BK codes
   if (p.K % BK != 0 && wave == full % W) {
     uint4 va[G::kNA], vw[G::kNB];
+    uint32_t xa = 0u, xw = 0u;
+    if constexpr (SHIFT) {
+      xa = word_behind<BK>(abase + (ax & ~3), full, p.K + sha);
+      xw = word_behind<BK>(wbase + (wx & ~3), full, p.K + shb);
+    }
 #pragma unroll
-    for (int i = 0; i < G::kNA; ++i) va[i] = load16(abase + aoff[i], full * BK + achk[i], p.K);
+    for (int i = 0; i < G::kNA; ++i) va[i] = load16(abase + aoff[i], full * BK + achk[i], p.K + atail[i]);
 #pragma unroll
-    for (int i = 0; i < G::kNB; ++i) vw[i] = load16(wbase + woff[i], full * BK + wchk[i], p.K);
+    for (int i = 0; i < G::kNB; ++i) vw[i] = load16(wbase + woff[i], full * BK + wchk[i], p.K + wtail[i]);
+    if constexpr (SHIFT) {
+      *reinterpret_cast<uint32_t*>(mine + (BM + BN) * BK + lane * 4) = xa;
+      *reinterpret_cast<uint32_t*>(mine + (BM + BN) * BK + 256 + lane * 4) = xw;
+    }
     to_lds(va, vw);
     products(0);
   }
@@ -667,6 +710,11 @@ void launch_tile(Form form, const GemmParams& p, hipStream_t stream) {
   }
 }
 
+template <int ROWS, bool SHIFT>
+void launch_split(const GemmParams& p, hipStream_t stream) {
+  k_gemm_w8a8_split<1, 1, 128, 4, ROWS, 2, SHIFT><<<grid_of(p, 32, 32), 256, 0, stream>>>(p);
+}
+
 }  // namespace
 
 extern "C" qssm_status qssm_gemm_w8a8(const qssm_gemm_w8a8_args* a, hipStream_t stream) {
@@ -694,14 +742,14 @@ extern "C" qssm_status qssm_gemm_w8a8(const qssm_gemm_w8a8_args* a, hipStream_t 
   if (cdiv(M, 256) * cdiv(N, 128) >= kMaxTiles) return fail(QSSM_ERR_UNSUPPORTED, "M * N too large");
   const GemmParams p{M, N, K, a->a_per_row != 0, a->y_dtype == QSSM_F16, a->a, a->a_stride, a->a_scales,
                      a->w, a->w_stride, a->w_scales, a->bias, a->y, a->y_stride};
-  // Direct loads take addresses that are multiples of 4 bytes. The split form then takes any K >= 16, the
-  // tiles without SHIFT a K that holds a full step. (1 x 1000 x 64: the split form 3.8 us, a shifted tile 4.5.)
+  // Direct loads take addresses that are multiples of 4 bytes; other rows, and in the tiles a K without a full
+  // step, take the shifted forms. The split form needs K >= 16 (1 x 1000 x 64: 3.8 us, a shifted tile 4.5).
   const bool direct = ((uintptr_t)a->a | (uintptr_t)a->w | (uintptr_t)a->a_stride | (uintptr_t)a->w_stride) % 4 == 0;
-  const Form form = choose(p, direct && K >= 128 ? FORMS : direct && K >= 16 ? TILE64DEEP : SPLIT32);
+  const Form form = choose(p, direct && K >= 128 ? FORMS : K >= 16 ? TILE64DEEP : SPLIT32);
   if (form == SPLIT32) {
     // up to 16 tokens load only 16 of a tile's 32 rows (8 tokens x 18560 x 4096: 18.9 us, 19.9 with all)
-    if (M <= 16) k_gemm_w8a8_split<1, 1, 128, 4, 16, 2><<<grid_of(p, 32, 32), 256, 0, stream>>>(p);
-    else k_gemm_w8a8_split<1, 1, 128, 4, 32, 2><<<grid_of(p, 32, 32), 256, 0, stream>>>(p);
+    if (M <= 16) direct ? launch_split<16, false>(p, stream) : launch_split<16, true>(p, stream);
+    else direct ? launch_split<32, false>(p, stream) : launch_split<32, true>(p, stream);
   } else if (!direct || K < 128) {
     // the shifted tiles at the same estimates: the fastest or within 6 % of it in 12 shapes of 1 .. 16384 tokens
     launch_tile<true>(form, p, stream);

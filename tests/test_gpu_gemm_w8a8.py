@@ -104,7 +104,9 @@ def test_every_form(dev, M, N, K):
 # and the shortest rows: (pads of a and w, offsets of a and w)
 ROWS_ANYWHERE = [(4100, 4100, 965), (2300, 4300, 131), (1300, 4000, 513), (2048, 2049, 255), (521, 5536, 1021), (540, 5500, 2047),
                  (1281, 2309, 129), (521, 5463, 135), (300, 4000, 703), (70, 1000, 133), (3, 130, 1023), (4000, 700, 127), (65, 300, 126), (130, 70, 3),
-                 (9, 33, 2), (1, 1, 125), (130, 130, 16), (66, 65, 15)]
+                 (9, 33, 2), (1, 1, 125), (130, 130, 16), (66, 65, 15),
+                 # K split over four waves, with 16 or 32 token rows
+                 (1, 4001, 4095), (20, 3000, 2047), (32, 1000, 130), (7, 500, 17), (16, 260, 257), (33, 50, 639)]
 
 
 @pytest.mark.parametrize("M,N,K", ROWS_ANYWHERE)
