@@ -112,13 +112,14 @@ __device__ __forceinline__ void round_store(__amdgpu_buffer_rsrc_t r, int c, flo
 // silu(z) = z / (1 + e^-z), in fp64 and rounded once to fp32. With y = -z / ln2 = n + f, |f| <= 1/2:
 // e^-z = 2^n p(f), p the polynomial of degree 9 with the least largest relative error against 2^f
 // (1.4e-14; coefficients by Remez exchange in 50 digits). Adding 1.5 * 2^52 rounds y to n, which is
-// then in the low word. Beyond |n| = 200 (an fp32 gate: |z| = 126) silu rounds to z or to -0 either
-// way, so n (z) is clamped there. An infinite gate gives a NaN, which like an infinity leaves its
-// group's codes at 0. One Newton step takes the reciprocal to ~2^-46.
+// then in the low word. The exponent's argument is clamped where silu rounds to z or to -0 either way:
+// an fp16 gate's n at 200 (65504 * 2^-200), an fp32 gate's z at 200 (the largest number * e^-200 is
+// 2^-160, below half the least denormal 2^-149). An infinite gate gives an infinity or a NaN, which
+// leave its group's codes at 0. One Newton step takes the reciprocal to ~2^-46.
 template <bool F16>
 __device__ __forceinline__ float silu_f64(float z) {
   constexpr double kLog2e = 1.4426950408889634, kMagic = 6755399441055744.0;
-  const double x = -(double)(F16 ? z : __builtin_amdgcn_fmed3f(z, -126.0f, 126.0f));
+  const double x = -(double)(F16 ? z : __builtin_amdgcn_fmed3f(z, -200.0f, 200.0f));
   const double t = fma(x, kLog2e, kMagic);
   const double f = fma(x, kLog2e, -(t - kMagic));
   double e = 0x1.b3f42432927dap-24;
