@@ -440,7 +440,8 @@ def update_args(x, x_group_of, x_scales, Bm, Cm, B_scales, C_scales, gs, delta, 
     Gbc, N = Bm.shape[1], Bm.shape[2]
     sdt = {torch.float32: QSSM_F32, torch.int8: QSSM_I8}.get(state.dtype, QSSM_F16)
     if sdt == QSSM_I8:
-        want = {"state": (state, (B, nh, P, N)), "y": (y, (B, nh, P)), "C": (Cm, (B, Gbc, N)),
+        want = {"state": (state, (B, nh, P, N)), "y": (y, (B, nh, P)), "B": (Bm, (B, Gbc, N)),
+                "C": (Cm, (B, Gbc, N)),
                 "delta": (delta, (B, nh)), "A": (A, (nh,)), "x_group_of": (x_group_of, (nh * P,)),
                 "B_scales": (B_scales, (Gbc * N // gs,)), "C_scales": (C_scales, (Gbc * N // gs,)),
                 "Dskip": (Dskip, (nh,)), "xq_out": (xq_out, (B, nh, P)),
