@@ -496,14 +496,16 @@ qssm_status qssm_rmsnorm_i8(const qssm_rmsnorm_args* a, hipStream_t stream);
  * W8A8 linear layer: int8 weights x int8 activations on int8 MFMA with int32 accumulation, one scale
  * per token and per output channel.
  * Quamba2, abstract (W8A8 for the Mamba1 and Mamba2 backbones, prefill and generation).
- *   y[m, n] = bias[n] + fl32(sa[m] * sw[n]) * sum_k a[m, k] * w[n, k]
+ *   y[m, n] = bias[n] + (sa[m] * sw[n]) * sum_k a[m, k] * w[n, k]
  * a: int8 codes [M, K], rows a_stride apart; a_scales [M] (a_per_row != 0: the token scales of
  *    qssm_rmsnorm_i8) or [1]; w: int8 codes [N, K], rows w_stride apart, and w_scales [N], as
  *    qssm_quant_w8 writes them; bias [N] fp32 or NULL; y [M, N] fp32 or fp16, rows y_stride apart.
  * A scale that is not valid gives its row or column y = bias. The integer sum is exact (K <= 131071,
- * else QSSM_ERR_UNSUPPORTED), is rounded once to fp32, and one fused multiply-add scales it and
- * adds the bias; an fp16 y is rounded once more. K == 0 gives y = bias. Any M, N >= 0, any
- * alignment of a and w (addresses and strides that are multiples of 4 bytes take the fast forms);
+ * else QSSM_ERR_UNSUPPORTED), is rounded once to fp32, and one fused multiply-add scales it by
+ * fl32(sa * sw) and adds the bias; where sa or sw lies outside [2^-63, 2^63], so that their product could
+ * leave fp32's normal range, all of it is fp64 and the result is rounded to fp32. An fp16 y is rounded
+ * once more. K == 0 gives y = bias. Any M, N >= 0, any alignment of a and w (addresses and strides
+ * that are multiples of 4 bytes take the fast forms);
  * a_stride and w_stride at most 2^22, M and N at most 2^27.
  */
 typedef struct qssm_gemm_w8a8_args {

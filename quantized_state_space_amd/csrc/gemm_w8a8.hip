@@ -2,7 +2,7 @@
 //
 // Quamba2, abstract: W8A8 blocks, prefill and generation (the in and out projections around the
 // recurrence).
-//     y[m, n] = bias[n] + fl32(sa[m] sw[n]) * sum_k a[m, k] w[n, k]
+//     y[m, n] = bias[n] + sa[m] sw[n] * sum_k a[m, k] w[n, k]      (roundings: scaled())
 // Both operands have k contiguous, which is the operand order of v_mfma_i32_32x32x32_i8: lane l of a
 // wave holds row (or column) l % 32 and the 16 consecutive k at 16 (l / 32). The weights go in as the
 // first operand, so a lane ends with one token and groups of 4 consecutive output channels.
@@ -14,6 +14,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.hpp"
 
@@ -44,6 +45,16 @@ __device__ __forceinline__ float valid_or_zero(float s) { return scale_ok(s) ? s
 // of the scales, one of the fused multiply-add (and one more to an fp16 y).
 __device__ __forceinline__ float scaled(float sa, float sw, int acc, float bias) {
   return fmaf(sa * sw, (float)acc, bias);
+}
+
+// s in [2^-63, 2^63], by its bits: the product of two such scales is a normal fp32 number.
+__device__ __forceinline__ bool tame(float s) { return __float_as_uint(s) - 0x20000000u <= 0x3f000000u; }
+
+// The same for any valid scales (2^-100 to 2^100) and the 0 of one that is not: a product that may be an
+// infinity, a 0 or a few bits in fp32 is taken in fp64, where it is exact, and the result rounds once.
+__device__ __forceinline__ float scaled_wide(float sa, float sw, int acc, float bias) {
+  if (tame(sa) && tame(sw)) return scaled(sa, sw, acc, bias);
+  return (float)fma((double)sa * (double)sw, (double)acc, (double)bias);
 }
 
 __device__ __forceinline__ void put(const GemmParams& p, int64_t m, int64_t n, float v) {
@@ -175,8 +186,9 @@ __device__ __forceinline__ void to_type(float v, float& o) { o = v; }
 
 // The wave's TM x TN tiles: lane l holds row l % 32 and, in register 4 j + i, column
 // 8 j + 4 (l / 32) + i. STREAM (the forms for large y): stores that do not displace the operands from
-// L2 (16384 x 18560 x 4096: 1162 us, 1203 without).
-template <int TM, int TN, bool STREAM, typename T>
+// L2 (16384 x 18560 x 4096: 1162 us, 1203 without). WIDE: some of the wave's scales are not tame(); a form of its
+// own, so that the usual one carries none of its code.
+template <bool WIDE, int TM, int TN, bool STREAM, typename T>
 __device__ __forceinline__ void epilogue(const GemmParams& p, int8_t* sm, const float* s_sw, const float* s_bias,
                                          const v16i (&acc)[TM][TN], const float (&sa)[TM], int64_t mw, int64_t nw,
                                          int wave, int lane) {
@@ -196,10 +208,11 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, int8_t* sm, const 
         const float4 sw = *reinterpret_cast<const float4*>(s_sw + c), bn = *reinterpret_cast<const float4*>(s_bias + c);
         const v16i& d = acc[mt][nt];
         T o[4];
-        to_type(scaled(sa[mt], sw.x, d[4 * j], bn.x), o[0]);
-        to_type(scaled(sa[mt], sw.y, d[4 * j + 1], bn.y), o[1]);
-        to_type(scaled(sa[mt], sw.z, d[4 * j + 2], bn.z), o[2]);
-        to_type(scaled(sa[mt], sw.w, d[4 * j + 3], bn.w), o[3]);
+        constexpr auto f = WIDE ? scaled_wide : scaled;
+        to_type(f(sa[mt], sw.x, d[4 * j], bn.x), o[0]);
+        to_type(f(sa[mt], sw.y, d[4 * j + 1], bn.y), o[1]);
+        to_type(f(sa[mt], sw.z, d[4 * j + 2], bn.z), o[2]);
+        to_type(f(sa[mt], sw.w, d[4 * j + 3], bn.w), o[3]);
         __builtin_memcpy(__builtin_assume_aligned(buf + (lane & 31) * kRowB + c * sizeof(T), 8), o, 4 * sizeof(T));
       }
     wait_vm_lds<63>();  // the wave's own buffer: its LDS operations run in order
@@ -466,11 +479,25 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_w8a8_tile(GemmParams p) {
     }
     st = nx;
   }
+  const int64_t mw = m0 + wm * TM * 32, nw = n0 + wn * TN * 32;
+  s_sw += wn * TN * 32;
+  s_bias += wn * TN * 32;
+  bool all_tame = tame(s_sw[lane % (TN * 32)]);
+#pragma unroll
+  for (int mt = 0; mt < TM; ++mt) all_tame &= tame(sa[mt]);
+  const bool wide = __any(!all_tame);
   wait_vm_lds<0>();  // no direct load outlives the stages it writes
   __syncthreads();   // every wave is done with them: they become the waves' output buffers
-  const int64_t mw = m0 + wm * TM * 32, nw = n0 + wn * TN * 32;
-  if (p.yf16) epilogue<TM, TN, G::kBM == 256, __half>(p, sm, s_sw + wn * TN * 32, s_bias + wn * TN * 32, acc, sa, mw, nw, wave, lane);
-  else epilogue<TM, TN, G::kBM == 256, float>(p, sm, s_sw + wn * TN * 32, s_bias + wn * TN * 32, acc, sa, mw, nw, wave, lane);
+  const auto out = [&](auto w, auto t) {
+    epilogue<decltype(w)::value, TM, TN, G::kBM == 256, decltype(t)>(p, sm, s_sw, s_bias, acc, sa, mw, nw, wave, lane);
+  };
+  if (__builtin_expect(wide, 0)) {
+    if (p.yf16) out(std::true_type(), __half());
+    else out(std::true_type(), float());
+  } else {
+    if (p.yf16) out(std::false_type(), __half());
+    else out(std::false_type(), float());
+  }
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -642,11 +669,23 @@ __global__ __launch_bounds__(W * 64, 2) void k_gemm_w8a8_split(GemmParams p) {
 #pragma unroll
     for (int q = 1; q < W; ++q) v += *reinterpret_cast<const v4i*>(red + (q * BM + row) * G::kRow + col);
     const float sa = valid_or_zero(p.a_scales[p.per_row ? m : 0]);
+    float sw[4], bias[4], o[4];
+    bool all_tame = tame(sa);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int64_t n = n0 + col + k;
-      if (n < p.N) put(p, m, n, scaled(sa, valid_or_zero(p.w_scales[n]), v[k], p.bias ? p.bias[n] : 0.0f));
+      const int64_t n = min(n0 + col + k, p.N - 1);
+      sw[k] = valid_or_zero(p.w_scales[n]);
+      bias[k] = p.bias ? p.bias[n] : 0.0f;
+      all_tame &= tame(sw[k]);
+      o[k] = scaled(sa, sw[k], v[k], bias[k]);
     }
+    if (!all_tame) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = scaled_wide(sa, sw[k], v[k], bias[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (n0 + col + k < p.N) put(p, m, n0 + col + k, o[k]);
   }
 }
 
