@@ -463,8 +463,8 @@ qssm_status qssm_state_update_i8(const qssm_update_args* a, const int8_t* state_
  * or residual_out is QSSM_ERR_UNSUPPORTED.
  * A group with a NaN or an infinity has codes 0 (r is 0 or NaN there).
  * x and residual are fp32 or fp16, the gate too; rows of each tensor lie `*_stride` elements apart
- * (>= D), so a slice of a wider tensor's columns can be given.
- * Supported: D <= 8192; up to 32768 when D / norm_groups is a multiple of 8, every stride a multiple
+ * (>= D, <= 2^40, and <= 2^58 / rows), so a slice of a wider tensor's columns can be given.
+ * Supported: rows <= 2^31 - 1; D <= 8192; up to 32768 when D / norm_groups is a multiple of 8, every stride a multiple
  * of 8, q 8-byte aligned and the other tensors 16-byte aligned (the form with wide loads). Every tensor
  * is aligned to its type, and q overlaps no input.
  */

@@ -374,14 +374,15 @@ extern "C" qssm_status qssm_rmsnorm_i8(const qssm_rmsnorm_args* a, hipStream_t s
     return fail(QSSM_ERR_UNSUPPORTED, "a gate together with a residual stream");
   if (!(a->eps >= 0.0f) || a->eps > 3.402823466e38f)
     return fail(QSSM_ERR_INVALID_ARG, "eps must be finite and >= 0");
-  const int64_t lim = (int64_t)1 << 40;  // row offsets stay far inside 64 bits
+  // row offsets in bytes stay inside 64 bits
+  const int64_t lim = std::min((int64_t)1 << 40, ((int64_t)1 << 58) / std::max<int64_t>(M, 1));
   if (a->x_stride < D || a->q_stride < D || (a->residual && a->residual_stride < D) ||
       (a->residual_out && a->residual_out_stride < D) || (a->gate && a->gate_stride < D))
     return fail(QSSM_ERR_INVALID_ARG, "a row stride is smaller than dim");
   if (a->x_stride > lim || a->q_stride > lim || (a->residual && a->residual_stride > lim) ||
       (a->residual_out && a->residual_out_stride > lim) || (a->gate && a->gate_stride > lim) ||
       M > 0x7fffffff)
-    return fail(QSSM_ERR_UNSUPPORTED, "rows above 2^31 - 1 or a stride above 2^40");
+    return fail(QSSM_ERR_UNSUPPORTED, "rows above 2^31 - 1, a stride above 2^40 or rows * stride above 2^58");
   if (a->residual && a->residual == a->residual_out && a->residual_stride != a->residual_out_stride)
     return fail(QSSM_ERR_INVALID_ARG, "residual_out == residual needs one stride");
   const int64_t Dg = D / a->norm_groups;
