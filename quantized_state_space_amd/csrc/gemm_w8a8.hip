@@ -766,9 +766,11 @@ extern "C" qssm_status qssm_gemm_w8a8(const qssm_gemm_w8a8_args* a, hipStream_t 
   if (K > 131071) return fail(QSSM_ERR_UNSUPPORTED, "K above 131071 (int32 sums)");
   if (a->a_stride < K || a->w_stride < K || a->y_stride < N)
     return fail(QSSM_ERR_INVALID_ARG, "a row stride is smaller than the row");
-  const int64_t lim = (int64_t)1 << 40;  // row offsets stay far inside 64 bits
+  const int64_t lim = (int64_t)1 << 40;
   if (a->a_stride > lim || a->w_stride > lim || a->y_stride > lim || M > (1 << 27) || N > (1 << 27))
     return fail(QSSM_ERR_UNSUPPORTED, "M or N above 2^27 or a stride above 2^40");
+  if (a->y_stride > ((int64_t)1 << 58) / std::max<int64_t>(M, 1))  // row offsets in bytes stay inside 64 bits
+    return fail(QSSM_ERR_UNSUPPORTED, "M * y_stride above 2^58");
   if (M == 0 || N == 0) return QSSM_OK;
   if (!a->a_scales || !a->w_scales || !a->y || (K > 0 && (!a->a || !a->w)))
     return fail(QSSM_ERR_INVALID_ARG, "null required pointer");
