@@ -458,15 +458,17 @@ qssm_status qssm_state_update_i8(const qssm_update_args* a, const int8_t* state_
  *     fl32(absmax * fl32(1/127)) of the row's largest finite |v| (absmax 0: 1; clamped to
  *     [2^-100, 2^100]).
  * compute_scales == 0: scales [1] is an input, the static scale of every row.
- * residual_out (may be NULL) receives h; it may be residual itself (then with the same stride). With
- * no residual it receives x in residual_dtype, and h is that value. A gate together with a residual
+ * residual_out (may be NULL) receives h; it may be residual itself (then with the same stride), or x
+ * itself where their types are one too. With no residual it receives x in residual_dtype, and h is that value. A gate together with a residual
  * or residual_out is QSSM_ERR_UNSUPPORTED.
  * A group with a NaN or an infinity has codes 0 (r is 0 or NaN there).
  * x and residual are fp32 or fp16, the gate too; rows of each tensor lie `*_stride` elements apart
  * (>= D, <= 2^40, and <= 2^58 / rows), so a slice of a wider tensor's columns can be given.
  * Supported: rows <= 2^31 - 1; D <= 8192; up to 32768 when D / norm_groups is a multiple of 8, every stride a multiple
  * of 8, q 8-byte aligned and the other tensors 16-byte aligned (the form with wide loads). Every tensor
- * is aligned to its type, and q overlaps no input.
+ * is aligned to its type. q, residual_out and written scales overlap no other tensor (columns of one
+ * wider tensor do not overlap; with different strides their rows have to be apart modulo the
+ * strides' greatest common divisor), but for residual_out as above.
  */
 typedef struct qssm_rmsnorm_args {
   int64_t rows, dim;

@@ -5,6 +5,9 @@
 #include <hip/hip_fp16.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <numeric>
+
 #include "qssm.h"
 
 namespace qssm {
@@ -18,6 +21,33 @@ qssm_status launch_status(const char* what);
 
 // Ceil division for launch geometry.
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Where a tensor lies: `rows` rows of `width` bytes, `stride` bytes apart (at least the width).
+struct Span {
+  const void* p;
+  int64_t rows, stride, width;
+};
+
+inline Span flat(const void* p, int64_t bytes) { return Span{p, 1, bytes, bytes}; }
+
+// Whether a row of a shares a byte with a row of b (a tensor that is null or empty shares none). Exact where the
+// strides are equal or a tensor has one row. Tensors of two strides whose ranges meet are apart if their rows
+// are modulo the strides' greatest common divisor (columns of wider tensors), and taken to overlap otherwise.
+inline bool overlap(Span a, Span b) {
+  if (!a.p || !b.p || a.rows * a.width == 0 || b.rows * b.width == 0) return false;
+  const int64_t d = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);
+  if (d >= (a.rows - 1) * a.stride + a.width || -d >= (b.rows - 1) * b.stride + b.width) return false;
+  if (a.rows == 1) a.stride = b.stride;
+  if (b.rows == 1) b.stride = a.stride;
+  if (a.stride == b.stride) {
+    // row j of b and row i of a meet where -b.width < d + (j - i) stride < a.width: the least such j - i
+    const int64_t s = a.stride, low = -b.width - d;
+    const int64_t k = std::max((low >= 0 ? low / s : -((s - 1 - low) / s)) + 1, 1 - a.rows);
+    return k <= b.rows - 1 && d + k * s < a.width;
+  }
+  const int64_t g = std::gcd(a.stride, b.stride), m = (d % g + g) % g;
+  return m < a.width || m + b.width > g;
+}
 
 // ---------------------------------------------------------------------------------------------
 // Device: the quantization rule.

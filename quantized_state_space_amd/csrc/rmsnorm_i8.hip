@@ -355,6 +355,25 @@ void launch_vec(const NormParams& p, int res, int gate, hipStream_t st) {
 
 bool dtype_ok(int32_t t) { return t == QSSM_F32 || t == QSSM_F16; }
 
+// A workgroup reads its row before it writes any of it, and another's row may be read after: an output is
+// apart from every other tensor, or residual_out is, element by element, residual or x.
+qssm_status check_apart(const qssm_rmsnorm_args* a) {
+  const int64_t M = a->rows, D = a->dim;
+  const int64_t xb = a->x_dtype == QSSM_F16 ? 2 : 4, rb = a->residual_dtype == QSSM_F16 ? 2 : 4,
+                zb = a->gate_dtype == QSSM_F16 ? 2 : 4;
+  const Span x{a->x, M, a->x_stride * xb, D * xb}, r{a->residual, M, a->residual_stride * rb, D * rb},
+      ro{a->residual_out, M, a->residual_out_stride * rb, D * rb}, z{a->gate, M, a->gate_stride * zb, D * zb},
+      q{a->q, M, a->q_stride, D}, w = flat(a->weight, D * 4), s = flat(a->scales, a->compute_scales ? M * 4 : 4);
+  const auto itself = [&](const Span& t) { return ro.p == t.p && ro.width == t.width && (M == 1 || ro.stride == t.stride); };
+  if (overlap(q, x) || overlap(q, r) || overlap(q, ro) || overlap(q, z) || overlap(q, w) || overlap(q, s))
+    return fail(QSSM_ERR_INVALID_ARG, "q overlaps another tensor");
+  if ((!itself(x) && overlap(ro, x)) || (!itself(r) && overlap(ro, r)) || overlap(ro, w) || overlap(ro, s))
+    return fail(QSSM_ERR_INVALID_ARG, "residual_out overlaps another tensor (it may be residual or x itself)");
+  if (a->compute_scales && (overlap(s, x) || overlap(s, r) || overlap(s, z) || overlap(s, w)))
+    return fail(QSSM_ERR_INVALID_ARG, "scales overlaps another tensor");
+  return QSSM_OK;
+}
+
 }  // namespace
 
 extern "C" qssm_status qssm_rmsnorm_i8(const qssm_rmsnorm_args* a, hipStream_t stream) {
@@ -402,6 +421,7 @@ extern "C" qssm_status qssm_rmsnorm_i8(const qssm_rmsnorm_args* a, hipStream_t s
       (stream_on && (off_type(a->residual, a->residual_dtype) || off_type(a->residual_out, a->residual_dtype))) ||
       (a->gate && off_type(a->gate, a->gate_dtype)))
     return fail(QSSM_ERR_INVALID_ARG, "a tensor is not aligned to its type");
+  if (qssm_status st = check_apart(a)) return st;
   NormParams p{M, (int32_t)D, (int32_t)Dg, a->norm_groups, a->compute_scales != 0,
                Dg > 1 ? (uint32_t)((((uint64_t)1 << 32) + Dg - 1) / Dg) : 0u, a->x, a->residual, a->residual_out,
                a->gate, a->x_stride, a->residual_stride, a->residual_out_stride, a->gate_stride,

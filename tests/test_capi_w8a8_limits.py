@@ -1,5 +1,8 @@
 """Limits of the W8A8 block's entry points that keep their address arithmetic inside 64 bits, and the tensors that they
 refuse for how they lie in memory. No GPU: every call here returns before any launch."""
+import ctypes
+
+import numpy as np
 import pytest
 
 import quantized_state_space_amd as qs
@@ -17,3 +20,53 @@ def test_norm_refuses_rows_past_64_bits(tensor):
 def test_gemm_refuses_rows_past_64_bits():
     for M, stride in ((2 ** 27, 2 ** 40), (2 ** 27, 2 ** 31 + 1), (2 ** 18 + 1, 2 ** 40)):
         assert gemm(M=M, y_stride=stride) == UNS and "2^58" in message(), (M, stride)
+
+
+def apart(n):
+    """Addresses of n tensors far from each other."""
+    return [(i + 1) << 32 for i in range(n)]
+
+
+def norm_at(**kw):
+    """A call on tensors apart from each other but for those given as (address, stride)."""
+    x, q, sc, res, ro, gate, w = apart(7)
+    a = dict(x=x, q=q, scales=sc, residual_dtype=qs.QSSM_F32, gate_dtype=qs.QSSM_F32)
+    for name, at in dict(residual=res, residual_out=ro, gate=gate, weight=w).items():
+        if name in kw and kw[name] is True:
+            a[name] = at
+            if name != "weight":
+                a[name + "_stride"] = 64
+    for k, v in kw.items():
+        if v is not True:
+            a[k] = v
+    return norm(**a)
+
+
+X, Q, SC, RES, RO, GATE, W = apart(7)
+
+
+@pytest.mark.parametrize("kw,word", [
+    # 4 rows of 64 fp32 values, 256 bytes apart: q's rows of 64 bytes
+    (dict(q=X), "q "), (dict(q=X + 1023), "q "), (dict(q=X - 255), "q "), (dict(residual=True, q=RES + 512), "q "),
+    (dict(gate=True, q=GATE + 255), "q "), (dict(weight=True, q=W + 255), "q "), (dict(q=SC - 255), "q "), (dict(q=SC + 15), "q "),
+    (dict(residual_out=True, q=RO + 1023), "q "), (dict(q=X + 255, q_stride=256), "q "), (dict(compute_scales=0, q=SC + 3), "q "),
+    # the stream over its own input, a row or an element off
+    (dict(residual=True, residual_out=RES + 256, residual_out_stride=64), "residual_out"),
+    (dict(residual=True, residual_out=RES - 256, residual_out_stride=64), "residual_out"),
+    (dict(residual=True, residual_out=RES + 4, residual_out_stride=64), "residual_out"),
+    (dict(residual=True, residual_out=RES - 4, residual_out_stride=64), "residual_out"),
+    (dict(residual=True, residual_out=RES + 1020, residual_out_stride=64), "residual_out"),
+    (dict(residual_out=X + 256, residual_out_stride=64), "residual_out"),
+    (dict(residual_out=X, residual_out_stride=128), "residual_out"),
+    (dict(residual_out=X, residual_out_stride=64, residual_dtype=qs.QSSM_F16), "residual_out"),
+    (dict(residual_out=X, residual_out_stride=128, residual_dtype=qs.QSSM_F16), "residual_out"),
+    (dict(weight=True, residual_out=W + 252, residual_out_stride=64), "residual_out"),
+    (dict(residual_out=SC - 1020, residual_out_stride=64), "residual_out"),
+    # columns of a tensor of 128 that meet by one element
+    (dict(x_stride=128, residual_out=X + 252, residual_out_stride=128), "residual_out"),
+    (dict(x_stride=128, residual_out=X - 252, residual_out_stride=128), "residual_out"),
+    # scales that are written
+    (dict(scales=X + 1020), "scales"), (dict(scales=X - 12), "scales"), (dict(residual=True, scales=RES + 4), "scales"),
+    (dict(gate=True, scales=GATE), "scales"), (dict(weight=True, scales=W + 252), "scales")])
+def test_norm_refuses_overlapping_tensors(kw, word):
+    assert norm_at(**kw) == INV and "overlap" in message() and message().startswith(word.strip()), message()
