@@ -508,7 +508,9 @@ qssm_status qssm_rmsnorm_i8(const qssm_rmsnorm_args* a, hipStream_t stream);
  * leave fp32's normal range, all of it is fp64 and the result is rounded to fp32. An fp16 y is rounded
  * once more. K == 0 gives y = bias. Any M, N >= 0, any alignment of a and w (addresses and strides
  * that are multiples of 4 bytes take the fast forms);
- * a_stride and w_stride at most 2^22, M and N at most 2^27, y_stride at most 2^40 and 2^58 / M.
+ * a_stride and w_stride at most 2^22, M and N at most 2^27, y_stride at most 2^40 and 2^58 / M. y
+ * overlaps no input (columns of one wider tensor do not overlap; with different strides, in bytes, the
+ * rows have to be apart modulo the strides' greatest common divisor).
  */
 typedef struct qssm_gemm_w8a8_args {
   int64_t M, N, K;

@@ -781,6 +781,10 @@ extern "C" qssm_status qssm_gemm_w8a8(const qssm_gemm_w8a8_args* a, hipStream_t 
     return fail(QSSM_ERR_UNSUPPORTED, "a_stride or w_stride above 2^22");
   // a grid holds fewer than 2^32 threads, 512 a workgroup
   if (cdiv(M, 256) * cdiv(N, 128) >= kMaxTiles) return fail(QSSM_ERR_UNSUPPORTED, "M * N too large");
+  const Span y{a->y, M, a->y_stride * (a->y_dtype == QSSM_F16 ? 2 : 4), N * (a->y_dtype == QSSM_F16 ? 2 : 4)};
+  if (overlap(y, Span{a->a, M, a->a_stride, K}) || overlap(y, Span{a->w, N, a->w_stride, K}) || overlap(y, flat(a->bias, N * 4)) ||
+      overlap(y, flat(a->a_scales, a->a_per_row ? M * 4 : 4)) || overlap(y, flat(a->w_scales, N * 4)))
+    return fail(QSSM_ERR_INVALID_ARG, "y overlaps an input");
   const GemmParams p{M, N, K, a->a_per_row != 0, a->y_dtype == QSSM_F16, a->a, a->a_stride, a->a_scales,
                      a->w, a->w_stride, a->w_scales, a->bias, a->y, a->y_stride};
   // Direct loads take addresses that are multiples of 4 bytes; other rows, and in the tiles a K without a full

@@ -70,3 +70,18 @@ X, Q, SC, RES, RO, GATE, W = apart(7)
     (dict(gate=True, scales=GATE), "scales"), (dict(weight=True, scales=W + 252), "scales")])
 def test_norm_refuses_overlapping_tensors(kw, word):
     assert norm_at(**kw) == INV and "overlap" in message() and message().startswith(word.strip()), message()
+
+
+def gemm_at(**kw):
+    """M = 4, N = 8, K = 64 with y fp32 (rows of 32 bytes), every tensor apart but for those given."""
+    return gemm(**dict(dict(a=X, w=W, y=RO, a_scales=SC, w_scales=RES, bias=GATE), **kw))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(y=X), dict(y=X + 252), dict(y=X - 124), dict(y=W + 508), dict(y=W - 124), dict(y=SC + 12), dict(y=SC - 124),
+    dict(a_per_row=0, y=SC), dict(y=RES + 28), dict(y=RES - 124), dict(y=GATE + 28), dict(y=GATE - 124),
+    dict(y=X + 60, a_stride=128, y_stride=32),                 # columns of one tensor that meet by 4 bytes
+    dict(y=X + 64, a_stride=128, y_stride=16),                 # rows of y in the gap, but twice as many
+    dict(y=X + 62, y_dtype=qs.QSSM_F16, a_stride=80, y_stride=40)])
+def test_gemm_refuses_an_overlapping_y(kw):
+    assert gemm_at(**kw) == INV and "overlap" in message(), message()
