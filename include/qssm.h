@@ -464,11 +464,11 @@ qssm_status qssm_state_update_i8(const qssm_update_args* a, const int8_t* state_
  * A group with a NaN or an infinity has codes 0 (r is 0 or NaN there).
  * x and residual are fp32 or fp16, the gate too; rows of each tensor lie `*_stride` elements apart
  * (>= D, <= 2^40, and <= 2^58 / rows), so a slice of a wider tensor's columns can be given.
- * Supported: rows <= 2^31 - 1; D <= 8192; up to 32768 when D / norm_groups is a multiple of 8, every stride a multiple
- * of 8, q 8-byte aligned and the other tensors 16-byte aligned (the form with wide loads). Every tensor
- * is aligned to its type. q, residual_out and written scales overlap no other tensor (columns of one
- * wider tensor do not overlap; with different strides their rows have to be apart modulo the
- * strides' greatest common divisor), but for residual_out as above.
+ * Supported: rows <= 2^31 - 1; D <= 8192; up to 32768 when D / norm_groups is a multiple of 8, every
+ * stride a multiple of 8, q 8-byte aligned and the other tensors 16-byte aligned (the form with wide
+ * loads). Every tensor is aligned to its type. q, residual_out and written scales overlap no other
+ * tensor, but for residual_out as above (columns of one wider tensor do not overlap; with different
+ * strides, in bytes, the rows have to be apart modulo the strides' greatest common divisor).
  */
 typedef struct qssm_rmsnorm_args {
   int64_t rows, dim;
@@ -507,10 +507,10 @@ qssm_status qssm_rmsnorm_i8(const qssm_rmsnorm_args* a, hipStream_t stream);
  * fl32(sa * sw) and adds the bias; where sa or sw lies outside [2^-63, 2^63], so that their product could
  * leave fp32's normal range, all of it is fp64 and the result is rounded to fp32. An fp16 y is rounded
  * once more. K == 0 gives y = bias. Any M, N >= 0, any alignment of a and w (addresses and strides
- * that are multiples of 4 bytes take the fast forms);
- * a_stride and w_stride at most 2^22, M and N at most 2^27, y_stride at most 2^40 and 2^58 / M. y
- * overlaps no input (columns of one wider tensor do not overlap; with different strides, in bytes, the
- * rows have to be apart modulo the strides' greatest common divisor).
+ * that are multiples of 4 bytes take the fast forms), the other tensors aligned to their types;
+ * a_stride and w_stride at most 2^22, M and N at most 2^27, y_stride at most 2^40 and 2^58 / M.
+ * y overlaps no input (columns of one wider tensor do not overlap; with different strides, in bytes,
+ * the rows have to be apart modulo the strides' greatest common divisor).
  */
 typedef struct qssm_gemm_w8a8_args {
   int64_t M, N, K;

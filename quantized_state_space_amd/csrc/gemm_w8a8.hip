@@ -776,6 +776,8 @@ extern "C" qssm_status qssm_gemm_w8a8(const qssm_gemm_w8a8_args* a, hipStream_t 
     return fail(QSSM_ERR_INVALID_ARG, "null required pointer");
   if (((uintptr_t)a->y) % (a->y_dtype == QSSM_F16 ? 2 : 4) != 0)
     return fail(QSSM_ERR_INVALID_ARG, "y is not aligned to its type");
+  if (((uintptr_t)a->a_scales | (uintptr_t)a->w_scales | (uintptr_t)a->bias) % 4 != 0)
+    return fail(QSSM_ERR_INVALID_ARG, "a_scales, w_scales or bias is not aligned to its type");
   // 32-bit offsets inside a tile
   if (std::max(a->a_stride, a->w_stride) > (1 << 22))
     return fail(QSSM_ERR_UNSUPPORTED, "a_stride or w_stride above 2^22");

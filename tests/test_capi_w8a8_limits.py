@@ -85,3 +85,8 @@ def gemm_at(**kw):
     dict(y=X + 62, y_dtype=qs.QSSM_F16, a_stride=80, y_stride=40)])
 def test_gemm_refuses_an_overlapping_y(kw):
     assert gemm_at(**kw) == INV and "overlap" in message(), message()
+
+
+@pytest.mark.parametrize("kw", [dict(a_scales=SC + 2), dict(a_scales=SC + 1, a_per_row=0), dict(w_scales=RES + 2), dict(bias=GATE + 3)])
+def test_gemm_refuses_misaligned_scales(kw):
+    assert gemm_at(**kw) == INV and "aligned" in message(), message()
