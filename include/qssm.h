@@ -421,7 +421,7 @@ qssm_status qssm_state_update(const qssm_update_args* a, hipStream_t stream);
  * qssm_state_quant writes rows (h [rows, N] fp32 or fp16: a scan's h_last) to codes [rows, N] and
  * scales [rows]; qssm_state_dequant reads them back (out [rows, N] fp32 or fp16, e.g. the h0 of a
  * following scan); a row whose scale is not valid reads back as 0. Any rows >= 0, N >= 1 (at most
- * 2^31 - 1).
+ * 2^31 - 1); the three tensors do not overlap.
  */
 qssm_status qssm_state_quant(const void* h, int32_t h_dtype, int64_t rows, int64_t N, int8_t* codes,
                              float* scales, hipStream_t stream);

@@ -159,11 +159,14 @@ __global__ __launch_bounds__(kThreads) void k_state_dequant(const int8_t* codes,
   }
 }
 
-// The pointers of a call with rows: none null, the values and the scales aligned to their types.
-qssm_status check_tensors(const void* values, int32_t dtype, const int8_t* codes, const float* scales) {
+// The pointers of a call with rows: none null, the values and the scales aligned to their types, no two tensors
+// over each other (a row's codes are shorter than its values, so even in place they would lie over other rows').
+qssm_status check_tensors(const void* values, int32_t dtype, int64_t rows, int64_t N, const int8_t* codes, const float* scales) {
   if (!values || !codes || !scales) return fail(QSSM_ERR_INVALID_ARG, "null required pointer");
   if ((uintptr_t)values % (dtype == QSSM_F16 ? 2 : 4) != 0 || (uintptr_t)scales % 4 != 0)
     return fail(QSSM_ERR_INVALID_ARG, "a tensor is not aligned to its type");
+  const Span v = flat(values, rows * N * (dtype == QSSM_F16 ? 2 : 4)), c = flat(codes, rows * N), s = flat(scales, rows * 4);
+  if (overlap(v, c) || overlap(v, s) || overlap(c, s)) return fail(QSSM_ERR_INVALID_ARG, "two of the tensors overlap");
   return QSSM_OK;
 }
 
@@ -213,7 +216,7 @@ extern "C" qssm_status qssm_state_quant(const void* h, int32_t h_dtype, int64_t 
   clear_error();
   if (qssm_status st = check(h_dtype, rows, N)) return st;
   if (rows == 0) return QSSM_OK;
-  if (qssm_status st = check_tensors(h, h_dtype, codes, scales)) return st;
+  if (qssm_status st = check_tensors(h, h_dtype, rows, N, codes, scales)) return st;
   const bool f16 = h_dtype == QSSM_F16;
   if (const int L = lanes_of(rows, N, h, h_dtype, codes)) {
     with_lanes(L, [&](auto l) {
@@ -234,7 +237,7 @@ extern "C" qssm_status qssm_state_dequant(const int8_t* codes, const float* scal
   clear_error();
   if (qssm_status st = check(out_dtype, rows, N)) return st;
   if (rows == 0) return QSSM_OK;
-  if (qssm_status st = check_tensors(out, out_dtype, codes, scales)) return st;
+  if (qssm_status st = check_tensors(out, out_dtype, rows, N, codes, scales)) return st;
   const bool f16 = out_dtype == QSSM_F16;
   if (const int L = lanes_of(rows, N, out, out_dtype, codes)) {
     with_lanes(L, [&](auto l) {

@@ -90,3 +90,13 @@ def test_gemm_refuses_an_overlapping_y(kw):
 @pytest.mark.parametrize("kw", [dict(a_scales=SC + 2), dict(a_scales=SC + 1, a_per_row=0), dict(w_scales=RES + 2), dict(bias=GATE + 3)])
 def test_gemm_refuses_misaligned_scales(kw):
     assert gemm_at(**kw) == INV and "aligned" in message(), message()
+
+
+@pytest.mark.parametrize("dtype,size", [(qs.QSSM_F32, 4), (qs.QSSM_F16, 2)])
+def test_state_rows_refuse_overlapping_tensors(dtype, size):
+    """10 rows of 16 values, their codes (160 bytes) and scales (40 bytes)."""
+    at, lib = ctypes.c_void_p, qs.load()
+    for v, c, s in ((X, X, SC), (X, X + 160 * size - 1, SC), (X, X - 159, SC), (X, Q, X + 160 * size - 4), (X, Q, X - 36),
+                    (X, Q, Q + 156), (X, Q, Q - 36)):
+        assert lib.qssm_state_quant(at(v), dtype, 10, 16, at(c), at(s), None) == INV and "overlap" in message()
+        assert lib.qssm_state_dequant(at(c), at(s), 10, 16, at(v), dtype, None) == INV and "overlap" in message()
