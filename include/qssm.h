@@ -432,7 +432,8 @@ qssm_status qssm_state_dequant(const int8_t* codes, const float* scales, int64_t
  * state = the codes [B, nh, P, N] written; state_scales [B, nh, P] receives the new row scales.
  * state_in and scales_in are the codes and scales read: both NULL updates state and state_scales in
  * place; given, they are left as they were (a caller that may take a token back keeps them). They
- * may be a->state and state_scales themselves, else the two must not overlap.
+ * may be a->state and state_scales themselves; else what is read, the codes written and the scales
+ * written must not overlap.
  * Per row, with dA = fl32(exp(fl32(delta * A[h]))) (exp in fp64) and every value fp32:
  *     h[n] = fma(fl(dA * s), q[n], fl(fl(delta * xh) * Bh[n]))      (one rounding; s invalid: 0)
  *     y = sum_n Ch[n] * h[n] + Dskip[h] * xh         (h before it is rounded to codes)

@@ -442,13 +442,12 @@ extern "C" qssm_status qssm_state_update_i8(const qssm_update_args* a, const int
   if (a->batch * a->nheads > ((int64_t)1 << 38) / a->headdim)
     return fail(QSSM_ERR_UNSUPPORTED, "batch * nheads * headdim above 2^38");
   // read and written ranges are one or apart: a row half over another's would be read after its write
-  const auto overlap = [](const void* in, const void* out, int64_t bytes) {
-    const uintptr_t i = (uintptr_t)in, o = (uintptr_t)out;
-    return in && i != o && (i < o ? o - i : i - o) < (uintptr_t)bytes;
-  };
   const int64_t rows = a->batch * a->nheads * a->headdim;
-  if (overlap(state_in, a->state, rows * a->dstate) || overlap(scales_in, state_scales, rows * 4))
+  const Span q = flat(a->state, rows * a->dstate), s = flat(state_scales, rows * 4),
+             qi = flat(state_in, rows * a->dstate), si = flat(scales_in, rows * 4);
+  if ((qi.p != q.p && overlap(qi, q)) || (si.p != s.p && overlap(si, s)) || overlap(qi, s) || overlap(si, q))
     return fail(QSSM_ERR_INVALID_ARG, "state_in or scales_in overlaps what is written");
+  if (overlap(q, s)) return fail(QSSM_ERR_INVALID_ARG, "state and state_scales overlap");
   const UpdParams p = params_of(a);
   int8_t* out = reinterpret_cast<int8_t*>(a->state);
   const StateI8 st{state_in ? state_in : out, scales_in ? scales_in : state_scales, out, state_scales, 0, 0};

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 import quantized_state_space_amd as qs
-from tests.test_capi_w8a8 import INV, P, UNS, gemm, message, norm
+from tests.test_capi_w8a8 import INV, P, UNS, gemm, message, norm, update
 
 
 @pytest.mark.parametrize("tensor", ["x", "q", "residual", "residual_out", "gate"])
@@ -100,3 +100,13 @@ def test_state_rows_refuse_overlapping_tensors(dtype, size):
                     (X, Q, Q + 156), (X, Q, Q - 36)):
         assert lib.qssm_state_quant(at(v), dtype, 10, 16, at(c), at(s), None) == INV and "overlap" in message()
         assert lib.qssm_state_dequant(at(c), at(s), 10, 16, at(v), dtype, None) == INV and "overlap" in message()
+
+
+def test_state_update_refuses_codes_over_scales():
+    """16 rows of 16 codes (256 bytes) and their scales (64 bytes), in or out."""
+    at = ctypes.c_void_p
+    for off in (-60, 0, 252):
+        assert update(state=at(X), state_scales=at(X + off)) == INV and "overlap" in message()
+        assert update(state=at(X), state_scales=at(SC), state_in=at(Q), scales_in=at(X + off)) == INV and "overlap" in message()
+    for off in (-240, 0, 48):
+        assert update(state=at(X), state_scales=at(SC), state_in=at(SC + off), scales_in=at(Q)) == INV and "overlap" in message()
