@@ -100,9 +100,9 @@ __device__ __forceinline__ void round_store(__amdgpu_buffer_rsrc_t r, int c, flo
     else __builtin_amdgcn_raw_buffer_store_b16((unsigned short)w[0], r, c * 2, 0, 0);
   } else {
     if constexpr (VEC == 8) {
-      const int* w = reinterpret_cast<const int*>(v);
-      __builtin_amdgcn_raw_buffer_store_b128(v4i{w[0], w[1], w[2], w[3]}, r, c * 4, 0, 0);
-      __builtin_amdgcn_raw_buffer_store_b128(v4i{w[4], w[5], w[6], w[7]}, r, c * 4 + 16, 0, 0);
+      const auto bits = [&](int k) { return __builtin_bit_cast(int, v[k]); };
+      __builtin_amdgcn_raw_buffer_store_b128(v4i{bits(0), bits(1), bits(2), bits(3)}, r, c * 4, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(v4i{bits(4), bits(5), bits(6), bits(7)}, r, c * 4 + 16, 0, 0);
     } else {
       __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, v[0]), r, c * 4, 0, 0);
     }
@@ -236,11 +236,12 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
       }
 #pragma unroll
       for (int off = 32; off > 0; off >>= 1) a += __shfl_xor(a, off, 64);
-      // every lane's reads precede: the shuffles wait for all of them
+      // every lane's reads precede: the shuffles wait for all of them (r as the double's low word: the
+      // array keeps one type)
       if (lane == 0) {
         const float r = group_r(a, p.Dg, p.eps);
         if constexpr (VEC == 1) reinterpret_cast<float*>(smem)[g * per] = r;
-        else reinterpret_cast<float*>(smem)[2 * g * per] = r;
+        else reinterpret_cast<double*>(smem)[g * per] = __builtin_bit_cast(double, (uint64_t)__builtin_bit_cast(uint32_t, r));
       }
     }
     __syncthreads();
@@ -262,7 +263,8 @@ __global__ __launch_bounds__(kMaxThreads) void k_rmsnorm_i8(NormParams p) {
     if (p.Gn > 1) {
       const int cc = min(c, p.D - VEC);  // (past D: any group's)
       const int g = p.Dg > 1 ? (int)__umulhi((uint32_t)cc, p.inv_dg) : cc, per = p.Dg / VEC;
-      r = reinterpret_cast<const float*>(smem)[VEC == 1 ? g * per : 2 * g * per];
+      if constexpr (VEC == 1) r = reinterpret_cast<const float*>(smem)[g * per];
+      else r = __builtin_bit_cast(float, (uint32_t)__builtin_bit_cast(uint64_t, reinterpret_cast<const double*>(smem)[g * per]));
     }
 #pragma unroll
     for (int k = 0; k < VEC; ++k) t[v][k] *= r;
