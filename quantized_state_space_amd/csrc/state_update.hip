@@ -211,6 +211,9 @@ __device__ __forceinline__ float row_max(float x) {
 
 template <int R>
 __global__ __launch_bounds__(kThreads) void k_state_update_i8(UpdParams p, StateI8 st) {
+  // products and sums round where the definition says (the new codes are fixed bit for bit); the fused ones are
+  // written as such
+#pragma clang fp contract(off)
   constexpr int N = 16 * R, kPass = kThreads / R, kBatch = 2;  // rows per pass, passes in flight
   __shared__ __align__(16) float bs[N], cs[N];
   __shared__ __align__(16) float4 rowc[kMaxRows];
