@@ -631,6 +631,9 @@ def rmsnorm_args(x, q, scales, weight=None, eps=1e-5, residual=None, residual_ou
         raise ValueError("scales must be [M], or [1] with compute_scales False")
     if weight is not None and weight.numel() != D:
         raise ValueError("weight must be [D]")
+    if int(norm_groups) != norm_groups or not 1 <= norm_groups <= max(D, 1):
+        # (the argument block's field holds 32 bits)
+        raise ValueError("norm_groups must be a whole number in 1 .. D")
     px, xs = _rows(x, None, "x", (M, D))
     pr, rs = _rows(residual, None, "residual", (M, D), True)
     po, ros = _rows(residual_out, None, "residual_out", (M, D), True)

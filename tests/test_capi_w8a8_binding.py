@@ -26,3 +26,12 @@ def test_update_args_refuses_tensors_of_other_sizes(name, label, shape):
     t[name] = torch.zeros(shape, dtype=t[name].dtype)
     with pytest.raises(ValueError, match=f"^{label} must have shape"):
         qs.update_args(**t)
+
+
+@pytest.mark.parametrize("groups,error", [(0, ValueError), (-1, ValueError), (65, ValueError), (2 ** 32 + 1, ValueError),
+                                          (2 ** 40 + 2, ValueError), (2.5, ValueError), (None, TypeError)])
+def test_norm_refuses_group_counts(groups, error):
+    """Among them counts that a 32-bit field or a conversion would turn into another one."""
+    with pytest.raises(error) as e:
+        qs.rmsnorm_args(torch.zeros(4, 64), torch.zeros(4, 64, dtype=I8), torch.zeros(4), norm_groups=groups)
+    assert "GPU" not in str(e.value)
