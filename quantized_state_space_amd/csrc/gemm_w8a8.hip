@@ -9,14 +9,14 @@
 //
 // Tiles shared by a workgroup's waves with K in common steps (k_gemm_w8a8_tile, with a variant for rows
 // at any address), and the smallest tiles with K split over the waves (k_gemm_w8a8_split: few tokens,
-// bound by the bytes of the weights and by latency). choose() picks by estimated time.
+// bound by the bytes of the weights and by latency). choose_form() picks by estimated time.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <cmath>
 #include <type_traits>
 
 #include "common.hpp"
+#include "gemm_w8a8_forms.hpp"
 
 using namespace qssm;
 
@@ -690,50 +690,6 @@ __global__ __launch_bounds__(W * 64, 2) void k_gemm_w8a8_split(GemmParams p) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// The form for a shape, by estimated time (us): a tile costs tile + step * (steps of 64 codes of K) of
-// its CU when it shares it, tile_alone + step_alone * steps when the last round leaves it alone there;
-// the whole at least the bytes at 4.3 TB/s. The constants follow a fit (16 % rms) to 30 shapes of 1 .. 16384
-// tokens, N = 1024 .. 18560 and K = 128 .. 8192 in every form; they named the fastest form at 27 of them
-// and one within 3 to 14 % of it at the others. Measured, e.g. (256x256 / 256x128 / 128x128 / 128x64 /
-// 64x64 / split 32x32):
-//   64 x 4096 x 8192      69 / 38 / 30 / 21 / 18 / 9.3      256 x 4096 x 8192   72 / 40 / 31 / 22 / 18 / 25 (deep 64x64: 16.4)
-//   1000 x 1536 x 768     13 / 8.8 / 7.4 / 5.8 / 5.7 / 13   256 x 18560 x 4096  56 / 33 / 47 / 45 / 46 / 88
-//   1024 x 4096 x 4096    40 / 24 / 21 / 24 / 30 / 62       4096 x 4096 x 4096  58 / 66 / 82 / 90 / 111 / 294
-enum Form { TILE256, TILE256X128, TILE128, TILE128X64, TILE64, SPLIT32, TILE64DEEP, FORMS };
-struct Cost {
-  int bm, bn, per_cu;
-  double tile, step, tile_alone, step_alone;
-};
-constexpr Cost kCost[FORMS] = {{256, 256, 1, 0.0, 0.68, 6.0, 0.591},    {256, 128, 1, 4.31, 0.321, 4.31, 0.321},
-                               {128, 128, 1, 3.93, 0.231, 3.93, 0.231}, {128, 64, 2, 1.48, 0.164, 2.56, 0.156},
-                               {64, 64, 3, 0.87, 0.104, 1.65, 0.111},   {32, 32, 2, 1.26, 0.048, 1.26, 0.048},
-                               {64, 64, 1, 1.0, 0.132, 1.0, 0.101}};
-
-constexpr int64_t kMaxTiles = ((int64_t)1 << 23) - 8;
-
-// The cheapest of the first n forms.
-Form choose(const GemmParams& p, int n) {
-  constexpr double kCus = 256.0;
-  const double steps = (double)cdiv(p.K, 64);
-  const double bytes = ((double)p.M + (double)p.N) * (double)p.K + (p.yf16 ? 2.0 : 4.0) * (double)p.M * (double)p.N;
-  int best = -1;
-  double least = 0.0;
-  for (int f = 0; f < n; ++f) {
-    const Cost& c = kCost[f];
-    const double tiles = (double)cdiv(p.M, c.bm) * (double)cdiv(p.N, c.bn), slots = kCus * c.per_cu;
-    if (tiles >= (double)kMaxTiles) continue;
-    const double busy = c.tile + c.step * steps, alone = c.tile_alone + c.step_alone * steps;
-    const double rounds = std::ceil(tiles / slots) - 1.0, on_cu = std::ceil((tiles - rounds * slots) / kCus);
-    const double last = on_cu <= 1.0 ? alone : std::max(alone, busy * on_cu);
-    const double t = std::max(rounds * c.per_cu * busy + last, bytes / 4.3e6);
-    if (best < 0 || t < least) {
-      least = t;
-      best = f;
-    }
-  }
-  return (Form)best;
-}
-
 unsigned grid_of(const GemmParams& p, int bm, int bn) { return (unsigned)(cdiv(cdiv(p.M, bm) * cdiv(p.N, bn), 8) * 8); }
 
 template <bool SHIFT>
@@ -789,19 +745,14 @@ extern "C" qssm_status qssm_gemm_w8a8(const qssm_gemm_w8a8_args* a, hipStream_t 
     return fail(QSSM_ERR_INVALID_ARG, "y overlaps an input");
   const GemmParams p{M, N, K, a->a_per_row != 0, a->y_dtype == QSSM_F16, a->a, a->a_stride, a->a_scales,
                      a->w, a->w_stride, a->w_scales, a->bias, a->y, a->y_stride};
-  // Direct loads take addresses that are multiples of 4 bytes; other rows, and in the tiles a K without a full
-  // step, take the shifted forms. The split form needs K >= 16 (1 x 1000 x 64: 3.8 us, a shifted tile 4.5).
   const bool direct = ((uintptr_t)a->a | (uintptr_t)a->w | (uintptr_t)a->a_stride | (uintptr_t)a->w_stride) % 4 == 0;
-  const Form form = choose(p, direct && K >= 128 ? FORMS : K >= 16 ? TILE64DEEP : SPLIT32);
+  const auto [form, shift] = choose_form(M, N, K, p.yf16, direct);
   if (form == SPLIT32) {
     // up to 16 tokens load only 16 of a tile's 32 rows (8 tokens x 18560 x 4096: 18.9 us, 19.9 with all)
-    if (M <= 16) direct ? launch_split<16, false>(p, stream) : launch_split<16, true>(p, stream);
-    else direct ? launch_split<32, false>(p, stream) : launch_split<32, true>(p, stream);
-  } else if (!direct || K < 128) {
-    // the shifted tiles at the same estimates: the fastest or within 6 % of it in 12 shapes of 1 .. 16384 tokens
-    launch_tile<true>(form, p, stream);
+    if (M <= 16) shift ? launch_split<16, true>(p, stream) : launch_split<16, false>(p, stream);
+    else shift ? launch_split<32, true>(p, stream) : launch_split<32, false>(p, stream);
   } else {
-    launch_tile<false>(form, p, stream);
+    shift ? launch_tile<true>(form, p, stream) : launch_tile<false>(form, p, stream);
   }
   return launch_status("gemm_w8a8");
 }
