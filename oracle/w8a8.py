@@ -81,6 +81,21 @@ def gemm_w8a8(a, a_scales, w, w_scales, bias=None):
     return y if bias is None else y + np.asarray(bias, np.float64)
 
 
+def fma32(a, b, c):
+    """fl32(a b + c) of fp32 values, rounded once. The product is exact in fp64 where its factors' bits are at most 53; the sum
+    is rounded to odd there (its last bit set where it is not exact), which no tie of the rounding to fp32 survives."""
+    a, b, c = (np.asarray(v, np.float32).astype(np.float64) for v in np.broadcast_arrays(a, b, c))
+    with np.errstate(over="ignore", invalid="ignore"):
+        p = a * b
+        s = p + c
+        t = s - p
+        e = (p - (s - t)) + (c - t)  # the sum's error, exactly
+    bits = s.view(np.int64).copy()
+    fix = np.isfinite(s) & (e != 0) & ((bits & 1) == 0)
+    bits[fix] += np.where((e[fix] > 0) == (s[fix] > 0), 1, -1)
+    return f32(bits.view(np.float64))
+
+
 def state_update(codes, scales, xh, Bh, Ch, delta, A, D=None):
     """One decode step on the int8 state: codes [B, nh, P, N], scales [B, nh, P]; xh [B, nh, P], Bh and
     Ch [B, nh, N] dequantized fp32 values (each head's group). Returns y (fp64), codes, scales, h."""
@@ -88,7 +103,7 @@ def state_update(codes, scales, xh, Bh, Ch, delta, A, D=None):
     dA = f32(np.exp((d * np.asarray(A, np.float32)).astype(np.float64)))
     keep = dA[:, :, None] * np.where(scale_ok(scales), scales, np.float32(0))
     add = (d[:, :, None] * xh)[..., None] * Bh[:, :, None, :]
-    h = f32(keep.astype(np.float64)[..., None] * codes + add.astype(np.float64))
+    h = fma32(keep[..., None], codes.astype(np.float32), add)
     y = (h.astype(np.float64) * Ch[:, :, None, :].astype(np.float64)).sum(axis=3)
     if D is not None:
         y = y + np.asarray(D, np.float64)[None, :, None] * xh
