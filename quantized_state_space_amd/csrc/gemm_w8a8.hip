@@ -155,8 +155,8 @@ __device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
 // read AHEAD slices of 32 codes ahead, and reads and loads are issued between the products.
 // AHEAD > 1 (small tiles, whose products are too few to cover an LDS read): the barrier then stands
 // where the fragments pass to the next step, and its step refills the stage before last; it pays with
-// many stages, which leave room for one tile per CU (256 x 4096 x 8192 in 64x64 tiles: 18.4 us with 3
-// stages, 18.0 with 6, 16.4 with 6 and AHEAD 3).
+// many stages, which leave room for one tile per CU (256 x 4096 x 8192 in 64x64 tiles: 18.1 us with 3
+// stages, 18.1 with 6, 16.0 with 6 and AHEAD 3).
 // Steps of 128 and few stages beat steps of 64 and twice the stages (half the barriers): 256x256 tiles,
 // 16384 x 18560 x 4096: 1069 us (2.33 POPS) and 1128; 128x64 tiles, 256 x 4096 x 8192: 22 and 27.
 // The many-token forms are bound by the power the matrix cores draw: with all operands 0 the same
@@ -165,7 +165,7 @@ __device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
 // zeros past K. Rows past M or N read the last row and are not stored.
 // Tile order: the tiles are cut into 8 contiguous ranges, one per XCD (workgroups are dealt to the
 // XCDs in turn), in groups of 4 row tiles, so the workgroups that run together on an XCD share rows
-// and columns in its L2 (16384 x 18560 x 4096: groups of 4 / 8 / 16 took 1151 / 1161 / 1195 us).
+// and columns in its L2 (16384 x 18560 x 4096: groups of 4 / 8 / 16 take 1029 / 1033 / 1049 us).
 // SHIFT: rows at any address, K of any length. Direct loads take multiples of 4 bytes, so a row lies in
 // LDS from the word on that holds its first code, 0 to 3 codes late, with the word behind each step's
 // BK bytes beside the stage; a fragment is its 16 bytes and the next word shifted into place (the sums
@@ -186,7 +186,7 @@ __device__ __forceinline__ void to_type(float v, float& o) { o = v; }
 
 // The wave's TM x TN tiles: lane l holds row l % 32 and, in register 4 j + i, column
 // 8 j + 4 (l / 32) + i. STREAM (the forms for large y): stores that do not displace the operands from
-// L2 (16384 x 18560 x 4096: 1162 us, 1203 without). WIDE: some of the wave's scales are not tame(); a form of its
+// L2 (16384 x 18560 x 4096: 1029 us, 1096 without). WIDE: some of the wave's scales are not tame(); a form of its
 // own, so that the usual one carries none of its code.
 template <bool WIDE, int TM, int TN, bool STREAM, typename T>
 __device__ __forceinline__ void epilogue(const GemmParams& p, int8_t* sm, const float* s_sw, const float* s_bias,
