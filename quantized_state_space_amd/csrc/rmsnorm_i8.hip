@@ -363,9 +363,12 @@ qssm_status check_apart(const qssm_rmsnorm_args* a) {
   const int64_t M = a->rows, D = a->dim;
   const int64_t xb = a->x_dtype == QSSM_F16 ? 2 : 4, rb = a->residual_dtype == QSSM_F16 ? 2 : 4,
                 zb = a->gate_dtype == QSSM_F16 ? 2 : 4;
-  const Span x{a->x, M, a->x_stride * xb, D * xb}, r{a->residual, M, a->residual_stride * rb, D * rb},
-      ro{a->residual_out, M, a->residual_out_stride * rb, D * rb}, z{a->gate, M, a->gate_stride * zb, D * zb},
-      q{a->q, M, a->q_stride, D}, w = flat(a->weight, D * 4), s = flat(a->scales, a->compute_scales ? M * 4 : 4);
+  const auto rows = [&](const void* t, int64_t stride, int64_t size) {  // (a null tensor's stride is not read)
+    return t ? Span{t, M, stride * size, D * size} : Span{};
+  };
+  const Span x = rows(a->x, a->x_stride, xb), r = rows(a->residual, a->residual_stride, rb),
+             ro = rows(a->residual_out, a->residual_out_stride, rb), z = rows(a->gate, a->gate_stride, zb),
+             q = rows(a->q, a->q_stride, 1), w = flat(a->weight, D * 4), s = flat(a->scales, a->compute_scales ? M * 4 : 4);
   const auto itself = [&](const Span& t) { return ro.p == t.p && ro.width == t.width && (M == 1 || ro.stride == t.stride); };
   if (overlap(q, x) || overlap(q, r) || overlap(q, ro) || overlap(q, z) || overlap(q, w) || overlap(q, s))
     return fail(QSSM_ERR_INVALID_ARG, "q overlaps another tensor");
