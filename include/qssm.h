@@ -17,7 +17,8 @@
  *    8-bit code (scale/4, scale, scale*4) with the mode in the top bits.
  *
  * Around the recurrence: the 4-bit and 8-bit linear layers, the root-mean-square norm that writes
- * their int8 input, and an int8 recurrent state for decoding.
+ * their int8 input, an int8 recurrent state for decoding, the short causal convolution in front of it,
+ * the unquantized scan over packed sequences, and the linear layer in block-scaled 8-bit floating point.
  *
  * The recurrence, per channel d and state n:
  *     h_t = exp(delta_t * A) * h_{t-1} + delta_t * B_t * x_t,     y_t = sum_n C_t * h_t + D * x_t
@@ -558,6 +559,169 @@ typedef struct qssm_gemm_args {
 qssm_status qssm_gemm_w4a8(const qssm_gemm_args* a, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * Packed sequences and their state cache, as qssm_causal_conv and qssm_selective_scan take them.
+ * The rows 0 .. tokens - 1 of the tensors hold nseq sequences one after the other:
+ *   seq_offsets (device int32 [nseq + 1], not decreasing): sequence i is the rows seq_offsets[i] ..
+ *     seq_offsets[i + 1] - 1; a sequence may be empty. Rows before the first and behind the last one are
+ *     neither read nor written. Values outside 0 .. tokens are taken as the nearest of the two.
+ *   seq_offsets NULL: nseq sequences of tokens / nseq rows each (tokens % nseq == 0). With one row each
+ *     (tokens == nseq) this is the decode step of nseq sequences, and runs as such.
+ * A sequence's state is row state_slots[i] (device int32 [nseq]; NULL: row i, and then slots >= nseq) of
+ * `state`, which is read, and of `state_out`, which is written; either may be NULL (nothing is read: the
+ * sequences start from zeros; nothing is written), and both may be one tensor (in place). A slot that is
+ * negative or not below `slots` reads zeros and writes nothing. Sequences of one call that have a slot
+ * have different ones. has_state (device uint8 [nseq], NULL: all 1): a sequence with 0 starts from zeros,
+ * whatever its slot holds. An empty sequence hands its initial state on. Slots of no sequence keep their contents.
+ * Rows of the 2-D tensors lie `*_stride` elements apart (at least a row, at most 2^40 and 2^58 / tokens),
+ * so columns of a wider tensor can be given. What is written overlaps nothing else, but for the states as above.
+ */
+
+/* ---------------------------------------------------------------------------------------------
+ * Short causal convolution, one filter per channel, with SiLU: what stands between the in-projection and
+ * the recurrence, for prompts and for single tokens.
+ * Quamba2, abstract (Mamba1 and Mamba2 blocks, prefill and generation).
+ *
+ * Per sequence, row t and channel c < dim, with x[t] for t < 0 the rows of the state (x[-1] its last):
+ *     v = bias[c] + sum_{k < width} weight[c, k] * x[t - (width - 1) + k, c],   y = v / (1 + e^-v) if silu, else v
+ * x is fp32 or fp16; weight [dim, width] and bias [dim] (NULL: 0) are fp32; 2 <= width <= 4.
+ * state [slots, width - 1, dim] of x's type holds the last width - 1 inputs, the oldest first, bit for bit.
+ * y is fp32 or fp16 (sum and SiLU in fp32), or int8 codes for a following W8A8 recurrence (QSSM_I8):
+ *     code = clamp(RNE(fl32(y) / s), -128, 127),  s = y_scales[y_group_of[c]]  by the quantization rule
+ * above, where y is the sum and SiLU in fp64; the codes do not depend on the order of the sum beyond
+ * ~2^-50. The y_* fields are read only for QSSM_I8. dim <= 2^24, nseq <= 2^24, tokens <= 2^31 - 64.
+ */
+typedef struct qssm_conv_args {
+  int64_t tokens, dim, nseq;
+  int32_t width, silu;
+  int32_t x_dtype;            /* QSSM_F32 or QSSM_F16 (x and both states) */
+  int32_t y_dtype;            /* QSSM_F32, QSSM_F16 or QSSM_I8 */
+  const int32_t* seq_offsets; /* [nseq + 1] or NULL */
+  const void* x;              /* [tokens, dim] */
+  int64_t x_stride;
+  const float* weight;        /* [dim, width] */
+  const float* bias;          /* [dim] or NULL */
+  void* y;                    /* [tokens, dim] */
+  int64_t y_stride;
+  const void* state;          /* [slots, width - 1, dim] or NULL */
+  void* state_out;            /* the same, or NULL; may be state */
+  int64_t slots;
+  const int32_t* state_slots; /* [nseq] or NULL */
+  const uint8_t* has_state;   /* [nseq] or NULL */
+  const uint8_t* y_group_of;  /* QSSM_I8: [dim] output group (< y_groups) of each channel */
+  const float* y_scales;      /* QSSM_I8: [y_groups] */
+  int32_t y_groups;           /* QSSM_I8: 1..256 */
+  int32_t reserved;           /* 0 */
+} qssm_conv_args;
+
+qssm_status qssm_causal_conv(const qssm_conv_args* a, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Selective scan on unquantized inputs over packed sequences (Mamba1): the recurrence of qssm_scan_w8a8 for
+ * layers that stay in fp16 or fp32, and the unquantized output that calibration compares the W8A8 one
+ * with; softplus, the skip and the gate are part of it, for prompts and for single tokens.
+ * Quamba2, abstract (the Mamba1 recurrence, prefill and generation).
+ *
+ * Per sequence, row t, channel d < dim and state n < dstate, with g = d / (dim / ngroups):
+ *     dt = softplus(delta[t, d] + delta_bias[d])      (delta_softplus; else the sum itself)
+ *     h[n] = exp(dt * A[d, n]) * h[n] + dt * x[t, d] * B[t, g * dstate + n]
+ *     y[t, d] = (sum_n C[t, g * dstate + n] * h[n] + Dskip[d] * x[t, d]) * silu(z[t, d])
+ * x, delta, z [tokens, dim] and B, C [tokens, ngroups * dstate] have one type (io_dtype, fp32 or fp16); z NULL: no
+ * gate. A [dim, dstate], Dskip [dim] (NULL: 0) and delta_bias [dim] (NULL: 0) are fp32. All arithmetic is
+ * fp32. The state [slots, dim, dstate] is fp32, or fp16, which is rounded to nearest even once per call
+ * and sequence (the decode cache in half the bytes; inside a call the state is fp32).
+ * Long sequences are cut into pieces that run in parallel: every piece but a sequence's last runs from
+ * zero, then every piece but the first again from its entering state, which is folded from the ends of
+ * the pieces before it (in their order, so results do not vary from call to call). How long the pieces
+ * are follows from the sizes alone; they meet the sequential results to fp32 rounding.
+ * Workspace: qssm_selective_scan_workspace_size bytes (0 when nothing is cut), 16-byte aligned; calls
+ * that overlap in time need their own.
+ * 1 <= dstate <= 64, dim <= 2^24, nseq <= 2^24, tokens <= 2^31 - 64, dim % ngroups == 0.
+ */
+typedef struct qssm_sscan_args {
+  int64_t tokens, dim, dstate, nseq;
+  int32_t ngroups;
+  int32_t io_dtype;           /* QSSM_F32 or QSSM_F16: x, delta, B, C, z */
+  int32_t y_dtype;            /* QSSM_F32 or QSSM_F16 */
+  int32_t state_dtype;        /* QSSM_F32 or QSSM_F16 */
+  int32_t delta_softplus;
+  int32_t reserved;           /* 0 */
+  const int32_t* seq_offsets; /* [nseq + 1] or NULL */
+  const void* x;              /* [tokens, dim] */
+  int64_t x_stride;
+  const void* delta;          /* [tokens, dim] */
+  int64_t delta_stride;
+  const void* B;              /* [tokens, ngroups * dstate] */
+  int64_t B_stride;
+  const void* C;              /* [tokens, ngroups * dstate] */
+  int64_t C_stride;
+  const void* z;              /* [tokens, dim] or NULL */
+  int64_t z_stride;
+  const float* A;             /* [dim, dstate] */
+  const float* Dskip;         /* [dim] or NULL */
+  const float* delta_bias;    /* [dim] or NULL */
+  void* y;                    /* [tokens, dim] */
+  int64_t y_stride;
+  const void* state;          /* [slots, dim, dstate] or NULL */
+  void* state_out;            /* the same, or NULL; may be state */
+  int64_t slots;
+  const int32_t* state_slots; /* [nseq] or NULL */
+  const uint8_t* has_state;   /* [nseq] or NULL */
+} qssm_sscan_args;
+
+size_t qssm_selective_scan_workspace_size(const qssm_sscan_args* a);
+qssm_status qssm_selective_scan(const qssm_sscan_args* a, void* workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * 8-bit floating point (e4m3: 4 significant bits, |values| up to 448, steps of at least 2^-9, bytes 0x7F and
+ * 0xFF are NaN) with one scale for each block of 128: activations per row and 128 columns, weights per 128 rows and
+ * 128 columns. For projections whose activations' range no single int8 scale covers.
+ * Quamba2, abstract (8-bit projections around the recurrence), with the block-wise code in the int8 one's place.
+ *
+ * qssm_quant_f8: codes [rows, K] of x (fp32 or fp16) and scales [ceil(K / 128), rows]:
+ *     s = fl32(absmax * fl32(1/448)), absmax the largest finite |x| of the row's 128 columns (absmax 0: s = 1;
+ *     clamped to [2^-60, 2^60]),  code = the e4m3 value nearest to x / s (the exact quotient, ties to
+ *     even), within +-448; a value that rounds to zero keeps its sign, NaN encodes as 0.
+ * The scale of row m and block b is scales[b * scales_stride + m]. codes and scales are fixed bit for bit.
+ * Rows of x and codes lie x_stride and codes_stride elements apart (>= K, at most 2^40 and 2^58 / rows);
+ * scales_stride >= rows, at most 2^40. rows <= 2^31 - 1, K <= 2^24. The outputs overlap nothing.
+ */
+qssm_status qssm_quant_f8(const void* x, int32_t x_dtype, int64_t rows, int64_t K, int64_t x_stride,
+                          uint8_t* codes, int64_t codes_stride, float* scales, int64_t scales_stride,
+                          hipStream_t stream);
+
+/* The linear layer on them:
+ *     y[m, n] = bias[n] + sum_b (sa[b, m] * sw[n / 128, b]) * (sum over the 128 k of block b of a[m, k] * w[n, k])
+ * a [M, K] and a_scales [ceil(K / 128), M] as qssm_quant_f8 writes them; w [N, K] and w_scales
+ * [ceil(N / 128), ceil(K / 128)] (contiguous) as qssm_quant_f8_weight does; bias [N] fp32 or NULL; y [M, N]
+ * fp32 or fp16. A block's products are exact and summed in fp32 for an fp32 y; for an fp16 y by the matrix cores' fp8
+ * instructions, which cut the smaller of 8 neighbouring products at 2^-13 of the largest one's power of two (about
+ * 1.4e-5 of the result; y's own rounding is 2^-11). The sum is scaled by fl32(sa * sw) and added to an fp32
+ * sum over the blocks. A scale is valid here when it is finite and in [2^-60, 2^60]; a block with another one counts
+ * as 0. A NaN code makes its row or column of y NaN, also there. K == 0 gives y = bias.
+ * Any M, N >= 0 and any alignment of a and w (addresses and strides that are multiples of 16 bytes take the
+ * fast forms); K <= 2^20; a_stride and w_stride at most 2^22, M and N at most 2^27, a_scales_stride and
+ * y_stride at most 2^40, y_stride at most 2^58 / M. y overlaps no input.
+ */
+typedef struct qssm_gemm_f8_args {
+  int64_t M, N, K;
+  int32_t y_dtype;          /* QSSM_F32 or QSSM_F16 */
+  int32_t reserved;         /* 0 */
+  const uint8_t* a;         /* [M, K] */
+  int64_t a_stride;         /* >= K */
+  const float* a_scales;    /* [ceil(K / 128), M] */
+  int64_t a_scales_stride;  /* >= M */
+  const uint8_t* w;         /* [N, K] */
+  int64_t w_stride;         /* >= K */
+  const float* w_scales;    /* [ceil(N / 128), ceil(K / 128)] */
+  const float* bias;        /* [N] or NULL */
+  void* y;                  /* [M, N] */
+  int64_t y_stride;         /* >= N */
+} qssm_gemm_f8_args;
+
+qssm_status qssm_gemm_f8(const qssm_gemm_f8_args* a, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Host-side offline calibration (CPU only; every pointer below is a HOST pointer).
  * Quamba2, method steps 1-2 (offline activation statistics; sort and cluster the x channels);
  * Quamba-SE, section 4.1 (L at the 5th and H at the 99.9th percentile, EMA with alpha = 0.1).
@@ -631,6 +795,12 @@ qssm_status qssm_quant_w4(const float* w, int64_t N, int64_t K, int32_t group, f
  * codes[n, k] = clamp(RNE(w / s), -128, 127) by the exact quotient (NaN -> 0, +-Inf saturate). */
 qssm_status qssm_quant_w8(const float* w, int64_t N, int64_t K, float* scales, int8_t* codes);
 
+/* Offline e4m3 weight quantization for qssm_gemm_f8 (host): for weights w [N, K] fp32, one scale per block of
+ * 128 rows and 128 columns (the last ones may be smaller), scales[ceil(N / 128), ceil(K / 128)] = fl32(absmax / 448)
+ * of the block's finite values (absmax 0 -> 1, clamped to [2^-60, 2^60]), and codes [N, K] the e4m3 values
+ * nearest to w / s (the exact quotient, ties to even), within +-448; NaN -> 0. */
+qssm_status qssm_quant_f8_weight(const float* w, int64_t N, int64_t K, float* scales, uint8_t* codes);
+
 /* ---------------------------------------------------------------------------------------------
  * Library information. */
 const char* qssm_status_string(qssm_status s);
@@ -638,7 +808,7 @@ const char* qssm_status_string(qssm_status s);
 const char* qssm_last_error(void);
 int32_t qssm_version(void);
 /* sizeof of the argument structs as compiled (0: scan, 1: s4d, 2: ssd, 3: update, 4: gemm, 5:
- * rmsnorm, 6: gemm_w8a8), so bindings can check their layout. Returns 0 for an unknown kind. */
+ * rmsnorm, 6: gemm_w8a8, 7: conv, 8: sscan, 9: gemm_f8), so bindings can check their layout. Returns 0 for an unknown kind. */
 size_t qssm_args_size(int32_t kind);
 
 /* ---------------------------------------------------------------------------------------------

@@ -89,8 +89,35 @@ class GemmW8A8Args(ctypes.Structure):
                 ("w_scales", _P), ("bias", _P), ("y", _P), ("y_stride", _I64)]
 
 
+class ConvArgs(ctypes.Structure):
+    _fields_ = [("tokens", _I64), ("dim", _I64), ("nseq", _I64), ("width", _I32), ("silu", _I32),
+                ("x_dtype", _I32), ("y_dtype", _I32), ("seq_offsets", _P), ("x", _P),
+                ("x_stride", _I64), ("weight", _P), ("bias", _P), ("y", _P), ("y_stride", _I64),
+                ("state", _P), ("state_out", _P), ("slots", _I64), ("state_slots", _P),
+                ("has_state", _P), ("y_group_of", _P), ("y_scales", _P), ("y_groups", _I32),
+                ("reserved", _I32)]
+
+
+class SscanArgs(ctypes.Structure):
+    _fields_ = [("tokens", _I64), ("dim", _I64), ("dstate", _I64), ("nseq", _I64),
+                ("ngroups", _I32), ("io_dtype", _I32), ("y_dtype", _I32), ("state_dtype", _I32),
+                ("delta_softplus", _I32), ("reserved", _I32), ("seq_offsets", _P), ("x", _P),
+                ("x_stride", _I64), ("delta", _P), ("delta_stride", _I64), ("B", _P),
+                ("B_stride", _I64), ("C", _P), ("C_stride", _I64), ("z", _P), ("z_stride", _I64),
+                ("A", _P), ("Dskip", _P), ("delta_bias", _P), ("y", _P), ("y_stride", _I64),
+                ("state", _P), ("state_out", _P), ("slots", _I64), ("state_slots", _P),
+                ("has_state", _P)]
+
+
+class GemmF8Args(ctypes.Structure):
+    _fields_ = [("M", _I64), ("N", _I64), ("K", _I64), ("y_dtype", _I32), ("reserved", _I32),
+                ("a", _P), ("a_stride", _I64), ("a_scales", _P), ("a_scales_stride", _I64),
+                ("w", _P), ("w_stride", _I64), ("w_scales", _P), ("bias", _P), ("y", _P),
+                ("y_stride", _I64)]
+
+
 ARG_STRUCTS = {0: ScanArgs, 1: S4dArgs, 2: SsdArgs, 3: UpdateArgs, 4: GemmArgs, 5: RmsnormArgs,
-               6: GemmW8A8Args}
+               6: GemmW8A8Args, 7: ConvArgs, 8: SscanArgs, 9: GemmF8Args}
 
 # Every symbol include/qssm.h declares, with its ctypes signature.
 SIGNATURES = {
@@ -115,6 +142,12 @@ SIGNATURES = {
     "qssm_rmsnorm_i8": (_I32, [ctypes.POINTER(RmsnormArgs), _P]),
     "qssm_gemm_w8a8": (_I32, [ctypes.POINTER(GemmW8A8Args), _P]),
     "qssm_quant_w8": (_I32, [_P, _I64, _I64, _P, _P]),
+    "qssm_causal_conv": (_I32, [ctypes.POINTER(ConvArgs), _P]),
+    "qssm_selective_scan_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(SscanArgs)]),
+    "qssm_selective_scan": (_I32, [ctypes.POINTER(SscanArgs), _P, ctypes.c_size_t, _P]),
+    "qssm_quant_f8": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _I64, _P]),
+    "qssm_gemm_f8": (_I32, [ctypes.POINTER(GemmF8Args), _P]),
+    "qssm_quant_f8_weight": (_I32, [_P, _I64, _I64, _P, _P]),
     "qssm_gemm_w4a8": (_I32, [ctypes.POINTER(GemmArgs), _P]),
     "qssm_quant_w4": (_I32, [_P, _I64, _I64, _I32, _P, _P]),
     "qssm_calib_channel_absmax": (_I32, [_P, _I64, _I64, _I64, _P]),
@@ -685,6 +718,173 @@ def qssm_gemm_w8a8(args, stream=None):
 
 
 # ------------------------------------------------------------------------------------------------
+# Packed sequences: causal convolution and selective scan
+
+def _sequences(tokens, row, state_dtypes, seq_offsets, nseq, state, state_out, state_slots, has_state):
+    """The fields of the packed sequences. row: the shape of a slot's state; state_dtypes: its types."""
+    torch = _t()
+    if seq_offsets is not None:
+        if seq_offsets.dim() != 1 or seq_offsets.numel() < 1:
+            raise ValueError("seq_offsets must be [nseq + 1]")
+        if nseq is not None and nseq != seq_offsets.numel() - 1:
+            raise ValueError("nseq and seq_offsets differ")
+        nseq = seq_offsets.numel() - 1
+    elif nseq is None:
+        raise ValueError("nseq or seq_offsets is required")
+    slots = 0
+    for t, name in ((state, "state"), (state_out, "state_out")):
+        if t is not None:
+            if t.dtype not in state_dtypes:
+                raise TypeError(f"{name} must be {' or '.join(map(str, state_dtypes))}, got {t.dtype}")
+            if t.dim() != 1 + len(row) or tuple(t.shape[1:]) != tuple(row):
+                raise ValueError(f"{name} must be [slots, {', '.join(map(str, row))}], got {tuple(t.shape)}")
+            slots = t.shape[0]
+    if state is not None and state_out is not None and (state.shape != state_out.shape or
+                                                        state.dtype != state_out.dtype):
+        raise ValueError("state and state_out must have one shape and type")
+    for t, name in ((state_slots, "state_slots"), (has_state, "has_state")):
+        if t is not None and t.numel() != nseq:
+            raise ValueError(f"{name} must have one entry per sequence")
+    return dict(nseq=int(nseq), seq_offsets=_ptr(seq_offsets, torch.int32, "seq_offsets", True),
+                state=_ptr(state, None, "state", True),
+                state_out=_ptr(state_out, None, "state_out", True), slots=slots,
+                state_slots=_ptr(state_slots, torch.int32, "state_slots", True),
+                has_state=_ptr(has_state, torch.uint8, "has_state", True))
+
+
+def causal_conv_args(x, weight, y, bias=None, silu=True, seq_offsets=None, nseq=None, state=None,
+                     state_out=None, state_slots=None, has_state=None, y_group_of=None, y_scales=None):
+    """x [T, C] float32 or float16 (rows may lie apart, as columns of a wider tensor do); weight float32
+    [C, W], bias float32 [C]; y [T, C] float32, float16, or int8 with y_group_of uint8 [C] and y_scales
+    float32 [G]. The rows are the sequences of seq_offsets int32 [nseq + 1], or nseq equal ones. state
+    (read) and state_out (written; may be state) [slots, W - 1, C] of x's type; state_slots int32 [nseq];
+    has_state uint8 [nseq]."""
+    torch = _t()
+    if x.dim() != 2 or weight.dim() != 2 or weight.shape[0] != x.shape[1]:
+        raise ValueError("x must be [T, C] and weight [C, W]")
+    (T, C), W = x.shape, weight.shape[1]
+    if bias is not None and bias.numel() != C:
+        raise ValueError("bias must be [C]")
+    i8 = y.dtype == torch.int8
+    if i8 and (y_group_of is None or y_scales is None or y_group_of.numel() != C):
+        raise ValueError("an int8 y needs y_group_of [C] and y_scales")
+    seqs = _sequences(T, (W - 1, C), (x.dtype,), seq_offsets, nseq, state, state_out, state_slots, has_state)
+    px, xs = _rows(x, None, "x", (T, C))
+    py, ys = _rows(y, None, "y", (T, C))
+    keep = (x, weight, y, bias, seq_offsets, state, state_out, state_slots, has_state, y_group_of, y_scales)
+    st = _fill(ConvArgs(), keep=keep, tokens=T, dim=C, width=W, silu=int(bool(silu)),
+               x_dtype=_float_type(x, "x"), y_dtype=QSSM_I8 if i8 else _float_type(y, "y"), x=px, x_stride=xs,
+               weight=_ptr(weight, torch.float32, "weight"), bias=_ptr(bias, torch.float32, "bias", True),
+               y=py, y_stride=ys, y_group_of=_ptr(y_group_of, torch.uint8, "y_group_of", True),
+               y_scales=_ptr(y_scales, torch.float32, "y_scales", True),
+               y_groups=int(y_scales.numel()) if y_scales is not None else 0, reserved=0, **seqs)
+    st._device = _device_of(*keep)
+    return st
+
+
+def qssm_causal_conv(args, stream=None):
+    _call("qssm_causal_conv", args._device, stream, ctypes.byref(args), keep=args._keep)
+
+
+def selective_scan_args(x, delta, A, B, C, y, D=None, z=None, delta_bias=None, delta_softplus=True,
+                        bc_groups=1, seq_offsets=None, nseq=None, state=None, state_out=None,
+                        state_slots=None, has_state=None):
+    """x, delta and z [T, D], B and C [T, bc_groups * N], all float32 or all float16 (rows may lie apart, as
+    columns of a wider tensor do); A float32 [D, N], D (the skip) and delta_bias float32 [D]; y [T, D]
+    float32 or float16. Sequences and states as in causal_conv_args, the states [slots, D, N] float32 or
+    float16."""
+    torch = _t()
+    if x.dim() != 2 or A.dim() != 2 or A.shape[0] != x.shape[1]:
+        raise ValueError("x must be [T, D] and A [D, N]")
+    (T, dim), N = x.shape, A.shape[1]
+    if int(bc_groups) != bc_groups or not 1 <= bc_groups <= max(dim, 1):
+        raise ValueError("bc_groups must be a whole number in 1 .. D")
+    for t, name in ((D, "D"), (delta_bias, "delta_bias")):
+        if t is not None and t.numel() != dim:
+            raise ValueError(f"{name} must be [D]")
+    seqs = _sequences(T, (dim, N), (torch.float32, torch.float16), seq_offsets, nseq, state, state_out,
+                      state_slots, has_state)
+    fields = {}
+    for t, name, cols in ((x, "x", dim), (delta, "delta", dim), (z, "z", dim), (B, "B", bc_groups * N),
+                          (C, "C", bc_groups * N)):
+        fields[name], fields[name + "_stride"] = _rows(t, x.dtype, name, (T, cols), name == "z")
+    py, ys = _rows(y, None, "y", (T, dim))
+    keep = (x, delta, A, B, C, y, D, z, delta_bias, seq_offsets, state, state_out, state_slots, has_state)
+    st = _fill(SscanArgs(), keep=keep, tokens=T, dim=dim, dstate=N, ngroups=int(bc_groups),
+               io_dtype=_float_type(x, "x"), y_dtype=_float_type(y, "y"),
+               state_dtype=_float_type(state if state is not None else state_out, "state"),
+               delta_softplus=int(bool(delta_softplus)), reserved=0, A=_ptr(A, torch.float32, "A"),
+               Dskip=_ptr(D, torch.float32, "D", True),
+               delta_bias=_ptr(delta_bias, torch.float32, "delta_bias", True), y=py, y_stride=ys,
+               **fields, **seqs)
+    st._device = _device_of(*keep)
+    return st
+
+
+def qssm_selective_scan_workspace_size(args):
+    """Bytes of the workspace; 0 where none is needed."""
+    return load().qssm_selective_scan_workspace_size(ctypes.byref(args))
+
+
+def qssm_selective_scan(args, workspace=None, stream=None):
+    """workspace: a contiguous uint8 tensor, or None where none is needed."""
+    torch = _t()
+    if workspace is not None and workspace.numel() > 0:
+        p, n = _ptr(workspace, torch.uint8, "workspace"), workspace.numel()
+        _device_of(workspace, args._keep[0])
+        keep = [*args._keep, workspace]
+    else:
+        p, n, keep = None, 0, args._keep
+    _call("qssm_selective_scan", args._device, stream, ctypes.byref(args), p, n, keep=keep)
+
+
+# ------------------------------------------------------------------------------------------------
+# Block-scaled 8-bit floating point
+
+def qssm_quant_f8(x, codes, scales, stream=None):
+    """x [M, K] float32 or float16 -> codes float8_e4m3fn [M, K] and scales float32 [ceil(K / 128), M]; rows of
+    each may lie apart."""
+    torch = _t()
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    px, xs = _rows(x, None, "x", (M, K))
+    pc, cs = _rows(codes, torch.float8_e4m3fn, "codes", (M, K))
+    ps, ss = _rows(scales, torch.float32, "scales", (-(-K // 128), M))
+    _call("qssm_quant_f8", _device_of(x, codes, scales), stream, px, _float_type(x, "x"), M, K, xs, pc, cs, ps,
+          max(ss, M), keep=(x, codes, scales))
+    return codes, scales
+
+
+def gemm_f8_args(a, a_scales, w, w_scales, y, bias=None):
+    """a [M, K] and w [N, K] float8_e4m3fn (rows may lie apart); a_scales float32 [ceil(K / 128), M] (rows may
+    lie apart), w_scales float32 [ceil(N / 128), ceil(K / 128)]; y float32 or float16 [M, N] (rows may lie
+    apart); bias float32 [N] or None."""
+    torch = _t()
+    if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1]:
+        raise ValueError("a must be [M, K] and w [N, K]")
+    (M, K), N = a.shape, w.shape[0]
+    kb, nb = -(-K // 128), -(-N // 128)
+    if tuple(w_scales.shape) != (nb, kb) or (bias is not None and bias.numel() != N):
+        raise ValueError("w_scales must be [ceil(N / 128), ceil(K / 128)] and bias [N]")
+    pa, sa = _rows(a, torch.float8_e4m3fn, "a", (M, K))
+    ps, ss = _rows(a_scales, torch.float32, "a_scales", (kb, M))
+    pw, sw = _rows(w, torch.float8_e4m3fn, "w", (N, K))
+    py, sy = _rows(y, None, "y", (M, N))
+    keep = (a, a_scales, w, w_scales, y, bias)
+    st = _fill(GemmF8Args(), keep=keep, M=M, N=N, K=K, y_dtype=_float_type(y, "y"), reserved=0, a=pa,
+               a_stride=sa, a_scales=ps, a_scales_stride=ss, w=pw, w_stride=sw,
+               w_scales=_ptr(w_scales, torch.float32, "w_scales"),
+               bias=_ptr(bias, torch.float32, "bias", True), y=py, y_stride=sy)
+    st._device = _device_of(*keep)
+    return st
+
+
+def qssm_gemm_f8(args, stream=None):
+    _call("qssm_gemm_f8", args._device, stream, ctypes.byref(args), keep=args._keep)
+
+
+# ------------------------------------------------------------------------------------------------
 # W4A8 linear layer
 
 def gemm_args(a, a_scale, w_packed, w_scales, group, y, bias=None):
@@ -734,6 +934,19 @@ def qssm_quant_w8(w):
     scales = np.empty(N, np.float32)
     codes = np.empty((N, K), np.int8)
     _check("qssm_quant_w8", load().qssm_quant_w8(_np_ptr(w), N, K, _np_ptr(scales), _np_ptr(codes)))
+    return scales, codes
+
+
+def qssm_quant_f8_weight(w):
+    """Offline e4m3 weight quantization (host): returns (scales [ceil(N / 128), ceil(K / 128)] float32,
+    codes [N, K] uint8, the bytes of float8_e4m3fn values)."""
+    import numpy as np
+    w = np.ascontiguousarray(w, dtype=np.float32)
+    N, K = w.shape
+    scales = np.empty((-(-N // 128), -(-K // 128)), np.float32)
+    codes = np.empty((N, K), np.uint8)
+    _check("qssm_quant_f8_weight", load().qssm_quant_f8_weight(_np_ptr(w), N, K, _np_ptr(scales),
+                                                                _np_ptr(codes)))
     return scales, codes
 
 

@@ -25,6 +25,20 @@ float calib_scale(float absmax) {
   return s;
 }
 
+// The e4m3 code of v / s: the exact quotient's nearest value, ties to even. The fp64 quotient q of two fp32 values
+// is a multiple of half a step (a tie) only where the exact one is: |v| - t s of a tie t of 5 bits is a
+// multiple of 2^-29 of |v|.
+uint8_t e4m3_code(float v, float s) {
+  if (v != v) return 0;
+  const uint8_t sign = std::signbit(v) ? 0x80 : 0;
+  const double q = std::min(std::fabs((double)v / (double)s), 448.0);
+  if (q < 0x1p-6) return sign | (uint8_t)std::nearbyint(q * 512.0);  // steps of 2^-9; the 8th is the least with an exponent
+  int e;
+  std::frexp(q, &e);  // q in [2^(e - 1), 2^e), steps of 2^(e - 4)
+  const int m = (int)std::nearbyint(std::ldexp(q, 4 - e));  // 8 .. 16
+  return sign | (uint8_t)(((e - 1 + 7) << 3) + (m - 8));
+}
+
 // Percentile with linear interpolation between order statistics (the "linear" rule:
 // virtual index (n-1) q), on ascending values.
 double percentile_linear(const std::vector<double>& sorted, double pct) {
@@ -300,6 +314,30 @@ qssm_status qssm_quant_w8(const float* w, int64_t N, int64_t K, float* scales, i
     scales[n] = s;
     for (int64_t k = 0; k < K; ++k) codes[n * K + k] = qssm::quant8(w[n * K + k], s);
   }
+  return QSSM_OK;
+}
+
+qssm_status qssm_quant_f8_weight(const float* w, int64_t N, int64_t K, float* scales, uint8_t* codes) {
+  qssm::clear_error();
+  if (N < 0 || K < 0) return fail(QSSM_ERR_INVALID_ARG, "negative extent");
+  if (N > 0 && K > 0 && (!w || !scales || !codes)) return fail(QSSM_ERR_INVALID_ARG, "null pointer");
+  const int64_t kb = qssm::cdiv(K, 128);
+  for (int64_t n0 = 0; n0 < N; n0 += 128)
+    for (int64_t b = 0; b < kb; ++b) {
+      const int64_t n1 = std::min(N, n0 + 128), k0 = b * 128, k1 = std::min(K, k0 + 128);
+      float m = 0.0f;
+      for (int64_t n = n0; n < n1; ++n)
+        for (int64_t k = k0; k < k1; ++k) {
+          const float a = std::fabs(w[n * K + k]);
+          if (a <= std::numeric_limits<float>::max() && a > m) m = a;
+        }
+      float s = (m == 0.0f) ? 1.0f : m / 448.0f;
+      if (s < 0x1p-60f) s = 0x1p-60f;
+      if (s > 0x1p60f) s = 0x1p60f;
+      scales[n0 / 128 * kb + b] = s;
+      for (int64_t n = n0; n < n1; ++n)
+        for (int64_t k = k0; k < k1; ++k) codes[n * K + k] = e4m3_code(w[n * K + k], s);
+    }
   return QSSM_OK;
 }
 

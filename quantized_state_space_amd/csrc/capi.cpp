@@ -57,6 +57,9 @@ size_t qssm_args_size(int32_t kind) {
     case 4: return sizeof(qssm_gemm_args);
     case 5: return sizeof(qssm_rmsnorm_args);
     case 6: return sizeof(qssm_gemm_w8a8_args);
+    case 7: return sizeof(qssm_conv_args);
+    case 8: return sizeof(qssm_sscan_args);
+    case 9: return sizeof(qssm_gemm_f8_args);
     default: return 0;
   }
 }

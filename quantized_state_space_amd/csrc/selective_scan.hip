@@ -1,0 +1,464 @@
+// Selective scan on unquantized inputs over packed sequences, with softplus, skip and gate.
+//
+// Quamba2, abstract: the Mamba1 recurrence, prefill and generation.
+//     dt = softplus(delta + bias)     h[n] = e^(dt A[n]) h[n] + dt x B[n]     y = (C h + D x) silu(z)
+//
+// Four neighbouring lanes own a channel, each a quarter of its states (NPL of them, in registers), and a
+// workgroup 64 channels of one B/C group. The rows run in batches of four: each lane of a channel loads
+// and prepares one row (dt, dt x, and later the gate), the four rows' values are passed around by lane
+// permutations, and the four lanes' sums are joined by a transposed reduction that leaves each lane the
+// sum of its own row. B and C of 32 rows at a time go through LDS as fp32 while the rows before are computed, and
+// the next 32 rows of x, delta and z are in registers by then.
+//
+// Bound by vector instructions: an update takes two products, an exponential (a quarter of the rate), and two fused
+// multiply-adds, 8 issue slots, of T D N updates.
+//
+// Few sequences with few channels do not fill the chip, so long sequences are cut into pieces (piece_rows()).
+// First every piece that has one behind it runs from zero without y, and each sequence's first piece in
+// full; then the others run in full from the state that they fold from the ends before them:
+//     h_in[c + 1] = e^(A sum dt over c) h_in[c] + end[c].
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "common.hpp"
+#include "sequences.hpp"
+
+using namespace qssm;
+
+namespace {
+
+struct SscanParams {
+  Seqs seq;
+  int32_t D, N, G, Dg, per_group;  // Dg = D / G channels in per_group workgroups
+  int32_t phase, piece;            // 1: the pieces from zero and the first ones in full, 2: the others
+  int32_t softplus, yf16, sf16;
+  const void *x, *delta, *B, *C, *z;
+  int64_t xs, ds, bs, cs, zs, ys;
+  const float *A, *Dskip, *bias;
+  void* y;
+  const void* state;
+  void* state_out;
+  float* carry;  // piece slot: ends [D, 4 NPL], sums of dt [D]
+};
+
+constexpr float kLog2e = 1.44269504f;
+
+template <typename T>
+__device__ __forceinline__ float as_float(T v) {
+  if constexpr (std::is_same_v<T, uint16_t>) return __half2float(__ushort_as_half(v));
+  else return __uint_as_float(v);
+}
+
+// max(v, 0) + log(1 + e), e = e^-|v|, by log(1 + e) = 2 atanh(s) = s P(s^2), s = e / (2 + e) <= 1/3: P of degree 4 is
+// within 4.1e-9 (a fit at Chebyshev nodes). A NaN stays one: s is.
+__device__ __forceinline__ float softplus(float v) {
+  const float e = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e);
+  const float s = e * __builtin_amdgcn_rcpf(2.0f + e), q = s * s;
+  float p = fmaf(q, 0.2816145375705998f, 0.27964344707516564f);
+  p = fmaf(p, q, 0.40024651333399913f);
+  p = fmaf(p, q, 0.6666632040642534f);
+  p = fmaf(p, q, 2.0000000077239766f);
+  return fmaf(s, p, fmaxf(v, 0.0f));
+}
+
+__device__ __forceinline__ float silu(float v) {
+  const float e = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e), r = __builtin_amdgcn_rcpf(1.0f + e);
+  return v * (v < 0.0f ? e * r : r);
+}
+
+// A log2(e), finite: e^(0 A) is 1 for an infinite A too, as a row that does not count needs it.
+__device__ __forceinline__ float decay_of(float a) { return __builtin_amdgcn_fmed3f(a * kLog2e, -3.402823466e38f, 3.402823466e38f) + 0.0f * (a != a ? a : 0.0f); }
+
+// x of lane K of the four
+template <int K>
+__device__ __forceinline__ float lane4(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), K * 0x55, 0xF, 0xF, true));
+}
+
+// p[s] is the lane's part of row s's sum; returns the four lanes' sum of row q = lane % 4.
+__device__ __forceinline__ float join4(const float (&p)[4], int q) {
+  const bool hi = q & 2, odd = q & 1;
+  const float a = (hi ? p[2] : p[0]) + dpp_partner<2>(hi ? p[0] : p[2]);
+  const float b = (hi ? p[3] : p[1]) + dpp_partner<2>(hi ? p[1] : p[3]);
+  return (odd ? b : a) + dpp_partner<1>(odd ? a : b);
+}
+
+__device__ __forceinline__ float sum4(float v) {
+  v += dpp_partner<1>(v);
+  return v + dpp_partner<2>(v);
+}
+
+template <int NPL>
+__device__ __forceinline__ void load_state(const SscanParams& p, int64_t slot, bool has, int d, int q, float (&h)[NPL]) {
+  const bool given = p.state && slot >= 0 && has;
+  const int64_t at = (slot * p.D + d) * p.N + q * NPL;
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) {
+    h[j] = 0.0f;
+    if (given && q * NPL + j < p.N)
+      h[j] = p.sf16 ? __half2float(reinterpret_cast<const __half*>(p.state)[at + j]) : reinterpret_cast<const float*>(p.state)[at + j];
+  }
+}
+
+template <int NPL>
+__device__ __forceinline__ void store_state(const SscanParams& p, int64_t slot, int d, int q, const float (&h)[NPL]) {
+  if (!p.state_out || slot < 0) return;
+  const int64_t at = (slot * p.D + d) * p.N + q * NPL;
+#pragma unroll
+  for (int j = 0; j < NPL; ++j)
+    if (q * NPL + j < p.N) {
+      if (p.sf16) reinterpret_cast<__half*>(p.state_out)[at + j] = __float2half_rn(h[j]);
+      else reinterpret_cast<float*>(p.state_out)[at + j] = h[j];
+    }
+}
+
+template <int NPL>
+__device__ __forceinline__ void load_decay(const SscanParams& p, int d, int q, float (&a)[NPL]) {
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) a[j] = q * NPL + j < p.N ? decay_of(p.A[(int64_t)d * p.N + q * NPL + j]) : 0.0f;
+}
+
+constexpr int kRows = 32;  // rows of B and C in LDS at a time
+
+template <int NPL, typename T>
+struct Piece {
+  static constexpr int kNP = 4 * NPL, kTS = kRows, kBatches = kTS / 4, kPer = kTS * 2 * kNP / 256;
+  const SscanParams& p;
+  const int d, q, g;  // the lane's channel (clamped), its place in the four, the B/C group
+  const bool live;
+  float* const lds;   // [2][kTS][2][kNP]
+  T xr[kBatches], dr[kBatches], zr[kBatches], bc[kPer];
+
+  // row t + 4 i + q of batch i
+  template <bool Z>
+  __device__ __forceinline__ void load_rows(int t, int end) {
+    const T* x = reinterpret_cast<const T*>(p.x) + (int64_t)(t + q) * p.xs + d;
+    const T* dl = reinterpret_cast<const T*>(p.delta) + (int64_t)(t + q) * p.ds + d;
+    const T* z = Z ? reinterpret_cast<const T*>(p.z) + (int64_t)(t + q) * p.zs + d : nullptr;
+#pragma unroll
+    for (int i = 0; i < kBatches; ++i) {
+      const bool in = t + 4 * i + q < end;
+      xr[i] = dr[i] = zr[i] = 0;
+      if (in) {
+        xr[i] = x[4 * i * p.xs];
+        dr[i] = dl[4 * i * p.ds];
+        if (Z) zr[i] = z[4 * i * p.zs];
+      }
+    }
+  }
+
+  __device__ __forceinline__ void load_bc(int t, int end) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = threadIdx.x + 256 * i, row = e / (2 * kNP), k = e % kNP;
+      const bool isC = (e / kNP) & 1;
+      bc[i] = 0;
+      if (t + row < end && k < p.N)
+        bc[i] = isC ? reinterpret_cast<const T*>(p.C)[(int64_t)(t + row) * p.cs + g * p.N + k]
+                    : reinterpret_cast<const T*>(p.B)[(int64_t)(t + row) * p.bs + g * p.N + k];
+    }
+  }
+
+  __device__ __forceinline__ void store_bc(int buf) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) lds[buf * kTS * 2 * kNP + threadIdx.x + 256 * i] = as_float(bc[i]);
+  }
+
+  // Rows begin .. end - 1 from the state in h, which becomes the state behind them; returns the sum of dt (the
+  // lane's rows). Y: with y.
+  template <bool Y>
+  __device__ __forceinline__ float run(int begin, int end, const float (&a)[NPL], float (&h)[NPL]) {
+    const float bias = p.bias ? p.bias[d] : 0.0f, skip = p.Dskip ? p.Dskip[d] : 0.0f;
+    float sum = 0.0f;
+    const bool gate = Y && p.z;
+    const auto rows = [&](int t) {
+      if (gate) load_rows<true>(t, end);
+      else load_rows<false>(t, end);
+    };
+    load_bc(begin, end);
+    rows(begin);
+    __syncthreads();  // (a piece before this one may have left its last rows in LDS)
+    store_bc(0);
+    __syncthreads();
+    int buf = 0;
+    for (int t = begin; t < end; t += kTS, buf ^= 1) {
+      T xc[kBatches], dc[kBatches], zc[kBatches];
+#pragma unroll
+      for (int i = 0; i < kBatches; ++i) xc[i] = xr[i], dc[i] = dr[i], zc[i] = zr[i];
+      const bool more = end - t > kTS;
+      if (more) {
+        load_bc(t + kTS, end);
+        rows(t + kTS);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatches; ++i) {
+        const int row = t + 4 * i + q;
+        if (t + 4 * i >= end) break;
+        const bool in = row < end;
+        const float x = as_float(xc[i]), dl = as_float(dc[i]) + bias;
+        const float dt = in ? (p.softplus ? softplus(dl) : dl) : 0.0f, u = in ? dt * x : 0.0f;
+        if (!Y) sum += dt;
+        float part[4];
+        const auto step = [&](auto k) {
+          constexpr int K = decltype(k)::value;
+          const float ds = lane4<K>(dt), us = lane4<K>(u);
+          const float* bq = lds + ((buf * kTS + 4 * i + K) * 2) * kNP + q * NPL;
+          part[K] = 0.0f;
+#pragma unroll
+          for (int j = 0; j < NPL; ++j) {
+            h[j] = fmaf(__builtin_amdgcn_exp2f(ds * a[j]), h[j], us * bq[j]);
+            if (Y) part[K] = fmaf(bq[kNP + j], h[j], part[K]);
+          }
+        };
+        step(std::integral_constant<int, 0>());
+        step(std::integral_constant<int, 1>());
+        step(std::integral_constant<int, 2>());
+        step(std::integral_constant<int, 3>());
+        if (Y) {
+          float y = fmaf(skip, x, join4(part, q));
+          if (gate) y *= silu(as_float(zc[i]));
+          if (in && live) {
+            const int64_t at = (int64_t)row * p.ys + d;
+            if (p.yf16) reinterpret_cast<__half*>(p.y)[at] = __float2half_rn(y);
+            else reinterpret_cast<float*>(p.y)[at] = y;
+          }
+        }
+      }
+      if (more) {
+        store_bc(buf ^ 1);
+        __syncthreads();
+      }
+    }
+    return sum;
+  }
+};
+
+template <int NPL, typename T>
+__global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
+  constexpr int kNP = 4 * NPL;
+  __shared__ __align__(16) float lds[2 * kRows * 2 * kNP];
+  const int blocks = p.G * p.per_group, cb = blockIdx.x % blocks;
+  const int64_t at = blockIdx.x / blocks;  // piece slot: sequence i has begin(i) / piece + i and the ones behind it
+  const Seqs& sq = p.seq;
+  int i;
+  if (sq.offsets) i = last_not_above(sq.nseq, at, [&](int k) { return (int64_t)(seq_begin(sq, k) / p.piece + k); });
+  else i = last_not_above(sq.nseq, at, [&](int k) { return (int64_t)(k * sq.each / p.piece + k); });
+  const int begin = uniform(seq_begin(sq, i)), end = uniform(seq_end(sq, i, begin));
+  const int64_t chunk = at - (begin / p.piece + i), pieces = max((int64_t)((int64_t)(end - begin) + p.piece - 1) / p.piece, (int64_t)1);
+  if (chunk < 0 || chunk >= pieces) return;
+  const bool last = chunk == pieces - 1;
+  if (p.phase == 1 ? chunk > 0 && last : chunk == 0) return;
+  const int g = cb / p.per_group, q = threadIdx.x & 3;
+  const int dg = cb % p.per_group * 64 + (threadIdx.x >> 2);
+  const int d = g * p.Dg + min(dg, p.Dg - 1);
+  const bool live = dg < p.Dg;
+  float a[NPL], h[NPL];
+  load_decay(p, d, q, a);
+  const int64_t slot = seq_slot(sq, i);
+  const int64_t size = (int64_t)p.D * (kNP + 1);
+  float* ends = p.carry + at * size + (int64_t)d * kNP + q * NPL;
+  if (p.phase == 1) {
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) h[j] = 0.0f;
+    if (chunk == 0) load_state(p, slot, !sq.has || sq.has[i] != 0, d, q, h);
+  } else {
+    const float* from = ends - chunk * size;
+    const float* sums = p.carry + (at - chunk) * size + (int64_t)p.D * kNP + d;
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) h[j] = from[j];
+#pragma unroll 4
+    for (int64_t c = 1; c < chunk; ++c) {
+      const float s = sums[c * size];
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) h[j] = fmaf(__builtin_amdgcn_exp2f(s * a[j]), h[j], from[c * size + j]);
+    }
+  }
+  Piece<NPL, T> piece{p, d, q, g, live, lds};
+  const int b = begin + (int)chunk * p.piece, e = last ? end : b + p.piece;
+  if (p.phase == 1 && chunk > 0) {
+    const float sum = sum4(piece.template run<false>(b, e, a, h));
+    if (live && q == 0) p.carry[at * size + (int64_t)p.D * kNP + d] = sum;
+  } else if (b < e) {
+    piece.template run<true>(b, e, a, h);
+  }
+  if (!live) return;
+  if (last) {
+    store_state(p, slot, d, q, h);
+  } else if (p.phase == 1) {
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) ends[j] = h[j];
+  }
+}
+
+// One row a sequence: four lanes own a channel of one sequence.
+template <int NPL, typename T>
+__global__ __launch_bounds__(256) void k_selective_step(SscanParams p) {
+  const int64_t id = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2);
+  const int q = threadIdx.x & 3;
+  const int64_t all = (int64_t)p.seq.nseq * p.D;
+  const bool live = id < all;
+  const int i = (int)(min(id, all - 1) / p.D), d = (int)(min(id, all - 1) % p.D), g = d / p.Dg;
+  const int64_t slot = seq_slot(p.seq, i);
+  float a[NPL], h[NPL];
+  load_decay(p, d, q, a);
+  load_state(p, slot, !p.seq.has || p.seq.has[i] != 0, d, q, h);
+  const float x = as_float(reinterpret_cast<const T*>(p.x)[(int64_t)i * p.xs + d]);
+  float dl = as_float(reinterpret_cast<const T*>(p.delta)[(int64_t)i * p.ds + d]) + (p.bias ? p.bias[d] : 0.0f);
+  const T* b = reinterpret_cast<const T*>(p.B) + (int64_t)i * p.bs + g * p.N + q * NPL;
+  const T* c = reinterpret_cast<const T*>(p.C) + (int64_t)i * p.cs + g * p.N + q * NPL;
+  const float dt = p.softplus ? softplus(dl) : dl, u = dt * x;
+  float y = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NPL; ++j)
+    if (q * NPL + j < p.N) {
+      h[j] = fmaf(__builtin_amdgcn_exp2f(dt * a[j]), h[j], u * as_float(b[j]));
+      y = fmaf(as_float(c[j]), h[j], y);
+    }
+  y = fmaf(p.Dskip ? p.Dskip[d] : 0.0f, x, sum4(y));
+  if (p.z) y *= silu(as_float(reinterpret_cast<const T*>(p.z)[(int64_t)i * p.zs + d]));
+  if (!live) return;
+  if (q == 0) {
+    if (p.yf16) reinterpret_cast<__half*>(p.y)[(int64_t)i * p.ys + d] = __float2half_rn(y);
+    else reinterpret_cast<float*>(p.y)[(int64_t)i * p.ys + d] = y;
+  }
+  store_state(p, slot, d, q, h);
+}
+
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;  // a grid holds fewer than 2^32 threads
+
+int npl_of(int64_t N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+
+int64_t blocks_of(const qssm_sscan_args& a) { return a.ngroups * cdiv(a.dim / a.ngroups, 64); }
+
+// Rows of a piece.
+int64_t piece_rows(const qssm_sscan_args& a) {
+  const int64_t waves = 4 * blocks_of(a), whole = std::max<int64_t>(a.tokens, 1);
+  if (a.nseq * waves >= 768) return a.seq_offsets ? std::min(whole, std::max<int64_t>(64, 4 * cdiv(whole, a.nseq))) : whole;
+  return std::min(whole, std::max<int64_t>(64, cdiv(cdiv(whole * waves, 2048), 32) * 32));
+}
+
+bool is_cut(const qssm_sscan_args& a, int64_t piece) {
+  return piece < (a.seq_offsets ? a.tokens : a.tokens / std::max<int64_t>(a.nseq, 1));
+}
+
+size_t carry_bytes(const qssm_sscan_args& a, int64_t piece) {
+  return (size_t)(a.tokens / piece + a.nseq) * (size_t)a.dim * (size_t)(4 * npl_of(a.dstate) + 1) * sizeof(float);
+}
+
+bool is_step(const qssm_sscan_args& a) { return !a.seq_offsets && a.tokens == a.nseq; }
+
+template <int NPL, typename T>
+qssm_status launch(SscanParams p, const qssm_sscan_args& a, hipStream_t stream) {
+  if (is_step(a)) {
+    const int64_t blocks = cdiv(a.nseq * a.dim, 64);
+    if (blocks > kMaxBlocks) return fail(QSSM_ERR_UNSUPPORTED, "nseq * dim above 2^30");
+    k_selective_step<NPL, T><<<(unsigned)blocks, 256, 0, stream>>>(p);
+    return launch_status("selective_scan");
+  }
+  const int64_t blocks = (a.tokens / p.piece + a.nseq) * blocks_of(a);
+  if (blocks > kMaxBlocks) return fail(QSSM_ERR_UNSUPPORTED, "tokens * dim too large");
+  p.phase = 1;
+  k_selective_scan<NPL, T><<<(unsigned)blocks, 256, 0, stream>>>(p);
+  if (is_cut(a, p.piece)) {
+    if (const qssm_status s = launch_status("selective_scan")) return s;
+    p.phase = 2;
+    k_selective_scan<NPL, T><<<(unsigned)blocks, 256, 0, stream>>>(p);
+  }
+  return launch_status("selective_scan");
+}
+
+template <typename T>
+qssm_status launch_n(const SscanParams& p, const qssm_sscan_args& a, hipStream_t stream) {
+  switch (npl_of(a.dstate)) {
+    case 2: return launch<2, T>(p, a, stream);
+    case 4: return launch<4, T>(p, a, stream);
+    case 8: return launch<8, T>(p, a, stream);
+    default: return launch<16, T>(p, a, stream);
+  }
+}
+
+// The sizes alone: what the workspace depends on.
+qssm_status check_sizes(const qssm_sscan_args& a) {
+  if (const qssm_status s = check_seqs(a.tokens, a.dim, a.nseq, a.seq_offsets, a.state, a.state_out, a.slots, a.state_slots)) return s;
+  if (a.dstate < 1 || a.dstate > 64) return fail(QSSM_ERR_UNSUPPORTED, "dstate must be in 1..64");
+  if (a.ngroups < 1 || a.dim % a.ngroups != 0) return fail(QSSM_ERR_INVALID_ARG, "dim is not a multiple of ngroups");
+  return QSSM_OK;
+}
+
+}  // namespace
+
+extern "C" size_t qssm_selective_scan_workspace_size(const qssm_sscan_args* a) {
+  clear_error();
+  if (!a || check_sizes(*a) != QSSM_OK || a->nseq == 0 || a->dim == 0 || is_step(*a)) return 0;
+  const int64_t piece = piece_rows(*a);
+  return is_cut(*a, piece) ? carry_bytes(*a, piece) : 0;
+}
+
+extern "C" qssm_status qssm_selective_scan(const qssm_sscan_args* a, void* workspace, size_t workspace_bytes,
+                                           hipStream_t stream) {
+  clear_error();
+  if (!a) return fail(QSSM_ERR_INVALID_ARG, "args is null");
+  if (const qssm_status s = check_sizes(*a)) return s;
+  const int64_t T = a->tokens, D = a->dim, N = a->dstate, GN = a->ngroups * N;
+  if (a->io_dtype != QSSM_F32 && a->io_dtype != QSSM_F16) return fail(QSSM_ERR_INVALID_ARG, "io_dtype must be QSSM_F32 or QSSM_F16");
+  if (a->y_dtype != QSSM_F32 && a->y_dtype != QSSM_F16) return fail(QSSM_ERR_INVALID_ARG, "y_dtype must be QSSM_F32 or QSSM_F16");
+  if (a->state_dtype != QSSM_F32 && a->state_dtype != QSSM_F16)
+    return fail(QSSM_ERR_INVALID_ARG, "state_dtype must be QSSM_F32 or QSSM_F16");
+  if (a->reserved != 0) return fail(QSSM_ERR_INVALID_ARG, "reserved must be 0");
+  const int64_t sx = type_size(a->io_dtype), sy = type_size(a->y_dtype), ss = type_size(a->state_dtype);
+  if (const qssm_status s = check_rows("x", a->x, T, D, a->x_stride, sx)) return s;
+  if (const qssm_status s = check_rows("delta", a->delta, T, D, a->delta_stride, sx)) return s;
+  if (const qssm_status s = check_rows("B", a->B, T, GN, a->B_stride, sx)) return s;
+  if (const qssm_status s = check_rows("C", a->C, T, GN, a->C_stride, sx)) return s;
+  if (const qssm_status s = check_rows("z", a->z, T, D, a->z_stride, sx)) return s;
+  if (const qssm_status s = check_rows("y", a->y, T, D, a->y_stride, sy)) return s;
+  if (a->nseq == 0 || D == 0) return QSSM_OK;
+  if (!a->A || (T > 0 && (!a->x || !a->delta || !a->B || !a->C || !a->y)))
+    return fail(QSSM_ERR_INVALID_ARG, "null required pointer");
+  if (((uintptr_t)a->A | (uintptr_t)a->Dskip | (uintptr_t)a->delta_bias) % 4 != 0 ||
+      ((uintptr_t)a->state | (uintptr_t)a->state_out) % ss != 0)
+    return fail(QSSM_ERR_INVALID_ARG, "A, Dskip, delta_bias or a state is not aligned to its type");
+  if (a->slots > ((int64_t)1 << 58) / (D * N)) return fail(QSSM_ERR_UNSUPPORTED, "slots * dim * dstate above 2^58");
+  SscanParams p{};
+  p.piece = (int32_t)piece_rows(*a);
+  const size_t need = !is_step(*a) && is_cut(*a, p.piece) ? carry_bytes(*a, p.piece) : 0;
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(QSSM_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : (size_t)0, need);
+  if (need && (uintptr_t)workspace % 16 != 0) return fail(QSSM_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+  const int64_t sb = a->slots * D * N * ss;
+  const Span y{a->y, T, a->y_stride * sy, D * sy}, out = flat(a->state_out, sb), ws = flat(need ? workspace : nullptr, (int64_t)need);
+  const Span in[] = {{a->x, T, a->x_stride * sx, D * sx},       {a->delta, T, a->delta_stride * sx, D * sx},
+                     {a->B, T, a->B_stride * sx, GN * sx},      {a->C, T, a->C_stride * sx, GN * sx},
+                     {a->z, T, a->z_stride * sx, D * sx},       flat(a->A, D * N * 4),
+                     flat(a->Dskip, D * 4),                     flat(a->delta_bias, D * 4),
+                     flat(a->seq_offsets, (a->nseq + 1) * 4),   flat(a->state_slots, a->nseq * 4),
+                     flat(a->has_state, a->nseq)};
+  for (const Span& s : in)
+    if (overlap(y, s) || overlap(out, s) || overlap(ws, s))
+      return fail(QSSM_ERR_INVALID_ARG, "y, state_out or the workspace overlaps an input");
+  const Span st = flat(a->state, sb);
+  if (overlap(y, st) || overlap(y, out) || overlap(y, ws) || overlap(ws, st) || overlap(ws, out) ||
+      (a->state_out != a->state && overlap(out, st)))
+    return fail(QSSM_ERR_INVALID_ARG, "y, state, state_out and the workspace overlap");
+  p.seq = make_seqs(T, a->nseq, a->seq_offsets, a->state_slots, a->has_state, a->slots);
+  p.D = (int32_t)D;
+  p.N = (int32_t)N;
+  p.G = a->ngroups;
+  p.Dg = (int32_t)(D / a->ngroups);
+  p.per_group = (int32_t)cdiv(p.Dg, 64);
+  p.softplus = a->delta_softplus != 0;
+  p.yf16 = a->y_dtype == QSSM_F16;
+  p.sf16 = a->state_dtype == QSSM_F16;
+  p.x = a->x, p.xs = a->x_stride;
+  p.delta = a->delta, p.ds = a->delta_stride;
+  p.B = a->B, p.bs = a->B_stride;
+  p.C = a->C, p.cs = a->C_stride;
+  p.z = a->z, p.zs = a->z_stride;
+  p.y = a->y, p.ys = a->y_stride;
+  p.A = a->A, p.Dskip = a->Dskip, p.bias = a->delta_bias;
+  p.state = a->state, p.state_out = a->state_out;
+  p.carry = static_cast<float*>(workspace);
+  return a->io_dtype == QSSM_F16 ? launch_n<uint16_t>(p, *a, stream) : launch_n<uint32_t>(p, *a, stream);
+}
