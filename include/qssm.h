@@ -630,12 +630,11 @@ qssm_status qssm_causal_conv(const qssm_conv_args* a, hipStream_t stream);
  * fp32. The state [slots, dim, dstate] is fp32, or fp16, which is rounded to nearest even once per call
  * and sequence (the decode cache in half the bytes; inside a call the state is fp32).
  * Long sequences are cut into pieces that run in parallel: every piece but a sequence's last runs from
- * zero, then every piece but the first again from its entering state, which is folded from the ends of
- * the pieces before it (in their order, so results do not vary from call to call). How long the pieces
+ * zero, then every piece again from its entering state, which is folded from the ends of the pieces before it (in their order, so results do not vary from call to call). How long the pieces
  * are follows from the sizes alone; they meet the sequential results to fp32 rounding.
  * Workspace: qssm_selective_scan_workspace_size bytes (0 when nothing is cut), 16-byte aligned; calls
  * that overlap in time need their own.
- * 1 <= dstate <= 64, dim <= 2^24, nseq <= 2^24, tokens <= 2^31 - 64, dim % ngroups == 0.
+ * 1 <= dstate <= 64, dim <= 2^24, nseq <= 2^24, tokens <= 2^31 - 64, dim % ngroups == 0; strides at most 2^23.
  */
 typedef struct qssm_sscan_args {
   int64_t tokens, dim, dstate, nseq;

@@ -14,12 +14,13 @@
 // multiply-adds, 8 issue slots, of T D N updates.
 //
 // Few sequences with few channels do not fill the chip, so long sequences are cut into pieces (piece_rows()).
-// First every piece that has one behind it runs from zero without y, and each sequence's first piece in
-// full; then the others run in full from the state that they fold from the ends before them:
+// First the pieces but the last run without y, the first from the initial state, the others from zero; then all run in
+// full from the state that they fold from the ends before them:
 //     h_in[c + 1] = e^(A sum dt over c) h_in[c] + end[c].
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <type_traits>
 
 #include "common.hpp"
@@ -32,7 +33,7 @@ namespace {
 struct SscanParams {
   Seqs seq;
   int32_t D, N, G, Dg, per_group;  // Dg = D / G channels in per_group workgroups
-  int32_t phase, piece;            // 1: the pieces from zero and the first ones in full, 2: the others
+  int32_t piece;                   // rows of a piece
   int32_t softplus, yf16, sf16;
   const void *x, *delta, *B, *C, *z;
   int64_t xs, ds, bs, cs, zs, ys;
@@ -66,6 +67,11 @@ __device__ __forceinline__ float softplus(float v) {
 __device__ __forceinline__ float silu(float v) {
   const float e = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e), r = __builtin_amdgcn_rcpf(1.0f + e);
   return v * (v < 0.0f ? e * r : r);
+}
+
+// a where mask is all ones, b where it is 0: a choice that stays one instruction, not a branch.
+__device__ __forceinline__ float choose(uint32_t mask, float a, float b) {
+  return __uint_as_float((__float_as_uint(a) & mask) | (__float_as_uint(b) & ~mask));
 }
 
 // A log2(e), finite: e^(0 A) is 1 for an infinite A too, as a row that does not count needs it.
@@ -122,111 +128,163 @@ __device__ __forceinline__ void load_decay(const SscanParams& p, int d, int q, f
 
 constexpr int kRows = 32;  // rows of B and C in LDS at a time
 
-template <int NPL, typename T>
+constexpr int kBufferWord3 = 0x00020000;  // buffer resource word 3 for raw 32-bit access (gfx9)
+constexpr uint32_t kNowhere = 0x80000000u;  // a byte offset behind every buffer below
+
+// Rows t .. min(t + kRows, end) - 1 of a tensor (none of a null one). Loads past them give 0 and stores past them are
+// dropped (the range check counts the scalar offset in), so no access needs a branch; strides of at most 2^23 elements
+// keep kRows rows inside 32 bits.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, int t, int end, int64_t stride, int size, int cols) {
+  const int rows = p ? min(end - t, kRows) : 0;
+  const char* q = reinterpret_cast<const char*>(p) + (rows > 0 ? t * stride * size : 0);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(q), (short)0, rows > 0 ? (int)(((rows - 1) * stride + cols) * size) : 0, kBufferWord3);
+}
+
+template <typename T>
+__device__ __forceinline__ T load1(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
+  if constexpr (sizeof(T) == 2) return (T)__builtin_amdgcn_raw_buffer_load_b16(r, voff, soff, 0);
+  else return (T)__builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, 0);
+}
+
+// f(0), ..., f(N - 1), as constants.
+template <int N, typename F>
+__device__ __forceinline__ void unrolled(F f) {
+  if constexpr (N > 0) {
+    unrolled<N - 1>(f);
+    f(std::integral_constant<int, N - 1>());
+  }
+}
+
+// u * b[J], of fp16 values in one instruction each.
+template <int J>
+__device__ __forceinline__ float times(float u, const uint32_t* b) { return u * __uint_as_float(b[J]); }
+template <int J>
+__device__ __forceinline__ float times(float u, const uint16_t* b) {
+  uint32_t w;
+  __builtin_memcpy(&w, b + (J & ~1), 4);
+  float r;
+  if constexpr (J & 1) asm("v_fma_mix_f32 %0, %1, %2, 0 op_sel:[0,1,0] op_sel_hi:[0,1,0]" : "=v"(r) : "v"(u), "v"(w));
+  else asm("v_fma_mix_f32 %0, %1, %2, 0 op_sel_hi:[0,1,0]" : "=v"(r) : "v"(u), "v"(w));
+  return r;
+}
+
+template <int NPL, typename T, typename Y>
 struct Piece {
-  static constexpr int kNP = 4 * NPL, kTS = kRows, kBatches = kTS / 4, kPer = kTS * 2 * kNP / 256;
+  static constexpr bool kY = !std::is_same_v<Y, void>;  // with y
+  static constexpr int kNP = 4 * NPL, kBatches = kRows / 4, kPer = kRows * kNP / 256, kSize = sizeof(T);
+  static constexpr int kYSize = std::is_same_v<Y, __half> ? 2 : 4;
+  static constexpr int kAhead = kSize * NPL <= 8 ? 4 : kSize * NPL <= 16 ? 2 : 1;  // rows of B and C fetched ahead
+  static constexpr int kAlign = kSize * NPL < 16 ? kSize * NPL : 16;
   const SscanParams& p;
   const int d, q, g;  // the lane's channel (clamped), its place in the four, the B/C group
   const bool live;
-  float* const lds;   // [2][kTS][2][kNP]
-  T xr[kBatches], dr[kBatches], zr[kBatches], bc[kPer];
+  T* const lds;       // [2][kRows][4][2][NPL]: a lane's values of B and C of a row side by side
+  T xr[kBatches], dr[kBatches], zr[kBatches], br[kPer], cr[kPer];
 
-  // row t + 4 i + q of batch i
-  template <bool Z>
-  __device__ __forceinline__ void load_rows(int t, int end) {
-    const T* x = reinterpret_cast<const T*>(p.x) + (int64_t)(t + q) * p.xs + d;
-    const T* dl = reinterpret_cast<const T*>(p.delta) + (int64_t)(t + q) * p.ds + d;
-    const T* z = Z ? reinterpret_cast<const T*>(p.z) + (int64_t)(t + q) * p.zs + d : nullptr;
-#pragma unroll
-    for (int i = 0; i < kBatches; ++i) {
-      const bool in = t + 4 * i + q < end;
-      xr[i] = dr[i] = zr[i] = 0;
-      if (in) {
-        xr[i] = x[4 * i * p.xs];
-        dr[i] = dl[4 * i * p.ds];
-        if (Z) zr[i] = z[4 * i * p.zs];
-      }
-    }
+  // x, delta and z of row t + 4 i + q, for batch i
+  __device__ __forceinline__ void load_rows(int i, __amdgpu_buffer_rsrc_t rx, __amdgpu_buffer_rsrc_t rd, __amdgpu_buffer_rsrc_t rz) {
+    const auto at = [&](__amdgpu_buffer_rsrc_t r, int64_t stride) {
+      return load1<T>(r, (uint32_t)(q * (int)stride + d) * kSize, (uint32_t)(4 * i * (int)stride) * kSize);
+    };
+    xr[i] = at(rx, p.xs);
+    dr[i] = at(rd, p.ds);
+    if (kY) zr[i] = at(rz, p.zs);
   }
 
+  // this thread's part of B and C: state k of rows row, row + 256 / kNP, ...
   __device__ __forceinline__ void load_bc(int t, int end) {
+    const int k = threadIdx.x % kNP, row = threadIdx.x / kNP, cols = p.G * p.N;
+    const auto rb = rows_rsrc(p.B, t, end, p.bs, kSize, cols), rc = rows_rsrc(kY ? p.C : nullptr, t, end, p.cs, kSize, cols);
+    const uint32_t vb = k < p.N ? (uint32_t)(row * (int)p.bs + g * p.N + k) * kSize : kNowhere;
+    const uint32_t vc = k < p.N ? (uint32_t)(row * (int)p.cs + g * p.N + k) * kSize : kNowhere;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int e = threadIdx.x + 256 * i, row = e / (2 * kNP), k = e % kNP;
-      const bool isC = (e / kNP) & 1;
-      bc[i] = 0;
-      if (t + row < end && k < p.N)
-        bc[i] = isC ? reinterpret_cast<const T*>(p.C)[(int64_t)(t + row) * p.cs + g * p.N + k]
-                    : reinterpret_cast<const T*>(p.B)[(int64_t)(t + row) * p.bs + g * p.N + k];
+      br[i] = load1<T>(rb, vb, (uint32_t)(i * (256 / kNP) * (int)p.bs) * kSize);
+      if (kY) cr[i] = load1<T>(rc, vc, (uint32_t)(i * (256 / kNP) * (int)p.cs) * kSize);
     }
   }
 
   __device__ __forceinline__ void store_bc(int buf) {
+    const int k = threadIdx.x % kNP, row = threadIdx.x / kNP;
+    T* at = lds + ((buf * kRows + row) * 4 + k / NPL) * 2 * NPL + k % NPL;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) lds[buf * kTS * 2 * kNP + threadIdx.x + 256 * i] = as_float(bc[i]);
+    for (int i = 0; i < kPer; ++i) {
+      at[i * (256 / kNP) * 2 * kNP] = br[i];
+      if (kY) at[i * (256 / kNP) * 2 * kNP + NPL] = cr[i];
+    }
   }
 
   // Rows begin .. end - 1 from the state in h, which becomes the state behind them; returns the sum of dt (the
-  // lane's rows). Y: with y.
-  template <bool Y>
+  // lane's rows; without y only).
   __device__ __forceinline__ float run(int begin, int end, const float (&a)[NPL], float (&h)[NPL]) {
-    const float bias = p.bias ? p.bias[d] : 0.0f, skip = p.Dskip ? p.Dskip[d] : 0.0f;
+    const float bias = p.bias ? p.bias[d] : 0.0f, skip = kY && p.Dskip ? p.Dskip[d] : 0.0f;
+    const uint32_t sp = p.softplus ? ~0u : 0u, gate = p.z ? ~0u : 0u;
+    const uint32_t yv = live ? (uint32_t)(q * (int)p.ys + d) * kYSize : kNowhere, ystep = (uint32_t)(4 * (int)p.ys) * kYSize;
     float sum = 0.0f;
-    const bool gate = Y && p.z;
-    const auto rows = [&](int t) {
-      if (gate) load_rows<true>(t, end);
-      else load_rows<false>(t, end);
-    };
+    const auto rx_of = [&](int t) { return rows_rsrc(p.x, t, end, p.xs, kSize, p.D); };
+    const auto rd_of = [&](int t) { return rows_rsrc(p.delta, t, end, p.ds, kSize, p.D); };
+    const auto rz_of = [&](int t) { return rows_rsrc(kY ? p.z : nullptr, t, end, p.zs, kSize, p.D); };
     load_bc(begin, end);
-    rows(begin);
-    __syncthreads();  // (a piece before this one may have left its last rows in LDS)
+    {
+      const auto rx = rx_of(begin), rd = rd_of(begin), rz = rz_of(begin);
+#pragma unroll
+      for (int i = 0; i < kBatches; ++i) load_rows(i, rx, rd, rz);
+    }
     store_bc(0);
     __syncthreads();
     int buf = 0;
-    for (int t = begin; t < end; t += kTS, buf ^= 1) {
-      T xc[kBatches], dc[kBatches], zc[kBatches];
+    for (int t = begin; t < end; t += kRows, buf ^= 1) {
+      // (behind the last rows these are empty)
+      const auto rx = rx_of(t + kRows), rd = rd_of(t + kRows), rz = rz_of(t + kRows);
+      const auto ry = rows_rsrc(kY ? p.y : nullptr, t, end, p.ys, kYSize, p.D);
+      load_bc(t + kRows, end);
+      const T* rows = lds + buf * kRows * 2 * kNP + q * 2 * NPL;
+      T now[kAhead][2 * NPL], next[kAhead][2 * NPL];
+      const auto fetch = [&](int unit) {
 #pragma unroll
-      for (int i = 0; i < kBatches; ++i) xc[i] = xr[i], dc[i] = dr[i], zc[i] = zr[i];
-      const bool more = end - t > kTS;
-      if (more) {
-        load_bc(t + kTS, end);
-        rows(t + kTS);
-      }
+        for (int n = 0; n < kAhead; ++n)
+          __builtin_memcpy(next[n], __builtin_assume_aligned(rows + (unit * kAhead + n) * 2 * kNP, kAlign), (kY ? 2 : 1) * sizeof(T) * NPL);
+      };
+      fetch(0);
 #pragma unroll
       for (int i = 0; i < kBatches; ++i) {
-        const int row = t + 4 * i + q;
-        if (t + 4 * i >= end) break;
-        const bool in = row < end;
-        const float x = as_float(xc[i]), dl = as_float(dc[i]) + bias;
-        const float dt = in ? (p.softplus ? softplus(dl) : dl) : 0.0f, u = in ? dt * x : 0.0f;
-        if (!Y) sum += dt;
+        if (i % 2 == 0 && t + 4 * i >= end) break;
+        const float x = as_float(xr[i]), dl = as_float(dr[i]) + bias, z = kY ? as_float(zr[i]) : 0.0f;
+        load_rows(i, rx, rd, rz);  // the next rows' into their place
+        // past the end: dt 0, and u too (x is 0 there)
+        const float dt = q < end - t - 4 * i ? choose(sp, softplus(dl), dl) : 0.0f, u = dt * x;
+        if (!kY) sum += dt;
         float part[4];
         const auto step = [&](auto k) {
           constexpr int K = decltype(k)::value;
-          const float ds = lane4<K>(dt), us = lane4<K>(u);
-          const float* bq = lds + ((buf * kTS + 4 * i + K) * 2) * kNP + q * NPL;
-          part[K] = 0.0f;
+          const int unit = (4 * i + K) / kAhead;
+          if (K % kAhead == 0) {
 #pragma unroll
-          for (int j = 0; j < NPL; ++j) {
-            h[j] = fmaf(__builtin_amdgcn_exp2f(ds * a[j]), h[j], us * bq[j]);
-            if (Y) part[K] = fmaf(bq[kNP + j], h[j], part[K]);
+            for (int n = 0; n < kAhead; ++n) {
+#pragma unroll
+              for (int j = 0; j < 2 * NPL; ++j) now[n][j] = next[n][j];
+            }
+            // the next rows' values are on their way while these are used (and no further ones: they would fill the registers)
+            if (unit + 1 < kRows / kAhead) fetch(unit + 1);
+            asm volatile("" ::: "memory");
           }
+          const float ds = lane4<K>(dt), us = lane4<K>(u);
+          const T* bq = now[K % kAhead];
+          part[K] = 0.0f;
+          unrolled<NPL>([&](auto n) {
+            constexpr int j = decltype(n)::value;
+            h[j] = fmaf(__builtin_amdgcn_exp2f(ds * a[j]), h[j], times<j>(us, bq));
+            if (kY) part[K] = fmaf(as_float(bq[NPL + j]), h[j], part[K]);
+          });
         };
-        step(std::integral_constant<int, 0>());
-        step(std::integral_constant<int, 1>());
-        step(std::integral_constant<int, 2>());
-        step(std::integral_constant<int, 3>());
-        if (Y) {
-          float y = fmaf(skip, x, join4(part, q));
-          if (gate) y *= silu(as_float(zc[i]));
-          if (in && live) {
-            const int64_t at = (int64_t)row * p.ys + d;
-            if (p.yf16) reinterpret_cast<__half*>(p.y)[at] = __float2half_rn(y);
-            else reinterpret_cast<float*>(p.y)[at] = y;
-          }
+        unrolled<4>(step);
+        if constexpr (kY) {
+          const float y = fmaf(skip, x, join4(part, q)) * choose(gate, silu(z), 1.0f);
+          if constexpr (kYSize == 2) __builtin_amdgcn_raw_buffer_store_b16(__half_as_ushort(__float2half_rn(y)), ry, yv, i * ystep, 0);
+          else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y), ry, yv, i * ystep, 0);
         }
       }
-      if (more) {
+      if (end - t > kRows) {
         store_bc(buf ^ 1);
         __syncthreads();
       }
@@ -235,10 +293,13 @@ struct Piece {
   }
 };
 
-template <int NPL, typename T>
+// Y void: the ends of the pieces that have one behind them, the first ones' from the initial state, the others' from
+// zero; else every piece with y, from the state that it folds from the ends.
+template <int NPL, typename T, typename Y>
 __global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
   constexpr int kNP = 4 * NPL;
-  __shared__ __align__(16) float lds[2 * kRows * 2 * kNP];
+  constexpr bool kY = !std::is_same_v<Y, void>;
+  __shared__ __align__(16) T lds[2 * kRows * 2 * kNP];
   const int blocks = p.G * p.per_group, cb = blockIdx.x % blocks;
   const int64_t at = blockIdx.x / blocks;  // piece slot: sequence i has begin(i) / piece + i and the ones behind it
   const Seqs& sq = p.seq;
@@ -246,10 +307,10 @@ __global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
   if (sq.offsets) i = last_not_above(sq.nseq, at, [&](int k) { return (int64_t)(seq_begin(sq, k) / p.piece + k); });
   else i = last_not_above(sq.nseq, at, [&](int k) { return (int64_t)(k * sq.each / p.piece + k); });
   const int begin = uniform(seq_begin(sq, i)), end = uniform(seq_end(sq, i, begin));
-  const int64_t chunk = at - (begin / p.piece + i), pieces = max((int64_t)((int64_t)(end - begin) + p.piece - 1) / p.piece, (int64_t)1);
+  const int chunk = (int)(at - (begin / p.piece + i)), pieces = max((int)(((uint32_t)(end - begin) + p.piece - 1) / (uint32_t)p.piece), 1);
   if (chunk < 0 || chunk >= pieces) return;
   const bool last = chunk == pieces - 1;
-  if (p.phase == 1 ? chunk > 0 && last : chunk == 0) return;
+  if (!kY && last) return;
   const int g = cb / p.per_group, q = threadIdx.x & 3;
   const int dg = cb % p.per_group * 64 + (threadIdx.x >> 2);
   const int d = g * p.Dg + min(dg, p.Dg - 1);
@@ -259,34 +320,42 @@ __global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
   const int64_t slot = seq_slot(sq, i);
   const int64_t size = (int64_t)p.D * (kNP + 1);
   float* ends = p.carry + at * size + (int64_t)d * kNP + q * NPL;
-  if (p.phase == 1) {
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) h[j] = 0.0f;
-    if (chunk == 0) load_state(p, slot, !sq.has || sq.has[i] != 0, d, q, h);
-  } else {
+  for (int j = 0; j < NPL; ++j) h[j] = 0.0f;
+  if (chunk == 0 && (last || !kY)) {
+    load_state(p, slot, !sq.has || sq.has[i] != 0, d, q, h);
+    // the last piece's slot has no ends: it keeps the initial state, which the last piece may overwrite in `state`
+    if (!kY && live) {
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) ends[(pieces - 1) * size + j] = h[j];
+    }
+  } else if (kY && chunk == 0) {
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) h[j] = ends[(pieces - 1) * size + j];
+  } else if (kY) {
     const float* from = ends - chunk * size;
     const float* sums = p.carry + (at - chunk) * size + (int64_t)p.D * kNP + d;
 #pragma unroll
     for (int j = 0; j < NPL; ++j) h[j] = from[j];
 #pragma unroll 4
-    for (int64_t c = 1; c < chunk; ++c) {
+    for (int c = 1; c < chunk; ++c) {
       const float s = sums[c * size];
 #pragma unroll
       for (int j = 0; j < NPL; ++j) h[j] = fmaf(__builtin_amdgcn_exp2f(s * a[j]), h[j], from[c * size + j]);
     }
   }
-  Piece<NPL, T> piece{p, d, q, g, live, lds};
-  const int b = begin + (int)chunk * p.piece, e = last ? end : b + p.piece;
-  if (p.phase == 1 && chunk > 0) {
-    const float sum = sum4(piece.template run<false>(b, e, a, h));
+  Piece<NPL, T, Y> piece{p, d, q, g, live, lds};
+  const int b = begin + chunk * p.piece, e = last ? end : b + p.piece;
+  float sum = 0.0f;
+  if (b < e) sum = piece.run(b, e, a, h);
+  if (!kY) {
+    sum = sum4(sum);
     if (live && q == 0) p.carry[at * size + (int64_t)p.D * kNP + d] = sum;
-  } else if (b < e) {
-    piece.template run<true>(b, e, a, h);
   }
   if (!live) return;
   if (last) {
     store_state(p, slot, d, q, h);
-  } else if (p.phase == 1) {
+  } else if (!kY) {
 #pragma unroll
     for (int j = 0; j < NPL; ++j) ends[j] = h[j];
   }
@@ -332,11 +401,16 @@ int npl_of(int64_t N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
 int64_t blocks_of(const qssm_sscan_args& a) { return a.ngroups * cdiv(a.dim / a.ngroups, 64); }
 
-// Rows of a piece.
+// Rows of a piece. A cut costs nearly twice the work, and pays where whole sequences leave SIMDs (1024 of them) without a
+// wave or wait for the longest one: sequences of one length that give nearly all of them a wave run whole (16 of
+// 1024 rows, 4096 channels: 298 us, 431 in pieces of 256; 8 of 1024, 1536 channels, three quarters of the SIMDs: 120,
+// and 103 in pieces of 128); others run in pieces that give about 6 waves a SIMD, of 64 to 256 rows (1 x 8192
+// rows, 1536 channels, pieces of 64 / 128 / 256 / 512: 147 / 123 / 118 / 149 us, whole 900; 24 sequences of very different
+// lengths, 16384 rows, 4096 channels: 567 / 485 / 457 / 465, whole 708; 100 of them, 1536 channels: 212 / 203 / 223 / 281, 220).
 int64_t piece_rows(const qssm_sscan_args& a) {
   const int64_t waves = 4 * blocks_of(a), whole = std::max<int64_t>(a.tokens, 1);
-  if (a.nseq * waves >= 768) return a.seq_offsets ? std::min(whole, std::max<int64_t>(64, 4 * cdiv(whole, a.nseq))) : whole;
-  return std::min(whole, std::max<int64_t>(64, cdiv(cdiv(whole * waves, 2048), 32) * 32));
+  if (!a.seq_offsets && a.nseq * waves >= 900) return whole;
+  return std::min<int64_t>(whole, std::clamp<int64_t>((whole * waves / 6144 + 16) / 32 * 32, 64, 256));
 }
 
 bool is_cut(const qssm_sscan_args& a, int64_t piece) {
@@ -359,13 +433,12 @@ qssm_status launch(SscanParams p, const qssm_sscan_args& a, hipStream_t stream) 
   }
   const int64_t blocks = (a.tokens / p.piece + a.nseq) * blocks_of(a);
   if (blocks > kMaxBlocks) return fail(QSSM_ERR_UNSUPPORTED, "tokens * dim too large");
-  p.phase = 1;
-  k_selective_scan<NPL, T><<<(unsigned)blocks, 256, 0, stream>>>(p);
   if (is_cut(a, p.piece)) {
+    k_selective_scan<NPL, T, void><<<(unsigned)blocks, 256, 0, stream>>>(p);
     if (const qssm_status s = launch_status("selective_scan")) return s;
-    p.phase = 2;
-    k_selective_scan<NPL, T><<<(unsigned)blocks, 256, 0, stream>>>(p);
   }
+  if (p.yf16) k_selective_scan<NPL, T, __half><<<(unsigned)blocks, 256, 0, stream>>>(p);
+  else k_selective_scan<NPL, T, float><<<(unsigned)blocks, 256, 0, stream>>>(p);
   return launch_status("selective_scan");
 }
 
@@ -407,6 +480,8 @@ extern "C" qssm_status qssm_selective_scan(const qssm_sscan_args* a, void* works
   if (a->state_dtype != QSSM_F32 && a->state_dtype != QSSM_F16)
     return fail(QSSM_ERR_INVALID_ARG, "state_dtype must be QSSM_F32 or QSSM_F16");
   if (a->reserved != 0) return fail(QSSM_ERR_INVALID_ARG, "reserved must be 0");
+  for (const int64_t stride : {a->x_stride, a->delta_stride, a->B_stride, a->C_stride, a->z_stride, a->y_stride})
+    if (stride > (1 << 23)) return fail(QSSM_ERR_UNSUPPORTED, "a stride above 2^23");
   const int64_t sx = type_size(a->io_dtype), sy = type_size(a->y_dtype), ss = type_size(a->state_dtype);
   if (const qssm_status s = check_rows("x", a->x, T, D, a->x_stride, sx)) return s;
   if (const qssm_status s = check_rows("delta", a->delta, T, D, a->delta_stride, sx)) return s;
