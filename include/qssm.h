@@ -627,7 +627,7 @@ qssm_status qssm_causal_conv(const qssm_conv_args* a, hipStream_t stream);
  *     y[t, d] = (sum_n C[t, g * dstate + n] * h[n] + Dskip[d] * x[t, d]) * silu(z[t, d])
  * x, delta, z [tokens, dim] and B, C [tokens, ngroups * dstate] have one type (io_dtype, fp32 or fp16); z NULL: no
  * gate. A [dim, dstate], Dskip [dim] (NULL: 0) and delta_bias [dim] (NULL: 0) are fp32. All arithmetic is
- * fp32. The state [slots, dim, dstate] is fp32, or fp16, which is rounded to nearest even once per call
+ * fp32; an infinite dt * x makes what follows infinite or NaN. The state [slots, dim, dstate] is fp32, or fp16, which is rounded to nearest even once per call
  * and sequence (the decode cache in half the bytes; inside a call the state is fp32).
  * Long sequences are cut into pieces that run in parallel: every piece but a sequence's last runs from
  * zero, then every piece again from its entering state, which is folded from the ends of the pieces before it (in their order, so results do not vary from call to call). How long the pieces

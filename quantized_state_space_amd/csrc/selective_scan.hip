@@ -96,22 +96,46 @@ __device__ __forceinline__ float sum4(float v) {
   return v + dpp_partner<2>(v);
 }
 
+// A lane's states of one channel, in one load or store where the channel has 4 NPL.
 template <int NPL>
 __device__ __forceinline__ void load_state(const SscanParams& p, int64_t slot, bool has, int d, int q, float (&h)[NPL]) {
   const bool given = p.state && slot >= 0 && has;
   const int64_t at = (slot * p.D + d) * p.N + q * NPL;
 #pragma unroll
-  for (int j = 0; j < NPL; ++j) {
-    h[j] = 0.0f;
-    if (given && q * NPL + j < p.N)
-      h[j] = p.sf16 ? __half2float(reinterpret_cast<const __half*>(p.state)[at + j]) : reinterpret_cast<const float*>(p.state)[at + j];
+  for (int j = 0; j < NPL; ++j) h[j] = 0.0f;
+  if (!given) return;
+  if (p.N == 4 * NPL) {
+    if (p.sf16) {
+      __half v[NPL];
+      __builtin_memcpy(v, reinterpret_cast<const __half*>(p.state) + at, sizeof(v));
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) h[j] = __half2float(v[j]);
+    } else {
+      __builtin_memcpy(h, reinterpret_cast<const float*>(p.state) + at, sizeof(h));
+    }
+    return;
   }
+#pragma unroll
+  for (int j = 0; j < NPL; ++j)
+    if (q * NPL + j < p.N)
+      h[j] = p.sf16 ? __half2float(reinterpret_cast<const __half*>(p.state)[at + j]) : reinterpret_cast<const float*>(p.state)[at + j];
 }
 
 template <int NPL>
 __device__ __forceinline__ void store_state(const SscanParams& p, int64_t slot, int d, int q, const float (&h)[NPL]) {
   if (!p.state_out || slot < 0) return;
   const int64_t at = (slot * p.D + d) * p.N + q * NPL;
+  if (p.N == 4 * NPL) {
+    if (p.sf16) {
+      __half v[NPL];
+#pragma unroll
+      for (int j = 0; j < NPL; ++j) v[j] = __float2half_rn(h[j]);
+      __builtin_memcpy(reinterpret_cast<__half*>(p.state_out) + at, v, sizeof(v));
+    } else {
+      __builtin_memcpy(reinterpret_cast<float*>(p.state_out) + at, h, sizeof(h));
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < NPL; ++j)
     if (q * NPL + j < p.N) {
@@ -361,38 +385,60 @@ __global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
   }
 }
 
-// One row a sequence: four lanes own a channel of one sequence.
-template <int NPL, typename T>
+// One row a sequence: four lanes own a channel of R sequences, whose decays, bias and skip are loaded once. Bound by the
+// bytes of the states: 256 sequences, 4096 channels, 16 fp32 states: TODO.
+template <int NPL, int R, typename T>
 __global__ __launch_bounds__(256) void k_selective_step(SscanParams p) {
-  const int64_t id = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2);
-  const int q = threadIdx.x & 3;
-  const int64_t all = (int64_t)p.seq.nseq * p.D;
-  const bool live = id < all;
-  const int i = (int)(min(id, all - 1) / p.D), d = (int)(min(id, all - 1) % p.D), g = d / p.Dg;
-  const int64_t slot = seq_slot(p.seq, i);
-  float a[NPL], h[NPL];
-  load_decay(p, d, q, a);
-  load_state(p, slot, !p.seq.has || p.seq.has[i] != 0, d, q, h);
-  const float x = as_float(reinterpret_cast<const T*>(p.x)[(int64_t)i * p.xs + d]);
-  float dl = as_float(reinterpret_cast<const T*>(p.delta)[(int64_t)i * p.ds + d]) + (p.bias ? p.bias[d] : 0.0f);
-  const T* b = reinterpret_cast<const T*>(p.B) + (int64_t)i * p.bs + g * p.N + q * NPL;
-  const T* c = reinterpret_cast<const T*>(p.C) + (int64_t)i * p.cs + g * p.N + q * NPL;
-  const float dt = p.softplus ? softplus(dl) : dl, u = dt * x;
-  float y = 0.0f;
+  const int cb = blockIdx.x % (p.G * p.per_group), g = cb / p.per_group, q = threadIdx.x & 3;
+  const int dg = cb % p.per_group * 64 + (threadIdx.x >> 2);
+  const int d = g * p.Dg + min(dg, p.Dg - 1);
+  const bool live = dg < p.Dg;
+  const int i0 = (int)(blockIdx.x / (p.G * p.per_group)) * R;
+  float h[R][NPL], x[R], dl[R], z[R];
+  T b[R][NPL], c[R][NPL];
+  int64_t slot[R];
+  const auto part = [&](const void* from, int64_t at, T (&to)[NPL]) {
+    const T* v = reinterpret_cast<const T*>(from) + at + g * p.N + q * NPL;
+    if (p.N == 4 * NPL) {
+      __builtin_memcpy(to, v, sizeof(to));
+    } else {
 #pragma unroll
-  for (int j = 0; j < NPL; ++j)
-    if (q * NPL + j < p.N) {
-      h[j] = fmaf(__builtin_amdgcn_exp2f(dt * a[j]), h[j], u * as_float(b[j]));
-      y = fmaf(as_float(c[j]), h[j], y);
+      for (int j = 0; j < NPL; ++j) to[j] = q * NPL + j < p.N ? v[j] : T(0);
     }
-  y = fmaf(p.Dskip ? p.Dskip[d] : 0.0f, x, sum4(y));
-  if (p.z) y *= silu(as_float(reinterpret_cast<const T*>(p.z)[(int64_t)i * p.zs + d]));
-  if (!live) return;
-  if (q == 0) {
-    if (p.yf16) reinterpret_cast<__half*>(p.y)[(int64_t)i * p.ys + d] = __float2half_rn(y);
-    else reinterpret_cast<float*>(p.y)[(int64_t)i * p.ys + d] = y;
+  };
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = min(i0 + r, p.seq.nseq - 1);
+    slot[r] = seq_slot(p.seq, i);
+    load_state(p, slot[r], !p.seq.has || p.seq.has[i] != 0, d, q, h[r]);
+    x[r] = as_float(reinterpret_cast<const T*>(p.x)[(int64_t)i * p.xs + d]);
+    dl[r] = as_float(reinterpret_cast<const T*>(p.delta)[(int64_t)i * p.ds + d]);
+    z[r] = p.z ? as_float(reinterpret_cast<const T*>(p.z)[(int64_t)i * p.zs + d]) : 0.0f;
+    part(p.B, (int64_t)i * p.bs, b[r]);
+    part(p.C, (int64_t)i * p.cs, c[r]);
   }
-  store_state(p, slot, d, q, h);
+  float a[NPL];
+  load_decay(p, d, q, a);
+  const float bias = p.bias ? p.bias[d] : 0.0f, skip = p.Dskip ? p.Dskip[d] : 0.0f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = i0 + r;
+    const float v = dl[r] + bias, dt = p.softplus ? softplus(v) : v, u = dt * x[r];
+    float y = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+      h[r][j] = fmaf(__builtin_amdgcn_exp2f(dt * a[j]), h[r][j], u * as_float(b[r][j]));
+      y = fmaf(as_float(c[r][j]), h[r][j], y);
+    }
+    y = fmaf(skip, x[r], sum4(y));
+    if (p.z) y *= silu(z[r]);
+    if (!live || i >= p.seq.nseq) continue;
+    if (q == 0) {
+      if (p.yf16) reinterpret_cast<__half*>(p.y)[(int64_t)i * p.ys + d] = __float2half_rn(y);
+      else reinterpret_cast<float*>(p.y)[(int64_t)i * p.ys + d] = y;
+    }
+    store_state(p, slot[r], d, q, h[r]);
+  }
 }
 
 constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;  // a grid holds fewer than 2^32 threads
@@ -426,9 +472,13 @@ bool is_step(const qssm_sscan_args& a) { return !a.seq_offsets && a.tokens == a.
 template <int NPL, typename T>
 qssm_status launch(SscanParams p, const qssm_sscan_args& a, hipStream_t stream) {
   if (is_step(a)) {
-    const int64_t blocks = cdiv(a.nseq * a.dim, 64);
+    // several sequences a lane where that leaves a wave to every SIMD
+    constexpr int kR = NPL <= 4 ? 4 : NPL <= 8 ? 2 : 1;
+    const int64_t several = cdiv(a.nseq, kR) * blocks_of(a);
+    const int64_t blocks = several >= 256 ? several : a.nseq * blocks_of(a);
     if (blocks > kMaxBlocks) return fail(QSSM_ERR_UNSUPPORTED, "nseq * dim above 2^30");
-    k_selective_step<NPL, T><<<(unsigned)blocks, 256, 0, stream>>>(p);
+    if (several >= 256) k_selective_step<NPL, kR, T><<<(unsigned)blocks, 256, 0, stream>>>(p);
+    else k_selective_step<NPL, 1, T><<<(unsigned)blocks, 256, 0, stream>>>(p);
     return launch_status("selective_scan");
   }
   const int64_t blocks = (a.tokens / p.piece + a.nseq) * blocks_of(a);
