@@ -53,16 +53,30 @@ struct GemmParams {
 // to 2^25) it overflows only where the result does.
 __device__ __forceinline__ float valid_or_zero(float s) { return s >= 0x1p-60f && s <= 0x1p60f ? s : 0.0f; }
 
-// 16 codes of a row from k on, at any address; codes at or past K are 0 and not read.
+// 16 codes of a row from k on, at any address (the hardware takes unaligned 16-byte loads); codes at or past K are 0 and
+// not read. A chunk that reaches past K is the end of the row's last 16 codes, shifted into place without a
+// branch, so that a thread's loads are in flight together; K >= 16 (load16_short: any K, byte by byte).
 __device__ __forceinline__ uint4 load16(const uint8_t* row, int64_t k, int64_t K) {
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-  if (k + 16 <= K) {
-    __builtin_memcpy(w, row + k, 16);
-  } else {
+  const int64_t at = min(k, K - 16);
+  uint32_t w[4];
+  __builtin_memcpy(w, row + at, 16);
+  const int n = (int)min(k - at, (int64_t)16);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (k + i < K) w[i / 4] |= (uint32_t)row[k + i] << (8 * (i % 4));
-  }
+  for (int i = 0; i < 4; ++i) w[i] = (n & 16) ? 0u : w[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (n & 8) ? (i < 2 ? w[(i + 2) & 3] : 0u) : w[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (n & 4) ? (i < 3 ? w[(i + 1) & 3] : 0u) : w[i];
+  const uint32_t b = n & 3;
+  return make_uint4(__builtin_amdgcn_alignbyte(w[1], w[0], b), __builtin_amdgcn_alignbyte(w[2], w[1], b),
+                    __builtin_amdgcn_alignbyte(w[3], w[2], b), __builtin_amdgcn_alignbyte(0u, w[3], b));
+}
+
+__device__ __forceinline__ uint4 load16_short(const uint8_t* row, int64_t k, int64_t K) {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (k + i < K) w[i / 4] |= (uint32_t)row[k + i] << (8 * (i % 4));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -186,6 +200,7 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, uint8_t* sm, const
       for (int c0 = 0; c0 < kCols; c0 += kLine) {
         const int c = c0 + lane % kLine;
         if (nw + c < p.N)
+#pragma unroll 8
           for (int r = lane / kLine; r < 32; r += kStep)
             if (mb + r < p.M) y[(mb + r) * p.ys + nw + c] = reinterpret_cast<const T*>(buf + r * kRowB)[c];
       }
@@ -418,8 +433,9 @@ __global__ __launch_bounds__(WM * WN * KG * 64) void k_gemm_f8_tile(GemmParams p
 }
 
 // Tiles of 64 x 64, a quarter a wave, with the operands through registers: rows at any address, any K.
-template <bool EXACT>
+template <bool EXACT, bool SHORT>
 __global__ __launch_bounds__(256) void k_gemm_f8_any(GemmParams p) {
+  constexpr auto load_chunk = SHORT ? load16_short : load16;
   __shared__ __align__(16) uint8_t sm[2][2][64 * 128];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), kh = lane >> 5;
   const int64_t nm = (p.M + 63) / 64;
@@ -432,8 +448,8 @@ __global__ __launch_bounds__(256) void k_gemm_f8_any(GemmParams p) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int row = (tid + 256 * i) / 8, c = tid % 8;
-      va[i] = load16(p.a + min(m0 + row, p.M - 1) * p.as, (int64_t)b * 128 + c * 16, p.K);
-      vw[i] = load16(p.w + min(n0 + row, p.N - 1) * p.ws, (int64_t)b * 128 + c * 16, p.K);
+      va[i] = load_chunk(p.a + min(m0 + row, p.M - 1) * p.as, (int64_t)b * 128 + c * 16, p.K);
+      vw[i] = load_chunk(p.w + min(n0 + row, p.N - 1) * p.ws, (int64_t)b * 128 + c * 16, p.K);
     }
   };
   const auto store = [&](int st) {
@@ -526,8 +542,12 @@ __global__ __launch_bounds__(W * 64) void k_gemm_f8_few(GemmParams p) {
     v4i fw[2], fa[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      fw[h] = __builtin_bit_cast(v4i, load16(w - q * 16, (int64_t)full * 128 + h * 64 + q * 16, p.K));
-      fa[h] = __builtin_bit_cast(v4i, load16(a - q * 16, (int64_t)full * 128 + h * 64 + q * 16, p.K));
+      const auto chunk = [&](const uint8_t* row) {
+        const int64_t k = (int64_t)full * 128 + h * 64 + q * 16;
+        return __builtin_bit_cast(v4i, p.K < 16 ? load16_short(row - q * 16, k, p.K) : load16(row - q * 16, k, p.K));
+      };
+      fw[h] = chunk(w);
+      fa[h] = chunk(a);
     }
     add(full, fw, fa, sa[full * p.sas]);
   }
@@ -555,7 +575,9 @@ void launch(const GemmParams& p, hipStream_t stream) {
   }
   // direct loads to LDS take multiples of 4 bytes, and whole blocks
   if (((uintptr_t)p.a | (uintptr_t)p.w | (uintptr_t)p.as | (uintptr_t)p.ws) % 4 != 0 || p.K < 128) {
-    k_gemm_f8_any<EXACT><<<(unsigned)(cdiv(p.M, 64) * cdiv(p.N, 64)), 256, 0, stream>>>(p);
+    const unsigned grid = (unsigned)(cdiv(p.M, 64) * cdiv(p.N, 64));
+    if (p.K < 16) k_gemm_f8_any<EXACT, true><<<grid, 256, 0, stream>>>(p);
+    else k_gemm_f8_any<EXACT, false><<<grid, 256, 0, stream>>>(p);
     return;
   }
   switch (choose_form(p.M, p.N, p.K, !EXACT)) {
