@@ -438,8 +438,8 @@ __global__ __launch_bounds__(256) void k_gemm_f8_any(GemmParams p) {
   constexpr auto load_chunk = SHORT ? load16_short : load16;
   __shared__ __align__(16) uint8_t sm[2][2][64 * 128];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), kh = lane >> 5;
-  const int64_t nm = (p.M + 63) / 64;
-  const int64_t m0 = blockIdx.x % nm * 64, n0 = blockIdx.x / nm * 64;
+  int64_t m0, n0;
+  if (!tile_of(p, 64, 64, m0, n0)) return;
   const int wm = wave & 1, wn = wave >> 1;
   const int64_t m = m0 + wm * 32 + (lane & 31), mc = min(m, p.M - 1);
   const float* sw = p.sw + n0 / 128 * p.kb;
@@ -460,7 +460,7 @@ __global__ __launch_bounds__(256) void k_gemm_f8_any(GemmParams p) {
       *reinterpret_cast<uint4*>(&sm[st][1][row * 128 + c * 16]) = vw[i];
     }
   };
-  v16f acc = v16f{};
+  v16f acc[1][1] = {{v16f{}}};
   if (p.kb > 0) {
     load(0);
     store(0);
@@ -474,15 +474,11 @@ __global__ __launch_bounds__(256) void k_gemm_f8_any(GemmParams p) {
     for (int ks = 0; ks < 2; ++ks)
       part = product<EXACT>(fragment(sm[b & 1][1], wn * 32 + (lane & 31), ks, kh), fragment(sm[b & 1][0], wm * 32 + (lane & 31), ks, kh), part);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = fmaf(part[i], s, acc[i]);
+    for (int i = 0; i < 16; ++i) acc[0][0][i] = fmaf(part[i], s, acc[0][0][i]);
     if (b + 1 < p.kb) store((b + 1) & 1);
   }
-  if (m >= p.M) return;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int64_t n = n0 + wn * 32 + 8 * (i / 4) + 4 * kh + i % 4;
-    if (n < p.N) put(p, m, n, acc[i] + (p.bias ? p.bias[n] : 0.0f));
-  }
+  __syncthreads();  // the stages become the waves' output buffers
+  epilogue<1, 1, false, Out<EXACT>>(p, &sm[0][0][0], acc, m0 + wm * 32, n0 + wn * 32, wave, lane);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -575,7 +571,8 @@ void launch(const GemmParams& p, hipStream_t stream) {
   }
   // direct loads to LDS take multiples of 4 bytes, and whole blocks
   if (((uintptr_t)p.a | (uintptr_t)p.w | (uintptr_t)p.as | (uintptr_t)p.ws) % 4 != 0 || p.K < 128) {
-    const unsigned grid = (unsigned)(cdiv(p.M, 64) * cdiv(p.N, 64));
+    // (128x128 tiles that load alike leave one wave to a SIMD: 4096 x 4095 x 4097 349 us, 265 in these)
+    const unsigned grid = grid_of(p, 64, 64);
     if (p.K < 16) k_gemm_f8_any<EXACT, true><<<grid, 256, 0, stream>>>(p);
     else k_gemm_f8_any<EXACT, false><<<grid, 256, 0, stream>>>(p);
     return;
@@ -615,7 +612,7 @@ extern "C" qssm_status qssm_gemm_f8(const qssm_gemm_f8_args* a, hipStream_t stre
   if (((uintptr_t)a->w_scales | (uintptr_t)a->bias) % 4 != 0)
     return fail(QSSM_ERR_INVALID_ARG, "w_scales or bias is not aligned to its type");
   // a grid holds fewer than 2^32 threads
-  if (cdiv(M, 64) * cdiv(N, 64) >= (1 << 24)) return fail(QSSM_ERR_UNSUPPORTED, "M * N too large");
+  if (cdiv(M, 64) * cdiv(N, 64) >= (1 << 24) - 8) return fail(QSSM_ERR_UNSUPPORTED, "M * N too large");
   const Span y{a->y, M, a->y_stride * sy, N * sy};
   if (overlap(y, Span{a->a, M, a->a_stride, K}) || overlap(y, Span{a->w, N, a->w_stride, K}) || overlap(y, flat(a->bias, N * 4)) ||
       overlap(y, Span{a->a_scales, kb, a->a_scales_stride * 4, M * 4}) || overlap(y, flat(a->w_scales, cdiv(N, 128) * kb * 4)))
