@@ -848,11 +848,17 @@ def qssm_quant_f8(x, codes, scales, stream=None):
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
     M, K = x.shape
-    px, xs = _rows(x, None, "x", (M, K))
-    pc, cs = _rows(codes, torch.float8_e4m3fn, "codes", (M, K))
-    ps, ss = _rows(scales, torch.float32, "scales", (-(-K // 128), M))
-    _call("qssm_quant_f8", _device_of(x, codes, scales), stream, px, _float_type(x, "x"), M, K, xs, pc, cs, ps,
-          max(ss, M), keep=(x, codes, scales))
+    # (no argument block keeps these checks from one call to the next: the usual case takes few steps)
+    xs, cs, ss = x.stride(), codes.stride(), scales.stride()
+    if not (x.is_cuda and codes.is_cuda and scales.is_cuda and codes.dtype is torch.float8_e4m3fn and
+            scales.dtype is torch.float32 and codes.shape == x.shape and scales.shape == (-(-K // 128), M) and
+            xs[1] == 1 and cs[1] == 1 and ss[1] == 1 and xs[0] >= K and cs[0] >= K and ss[0] >= M):
+        # one element or row, an empty tensor, or what these refuse
+        xs = (_rows(x, None, "x", (M, K))[1],)
+        cs = (_rows(codes, torch.float8_e4m3fn, "codes", (M, K))[1],)
+        ss = (max(_rows(scales, torch.float32, "scales", (-(-K // 128), M))[1], M),)
+    _call("qssm_quant_f8", _device_of(x, codes, scales), stream, x.data_ptr(), _float_type(x, "x"), M, K, xs[0],
+          codes.data_ptr(), cs[0], scales.data_ptr(), ss[0], keep=(x, codes, scales))
     return codes, scales
 
 

@@ -63,68 +63,39 @@ __device__ __forceinline__ float as_float(T v) {
   else return __uint_as_float(v);
 }
 
-// e^-|v| and 1 / (1 + e^-|v|): no overflow on either side.
+// v / (1 + e^-v). Where e^-v overflows (v < -88) the simple form gives -0 for a value of at most 5.3e-37, which fp16 and
+// int8 outputs round to 0 as well (the least valid scale is 2^-100); the other form keeps it, by e^-|v| <= 1.
+template <bool SIMPLE>
 __device__ __forceinline__ float silu_fast(float v) {
+  if (SIMPLE) return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f));
   const float e = __builtin_amdgcn_exp2f(-fabsf(v) * 1.44269504f);
   const float r = __builtin_amdgcn_rcpf(1.0f + e);
   return v * (v < 0.0f ? e * r : r);
 }
 
-__device__ __noinline__ float exact_value(const float* w, const float* x, int W, float bias, int silu) {
-  double v = bias;
-  for (int k = 0; k < W; ++k) v = fma((double)w[k], (double)x[k], v);
-  if (silu) v = v / (1.0 + exp(-v));
-  return (float)v;
+// x, and the compiler does not know that: no fp64 copies of the weights are kept in registers for the rare path.
+__device__ __forceinline__ float opaque(float x) {
+  asm volatile("" : "+v"(x));
+  return x;
 }
 
-// One output row of VEC channels from the W input rows in x (the oldest first).
-// int8 codes are those of the value in fp64, rounded once to fp32. The fp32 value decides where it is sure to
-// give the same: its sum is off by at most W 2^-24 (|bias| + sum |w x|), which silu passes on by at most
-// 1.1 times, and its silu by (8 + |v|) 2^-23 of itself (exponential, reciprocal and two roundings of 2^-23 or
-// less, and the exponent's rounding, |v| 2^-24); a code is sure where v / s is further than that from the nearest half-integer.
-// Lanes where it is not (~1 in 2000 for ordinary inputs) take the fp64 path.
-template <int VEC, int W, typename Y>
-__device__ __forceinline__ void put_row(const ConvParams& p, const float (&w)[VEC][W], const float (&bias)[VEC],
-                                        const float (&x)[W][VEC], const float (&sc)[VEC], const float (&rc)[VEC],
-                                        Y* out) {
-  Raw<VEC, Y> o;
-#pragma unroll
-  for (int c = 0; c < VEC; ++c) {
-    float v = bias[c];
-#pragma unroll
-    for (int k = 0; k < W; ++k) v = fmaf(w[c][k], x[k][c], v);
-    float y = p.silu ? silu_fast(v) : v;
-    if constexpr (std::is_same_v<Y, int8_t>) {
-      float s = fabsf(bias[c]);
-#pragma unroll
-      for (int k = 0; k < W; ++k) s = fmaf(fabsf(w[c][k]), fabsf(x[k][c]), s);
-      const float off = fmaf(s, 1.11f * (W + 1) * 0x1p-24f, fabsf(y) * ((8.0f + fabsf(v)) * 0x1p-23f));
-      const float f = __builtin_amdgcn_fmed3f(y * rc[c], -256.0f, 256.0f);
-      const float t = rintf(f);
-      // (not less: a NaN is not sure either)
-      const bool sure = fabsf(f - t) + off * rc[c] * 1.01f < 0.4999f;
-      int q = (int)__builtin_amdgcn_fmed3f(t, -128.0f, 127.0f);
-      if (!sure) {
-        float wk[W], xk[W];
-#pragma unroll
-        for (int k = 0; k < W; ++k) wk[k] = w[c][k], xk[k] = x[k][c];
-        q = quant8(exact_value(wk, xk, W, bias[c], p.silu), sc[c]);
-      }
-      o.v[c] = (int8_t)(rc[c] != 0.0f ? q : 0);
-    } else if constexpr (std::is_same_v<Y, uint16_t>) {
-      o.v[c] = __half_as_ushort(__float2half_rn(y));
-    } else {
-      o.v[c] = __float_as_uint(y);
-    }
-  }
-  store_raw<VEC>(out, o);
+// The larger of two |x| as they lie in memory, by their bits (a NaN is the largest), two of fp16 at a time.
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a & 0x7fffffffu, b & 0x7fffffffu); }
+typedef unsigned short v2u __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ v2u larger(v2u a, v2u b) {
+  const v2u m = {0x7fff, 0x7fff};
+  return __builtin_elementwise_max((v2u)(a & m), (v2u)(b & m));
 }
 
 template <int VEC, int W, typename X, typename Y>
 struct Lane {
+  static constexpr bool kI8 = std::is_same_v<Y, int8_t>;
   const ConvParams& p;
   int c;  // the lane's first channel
-  float w[VEC][W], bias[VEC], sc[VEC], rc[VEC];
+  float w[VEC][W], bias[VEC];
+  // int8: the reciprocal of the scale (0: no valid one), and what a code's distance from the nearest half-integer loses
+  // for each unit of |x|, and without any
+  float rc[VEC], loss[VEC], room[VEC];
   const X* x;
   Y* y;
 
@@ -133,21 +104,103 @@ struct Lane {
     y = reinterpret_cast<Y*>(p.y) + c;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
+      float sum = 0.0f;
 #pragma unroll
-      for (int k = 0; k < W; ++k) w[i][k] = p.w[(int64_t)(c + i) * W + k];
+      for (int k = 0; k < W; ++k) {
+        w[i][k] = p.w[(int64_t)(c + i) * W + k];
+        sum += fabsf(w[i][k]);
+      }
       bias[i] = p.bias ? p.bias[c + i] : 0.0f;
-      sc[i] = rc[i] = 0.0f;
-      if constexpr (std::is_same_v<Y, int8_t>) {
-        sc[i] = p.scales[min((int)p.group_of[c + i], p.groups - 1)];
-        rc[i] = recip_or_zero(sc[i]);
+      if constexpr (kI8) {
+        rc[i] = recip_or_zero(scale(i));
+        constexpr float kSum = 1.13f * (W + 1) * 0x1p-24f;
+        loss[i] = -kSum * sum * rc[i];
+        room[i] = 0.4999f - kSum * fabsf(bias[i]) * rc[i];
       }
     }
   }
 
+  __device__ __forceinline__ float scale(int i) const { return p.scales[min((int)p.group_of[c + i], p.groups - 1)]; }
+  __device__ __forceinline__ bool has(int i) const { return !p.seq.has || p.seq.has[i] != 0; }
   __device__ __forceinline__ Raw<VEC, X> row(int64_t t) const { return load_raw<VEC>(x + t * p.xs); }
 
+  // The largest |x| of each channel over `rows` rows.
+  template <int N>
+  __device__ __forceinline__ void largest(const Raw<VEC, X> (&r)[N], float (&m)[VEC]) const {
+    if constexpr (std::is_same_v<X, uint16_t> && VEC % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < VEC; i += 2) {
+        v2u a = {0, 0};
+#pragma unroll
+        for (int k = 0; k < N; ++k) a = larger(a, v2u{r[k].v[i], r[k].v[i + 1]});
+        m[i] = as_float((X)a[0]);
+        m[i + 1] = as_float((X)a[1]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        uint32_t a = 0;
+#pragma unroll
+        for (int k = 0; k < N; ++k) a = max(a, std::is_same_v<X, uint16_t> ? r[k].v[i] & 0x7fffu : r[k].v[i] & 0x7fffffffu);
+        m[i] = as_float((X)a);
+      }
+    }
+  }
+
+  // Output row t of the W input rows from r[0] on (the oldest first); limit: room less the loss at the largest |x|.
+  //
+  // int8 codes are those of the value in fp64, rounded once to fp32. The fp32 value decides where it is sure to give the
+  // same: its sum is off by at most W 2^-24 (|bias| + sum |w x|), which silu passes on by at most 1.1 times, and the value
+  // by (6 + |v|) 2^-23 of itself (the exponent's rounding |v| 2^-23, exponential and reciprocal 2^-23 each, four
+  // roundings of 2^-24, the definition's rounding and the quotient's). A code is sure where the quotient is nearer
+  // than 1/2 less these to a whole number. Lanes where it is not (1 in ~4000 for ordinary inputs) take the fp64 path.
+  __device__ __forceinline__ void put(int64_t t, const Raw<VEC, X>* r, const float (&limit)[VEC]) const {
+    constexpr bool kSimple = kI8 || std::is_same_v<Y, uint16_t>;
+    constexpr float kMagic = 12582912.0f;  // 1.5 2^23: the sum with it holds the rounded value in its low bits
+    Raw<VEC, Y> o;
+    bool sure[VEC], all = true;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      float v = bias[i];
+#pragma unroll
+      for (int k = 0; k < W; ++k) v = fmaf(w[i][k], as_float(r[k].v[i]), v);
+      const float z = p.silu ? silu_fast<kSimple>(v) : v;
+      if constexpr (kI8) {
+        const float f = z * rc[i], fc = __builtin_amdgcn_fmed3f(f, -128.0f, 127.0f);
+        const float m = fc + kMagic, d = fc - (m - kMagic);
+        // (not less: a NaN is not sure either)
+        sure[i] = fabsf(d) < fmaf(-fabsf(f), fmaf(fabsf(v), 0x1p-23f, 6.0f * 0x1p-23f), limit[i]);
+        all &= sure[i];
+        o.v[i] = (int8_t)__float_as_uint(m);
+      } else if constexpr (std::is_same_v<Y, uint16_t>) {
+        o.v[i] = __half_as_ushort(__float2half_rn(z));
+      } else {
+        o.v[i] = __float_as_uint(z);
+      }
+    }
+    if constexpr (kI8) {
+      if (!all) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          if (sure[i]) continue;
+          double v = opaque(bias[i]);
+#pragma unroll
+          for (int k = 0; k < W; ++k) v = fma((double)opaque(w[i][k]), (double)as_float(r[k].v[i]), v);
+          if (p.silu) v = v / (1.0 + exp(-v));
+          o.v[i] = quant8((float)v, scale(i));
+        }
+      }
+    }
+    store_raw<VEC>(y + t * p.ys, o);
+  }
+
+  __device__ __forceinline__ void limits(const float (&m)[VEC], float (&limit)[VEC]) const {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) limit[i] = fmaf(loss[i], m[i], room[i]);
+  }
+
   // A sequence's initial rows, the oldest first.
-  __device__ __forceinline__ void initial(int64_t slot, bool has, Raw<VEC, X> (&r)[W - 1]) const {
+  __device__ __forceinline__ void initial(int64_t slot, bool has, Raw<VEC, X>* r) const {
     const bool given = p.state && slot >= 0 && has;
     const X* at = reinterpret_cast<const X*>(p.state) + slot * (W - 1) * p.C + c;
 #pragma unroll
@@ -155,7 +208,7 @@ struct Lane {
   }
 
   // The state behind a sequence of `len` rows from `begin` on: its last W - 1 rows, the initial ones before its first.
-  __device__ __forceinline__ void final(int64_t slot, int64_t begin, int len, const Raw<VEC, X> (&init)[W - 1]) const {
+  __device__ __forceinline__ void final(int64_t slot, int64_t begin, int len, const Raw<VEC, X>* init) const {
     if (!p.state_out || slot < 0) return;
     X* at = reinterpret_cast<X*>(p.state_out) + slot * (W - 1) * p.C + c;
     Raw<VEC, X> r[W - 1];
@@ -174,14 +227,12 @@ struct Lane {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) store_raw<VEC>(at + (int64_t)j * p.C, r[j]);
   }
-
-  __device__ __forceinline__ bool has(int i) const { return !p.seq.has || p.seq.has[i] != 0; }
 };
 
-constexpr int kAhead = 4;  // rows loaded ahead
 
 template <int VEC, int W, typename X, typename Y>
 __global__ __launch_bounds__(256) void k_causal_conv(ConvParams p) {
+  constexpr int kAhead = VEC == 2 ? 8 : 4;  // rows loaded ahead
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int cb = blockIdx.x % p.cblocks;
   const int64_t strip = (int64_t)(blockIdx.x / p.cblocks) * 4 + wave;
@@ -213,32 +264,23 @@ __global__ __launch_bounds__(256) void k_causal_conv(ConvParams p) {
   int begin = uniform(seq_begin(sq, s)), end = uniform(seq_end(sq, s, begin));
   if (begin < t0 && t0 - begin < W - 1) t = min(begin + W - 1, end);
   if (c >= p.C) return;
-  const Lane<VEC, W, X, Y> ln(p, c);
-  float hist[W - 1][VEC];
-  const auto keep = [&](const Raw<VEC, X> (&r)[W - 1]) {
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) hist[j][i] = as_float(r[j].v[i]);
-  };
+  using L = Lane<VEC, W, X, Y>;
+  const L ln(p, c);
+  // the rows before t, then kAhead rows from t on
+  Raw<VEC, X> win[W - 1 + kAhead], next[kAhead];
   // sequence s begins at row t
-  const auto enter = [&]() {
-    Raw<VEC, X> init[W - 1];
+  const auto enter = [&](Raw<VEC, X>* before) {
     const int64_t slot = seq_slot(sq, s);
-    ln.initial(slot, ln.has(s), init);
-    ln.final(slot, begin, end - begin, init);
-    keep(init);
+    ln.initial(slot, ln.has(s), before);
+    ln.final(slot, begin, end - begin, before);
     te = max(te, (int)min((int64_t)begin + W - 1, (int64_t)end));
   };
   if (t == begin) {
-    enter();
-  } else if (t < end) {
-    Raw<VEC, X> before[W - 1];
+    enter(win);
+  } else {
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) before[j] = ln.row(t - (W - 1) + j);
-    keep(before);
+    for (int j = 0; j < W - 1; ++j) win[j] = t < end ? ln.row(t - (W - 1) + j) : Raw<VEC, X>{};
   }
-  Raw<VEC, X> next[kAhead];
   const auto load = [&](int64_t from) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
@@ -246,30 +288,42 @@ __global__ __launch_bounds__(256) void k_causal_conv(ConvParams p) {
   };
   load(t);
   while (t < te) {
-    Raw<VEC, X> now[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) now[u] = next[u];
+    for (int u = 0; u < kAhead; ++u) win[W - 1 + u] = next[u];
     const bool ahead = t + kAhead < te;
     if (ahead) load((int64_t)t + kAhead);
+    float limit[VEC], m[VEC];
+    const bool whole = t + kAhead <= min(te, end);
+    if (whole) {
+      if constexpr (L::kI8) {
+        ln.largest(win, m);
+        ln.limits(m, limit);
+      }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (t + u < te) {
+      for (int u = 0; u < kAhead; ++u) ln.put((int64_t)t + u, win + u, limit);
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) win[j] = win[kAhead + j];
+    } else {
+      // rows of more than one sequence, or the strip's last
+#pragma unroll 1
+      for (int u = 0; u < kAhead && t + u < te; ++u) {
         while (t + u >= end && s + 1 < sq.nseq) {  // the next sequence, past those without rows
           ++s;
           begin = end;
           end = uniform(max(seq_end(sq, s, seq_begin(sq, s)), begin));
-          if (t + u < end) enter();
+          if (t + u < end) enter(win);
         }
-        float v[W][VEC];
+        Raw<VEC, X> r[W];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-#pragma unroll
-          for (int k = 0; k < W - 1; ++k) v[k][i] = hist[k][i];
-          v[W - 1][i] = as_float(now[u].v[i]);
-#pragma unroll
-          for (int k = 0; k < W - 1; ++k) hist[k][i] = v[k + 1][i];
+        for (int j = 0; j < W - 1; ++j) r[j] = win[j];
+        r[W - 1] = ln.row(t + u);
+        if constexpr (L::kI8) {
+          ln.largest(r, m);
+          ln.limits(m, limit);
         }
-        put_row<VEC, W>(p, ln.w, ln.bias, v, ln.sc, ln.rc, ln.y + (int64_t)(t + u) * p.ys);
+        ln.put((int64_t)t + u, r, limit);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) win[j] = r[j + 1];
       }
     }
     if (!ahead && t + kAhead < te) load((int64_t)t + kAhead);  // a sequence that began here goes on past the strip
@@ -284,24 +338,22 @@ __global__ __launch_bounds__(256) void k_causal_conv_step(ConvParams p) {
   const int per = p.C / VEC;
   const int i = (int)(id / per);
   if (i >= p.seq.nseq) return;
-  const Lane<VEC, W, X, Y> ln(p, (int)(id % per) * VEC);
-  Raw<VEC, X> init[W - 1];
+  using L = Lane<VEC, W, X, Y>;
+  const L ln(p, (int)(id % per) * VEC);
+  Raw<VEC, X> r[W];
   const int64_t slot = seq_slot(p.seq, i);
-  ln.initial(slot, ln.has(i), init);
-  const Raw<VEC, X> x = ln.row(i);
-  float v[W][VEC];
-#pragma unroll
-  for (int c = 0; c < VEC; ++c) {
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) v[k][c] = as_float(init[k].v[c]);
-    v[W - 1][c] = as_float(x.v[c]);
+  ln.initial(slot, ln.has(i), r);
+  r[W - 1] = ln.row(i);
+  float limit[VEC], m[VEC];
+  if constexpr (L::kI8) {
+    ln.largest(r, m);
+    ln.limits(m, limit);
   }
-  put_row<VEC, W>(p, ln.w, ln.bias, v, ln.sc, ln.rc, ln.y + (int64_t)i * p.ys);
+  ln.put(i, r, limit);
   if (p.state_out && slot >= 0) {
     X* at = reinterpret_cast<X*>(p.state_out) + slot * (W - 1) * p.C + ln.c;
 #pragma unroll
-    for (int k = 0; k < W - 2; ++k) store_raw<VEC>(at + (int64_t)k * p.C, init[k + 1]);
-    store_raw<VEC>(at + (int64_t)(W - 2) * p.C, x);
+    for (int k = 0; k < W - 1; ++k) store_raw<VEC>(at + (int64_t)k * p.C, r[k + 1]);
   }
 }
 
@@ -331,7 +383,7 @@ qssm_status launch(ConvParams p, bool step, hipStream_t stream) {
 
 template <int W, typename X, typename Y>
 qssm_status launch_vec(const ConvParams& p, bool step, hipStream_t stream) {
-  return p.C % 8 == 0 ? launch<8, W, X, Y>(p, step, stream) : launch<1, W, X, Y>(p, step, stream);
+  return p.C % 2 == 0 ? launch<2, W, X, Y>(p, step, stream) : launch<1, W, X, Y>(p, step, stream);
 }
 
 template <int W, typename X>

@@ -33,6 +33,14 @@ __device__ __forceinline__ float as_float(T v) {
   else return __uint_as_float(v);
 }
 
+typedef unsigned short v2u __attribute__((ext_vector_type(2)));
+
+// x of the lane that differs in one bit of its number, as dpp_partner.
+template <int STEP>
+__device__ __forceinline__ uint32_t partner(uint32_t x) {
+  return __float_as_uint(dpp_partner<STEP>(__uint_as_float(x)));
+}
+
 __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
   const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true);
@@ -82,33 +90,44 @@ __global__ __launch_bounds__(256) void k_quant_f8(QuantParams p) {
   for (int r = 0; r < kRowsPer; ++r) {
     const int64_t m = m0 + r;
     if (m >= p.M) return;
-    float v[8], a = 0.0f;
+    // the largest |x| by its bits: a NaN or an infinity is larger than every number
+    uint32_t most = 0;
+    if constexpr (std::is_same_v<T, uint16_t>) {
+      v2u pair = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = as_float(raw[r][i]);
-      a = fmaxf(a, finite_abs(v[i]));
+      for (int i = 0; i < 8; i += 2) pair = __builtin_elementwise_max(pair, (v2u)(v2u{raw[r][i], raw[r][i + 1]} & v2u{0x7fff, 0x7fff}));
+      most = max(pair[0], pair[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) most = max(most, raw[r][i] & 0x7fffffffu);
     }
-    a = fmaxf(a, dpp_partner<1>(a));
-    a = fmaxf(a, dpp_partner<2>(a));
-    a = fmaxf(a, dpp_partner<4>(a));
-    a = fmaxf(a, dpp_partner<8>(a));
+    most = max(most, partner<1>(most));
+    most = max(most, partner<2>(most));
+    most = max(most, partner<4>(most));
+    most = max(most, partner<8>(most));
+    const bool special = most >= (std::is_same_v<T, uint16_t> ? 0x7c00u : 0x7f800000u);  // one of the block is no number
+    float v[8], a = as_float((T)most);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = as_float(raw[r][i]);
+    if (special) {
+      a = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a = fmaxf(a, finite_abs(v[i]));
+      a = fmaxf(a, dpp_partner<1>(a));
+      a = fmaxf(a, dpp_partner<2>(a));
+      a = fmaxf(a, dpp_partner<4>(a));
+      a = fmaxf(a, dpp_partner<8>(a));
+    }
     const float s = a == 0.0f ? 1.0f : fminf(fmaxf(a * (1.0f / 448.0f), 0x1p-60f), 0x1p60f);
     if (col >= p.K) continue;
     if ((lane & 15) == 0) p.scales[block * p.ss + m] = s;
-    // f is within 2^-23 (1 + 2^-24) of the quotient, relative: where the codes of f (1 -+ 2^-22) are one, it is the quotient's
-    const float rc = 1.0f / s;
-    float f[8], lo[8], hi[8];
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      f[i] = __builtin_amdgcn_fmed3f(v[i] * rc, -448.0f, 448.0f);
-      lo[i] = f[i] * (1.0f - 0x1p-22f);
-      hi[i] = __builtin_amdgcn_fmed3f(f[i] * (1.0f + 0x1p-22f), -448.0f, 448.0f);
-      bad |= v[i] != v[i];
-    }
-    uint32_t w[2] = {pack4(lo[0], lo[1], lo[2], lo[3]), pack4(lo[4], lo[5], lo[6], lo[7])};
-    bad |= w[0] != pack4(hi[0], hi[1], hi[2], hi[3]) || w[1] != pack4(hi[4], hi[5], hi[6], hi[7]);
-    if (bad) {
+    // v lo and v hi lie around the quotient (lo and hi are within 2^-23 of 1 / s (1 -+ 2^-21), the products round by 2^-24): where
+    // their codes are one, it is the quotient's. Both stay below 464, where e4m3 has no more number.
+    const float rc = 1.0f / s, lo = rc * (1.0f - 0x1p-21f), hi = rc * (1.0f + 0x1p-21f);
+    uint32_t w[2] = {pack4(v[0] * lo, v[1] * lo, v[2] * lo, v[3] * lo), pack4(v[4] * lo, v[5] * lo, v[6] * lo, v[7] * lo)};
+    const bool two = w[0] != pack4(v[0] * hi, v[1] * hi, v[2] * hi, v[3] * hi) || w[1] != pack4(v[4] * hi, v[5] * hi, v[6] * hi, v[7] * hi);
+    // (the largest scale: what is far beyond 448 of it goes there too)
+    if (two || special || a > 450.0f * s) {
       w[0] = w[1] = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i / 4] |= exact_code(v[i], s, v[i] * rc) << (8 * (i % 4));
