@@ -20,7 +20,8 @@ from . import (QSSM_F16, QSSM_F32, QSSM_I8, QSSM_I16, QSSM_X_INT8, QSSM_X_SOFTED
                qssm_ssd_workspace_size, qssm_state_update, s4d_args, scan_args, ssd_args,
                update_args, gemm_args, qssm_gemm_w4a8, qssm_quant_w4, qssm_quant_w8, rmsnorm_args,
                qssm_rmsnorm_i8, gemm_w8a8_args, qssm_gemm_w8a8, qssm_state_quant, qssm_state_dequant,
-               qssm_state_update_i8)
+               qssm_state_update_i8, causal_conv_args, gemm_f8_args, qssm_causal_conv, qssm_gemm_f8, qssm_quant_f8,
+               qssm_quant_f8_weight, qssm_selective_scan, qssm_selective_scan_workspace_size, selective_scan_args)
 
 
 def _dev(a, device, dtype=None):
@@ -573,3 +574,76 @@ class W8A8DecodeBlock:
         self.core.step()
         qssm_rmsnorm_i8(self.gated)
         return self.out.step()
+
+
+# ------------------------------------------------------------------------------------------------
+# Mamba1 block with block-scaled 8-bit floating point projections
+
+class F8Linear:
+    """y = x W^T (+ bias) in e4m3: the weights [N, K] quantized offline in 128 x 128 blocks, up to `rows` rows of
+    activations quantized at every call, 128 columns under a scale."""
+
+    def __init__(self, w, rows, device, bias=None):
+        """w: host fp32 [N, K]."""
+        import torch
+        self.w_scales_host, self.w_host = qssm_quant_f8_weight(w)
+        self.w = _dev(self.w_host, device).view(torch.float8_e4m3fn)
+        self.ws = _dev(self.w_scales_host, device)
+        self.bias = None if bias is None else _dev(np.asarray(bias, np.float32), device)
+        K = w.shape[1]
+        self.codes = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=device)
+        self.scales = torch.empty((-(-K // 128), rows), dtype=torch.float32, device=device)
+
+    def step(self, x, y):
+        M = x.shape[0]
+        codes, scales = self.codes[:M], self.scales[:, :M]
+        qssm_quant_f8(x, codes, scales)
+        qssm_gemm_f8(gemm_f8_args(codes, scales, self.w, self.ws, y, bias=self.bias))
+        return y
+
+
+class F8MambaBlock:
+    """Mamba1 block on packed sequences, prompts and single tokens alike, its projections in block-scaled e4m3: the
+    in-projection into x and the gate z, the causal convolution, the projections into dt's low rank, B and C and
+    from there into dt, the selective scan with the gate, and the out-projection. Both states live in caches of `slots`
+    slots. Activations between the operators are fp16.
+
+    params: host fp32 w_in [2 D, d], conv_w [D, W], conv_b [D], w_x [R + 2 N, D], w_dt [D, R], dt_b [D], A [D, N],
+    Dskip [D], w_out [d, D]. tokens: the most rows of a step."""
+
+    def __init__(self, params, slots, tokens, device):
+        import torch
+        self.D, self.W = params["conv_w"].shape
+        self.N, self.R = params["A"].shape[1], params["w_dt"].shape[1]
+        d = params["w_in"].shape[1]
+        e = lambda *shape, dtype=torch.float16: torch.zeros(shape, dtype=dtype, device=device)  # noqa: E731
+        self.proj_in, self.proj_x, self.proj_dt, self.proj_out = (
+            F8Linear(params[k], tokens, device) for k in ("w_in", "w_x", "w_dt", "w_out"))
+        self.conv_w, self.conv_b, self.dt_b, self.A, self.Dskip = (
+            _dev(params[k], device) for k in ("conv_w", "conv_b", "dt_b", "A", "Dskip"))
+        self.xz, self.x, self.dbc = e(tokens, 2 * self.D), e(tokens, self.D), e(tokens, self.R + 2 * self.N)
+        self.dt, self.y, self.out = e(tokens, self.D), e(tokens, self.D), e(tokens, d)
+        self.conv_state = e(slots, self.W - 1, self.D)
+        self.ssm_state = e(slots, self.D, self.N, dtype=torch.float32)
+        self.workspace = None
+
+    def step(self, hidden, state_slots, seq_offsets=None, has_state=None):
+        """hidden [T, d] float16: the sequences of seq_offsets, or without them one token of each. state_slots int32
+        and has_state uint8 [nseq] as in causal_conv_args. Returns the block's output [T, d]."""
+        import torch
+        T, D, N, R = hidden.shape[0], self.D, self.N, self.R
+        xz, x, dbc, dt, y, out = (t[:T] for t in (self.xz, self.x, self.dbc, self.dt, self.y, self.out))
+        seqs = dict(nseq=T) if seq_offsets is None else dict(seq_offsets=seq_offsets)
+        seqs.update(state_slots=state_slots, has_state=has_state)
+        self.proj_in.step(hidden, xz)
+        qssm_causal_conv(causal_conv_args(xz[:, :D], self.conv_w, x, bias=self.conv_b, state=self.conv_state,
+                                          state_out=self.conv_state, **seqs))
+        self.proj_x.step(x, dbc)
+        self.proj_dt.step(dbc[:, :R], dt)
+        args = selective_scan_args(x, dt, self.A, dbc[:, R:R + N], dbc[:, R + N:], y, D=self.Dskip, z=xz[:, D:],
+                                   delta_bias=self.dt_b, state=self.ssm_state, state_out=self.ssm_state, **seqs)
+        need = qssm_selective_scan_workspace_size(args)
+        if need > (0 if self.workspace is None else self.workspace.numel()):
+            self.workspace = torch.empty(need, dtype=torch.uint8, device=hidden.device)
+        qssm_selective_scan(args, self.workspace)
+        return self.proj_out.step(y, out)
