@@ -7,16 +7,21 @@
 // workgroup 64 channels of one B/C group. The rows run in batches of four: each lane of a channel loads
 // and prepares one row (dt, dt x, and later the gate), the four rows' values are passed around by lane
 // permutations, and the four lanes' sums are joined by a transposed reduction that leaves each lane the
-// sum of its own row. B and C of 32 rows at a time go through LDS as fp32 while the rows before are computed, and
-// the next 32 rows of x, delta and z are in registers by then.
+// sum of its own row. B and C of 32 rows at a time go through LDS in their own type while the rows before are computed
+// (fp16 ones are multiplied as they are, by mixed fused multiply-adds), and the next 32 rows of x, delta and z are in
+// registers by then.
 //
-// Bound by vector instructions: an update takes two products, an exponential (a quarter of the rate), and two fused
-// multiply-adds, 8 issue slots, of T D N updates.
+// Bound by vector instructions: an update takes two products, an exponential (half the rate) and two fused
+// multiply-adds, 6 issue slots, of T D N updates. The vector units are 92 % busy with y and 89 % without it. A batch of
+// four rows takes 135 instructions for a lane's 16 updates (N 16), 80 of them the updates'. 16 x 1024 rows, 4096
+// channels, whole: 298 us; the same rows as 24 sequences of very different lengths: 192 us for the pieces' ends and
+// 270 with y (175 for the updates' slots alone); 256 single rows: 35 us, 4.1 TB/s.
 //
 // Few sequences with few channels do not fill the chip, so long sequences are cut into pieces (piece_rows()).
 // First the pieces but the last run without y, the first from the initial state, the others from zero; then all run in
 // full from the state that they fold from the ends before them:
 //     h_in[c + 1] = e^(A sum dt over c) h_in[c] + end[c].
+// In a packed batch the first pieces, whose state is known, run in full at once (runs_first()).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -34,6 +39,7 @@ struct SscanParams {
   Seqs seq;
   int32_t D, N, G, Dg, per_group;  // Dg = D / G channels in per_group workgroups
   int32_t piece;                   // rows of a piece
+  int32_t first;                   // whether the first of several pieces runs in full with the others' ends
   int32_t softplus, yf16, sf16;
   const void *x, *delta, *B, *C, *z;
   int64_t xs, ds, bs, cs, zs, ys;
@@ -317,12 +323,11 @@ struct Piece {
   }
 };
 
-// Y void: the ends of the pieces that have one behind them, the first ones' from the initial state, the others' from
-// zero; else every piece with y, from the state that it folds from the ends.
-template <int NPL, typename T, typename Y>
+// ENDS: the ends of the pieces that have one behind them, the first ones' from the initial state (with their y unless
+// Y is void), the others' from zero. Else every other piece with y, from the state that it folds from the ends.
+template <int NPL, typename T, typename Y, bool ENDS>
 __global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
   constexpr int kNP = 4 * NPL;
-  constexpr bool kY = !std::is_same_v<Y, void>;
   __shared__ __align__(16) T lds[2 * kRows * 2 * kNP];
   const int blocks = p.G * p.per_group, cb = blockIdx.x % blocks;
   const int64_t at = blockIdx.x / blocks;  // piece slot: sequence i has begin(i) / piece + i and the ones behind it
@@ -334,7 +339,7 @@ __global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
   const int chunk = (int)(at - (begin / p.piece + i)), pieces = max((int)(((uint32_t)(end - begin) + p.piece - 1) / (uint32_t)p.piece), 1);
   if (chunk < 0 || chunk >= pieces) return;
   const bool last = chunk == pieces - 1;
-  if (!kY && last) return;
+  if (ENDS ? last : p.first && chunk == 0 && !last) return;
   const int g = cb / p.per_group, q = threadIdx.x & 3;
   const int dg = cb % p.per_group * 64 + (threadIdx.x >> 2);
   const int d = g * p.Dg + min(dg, p.Dg - 1);
@@ -346,17 +351,17 @@ __global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
   float* ends = p.carry + at * size + (int64_t)d * kNP + q * NPL;
 #pragma unroll
   for (int j = 0; j < NPL; ++j) h[j] = 0.0f;
-  if (chunk == 0 && (last || !kY)) {
+  if (chunk == 0 && (last || ENDS)) {
     load_state(p, slot, !sq.has || sq.has[i] != 0, d, q, h);
     // the last piece's slot has no ends: it keeps the initial state, which the last piece may overwrite in `state`
-    if (!kY && live) {
+    if (std::is_same_v<Y, void> && live) {
 #pragma unroll
       for (int j = 0; j < NPL; ++j) ends[(pieces - 1) * size + j] = h[j];
     }
-  } else if (kY && chunk == 0) {
+  } else if (!ENDS && chunk == 0) {
 #pragma unroll
     for (int j = 0; j < NPL; ++j) h[j] = ends[(pieces - 1) * size + j];
-  } else if (kY) {
+  } else if (!ENDS) {
     const float* from = ends - chunk * size;
     const float* sums = p.carry + (at - chunk) * size + (int64_t)p.D * kNP + d;
 #pragma unroll
@@ -368,18 +373,17 @@ __global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
       for (int j = 0; j < NPL; ++j) h[j] = fmaf(__builtin_amdgcn_exp2f(s * a[j]), h[j], from[c * size + j]);
     }
   }
-  Piece<NPL, T, Y> piece{p, d, q, g, live, lds};
   const int b = begin + chunk * p.piece, e = last ? end : b + p.piece;
-  float sum = 0.0f;
-  if (b < e) sum = piece.run(b, e, a, h);
-  if (!kY) {
-    sum = sum4(sum);
+  if (ENDS && (chunk > 0 || std::is_same_v<Y, void>)) {
+    const float sum = sum4(Piece<NPL, T, void>{p, d, q, g, live, lds}.run(b, e, a, h));
     if (live && q == 0) p.carry[at * size + (int64_t)p.D * kNP + d] = sum;
+  } else if (b < e) {
+    Piece<NPL, T, Y>{p, d, q, g, live, lds}.run(b, e, a, h);
   }
   if (!live) return;
   if (last) {
     store_state(p, slot, d, q, h);
-  } else if (!kY) {
+  } else if (ENDS) {
 #pragma unroll
     for (int j = 0; j < NPL; ++j) ends[j] = h[j];
   }
@@ -472,7 +476,24 @@ size_t carry_bytes(const qssm_sscan_args& a, int64_t piece) {
   return (size_t)(a.tokens / piece + a.nseq) * (size_t)a.dim * (size_t)(4 * npl_of(a.dstate) + 1) * sizeof(float);
 }
 
+// First pieces in full with the others' ends: a pass less of their rows, but the first launch then waits for rows with y.
+// It gains where the second one has sequences of different lengths to level out (16384 rows, 4096 channels in 24
+// of them: 458 us without, 435 with; in 100, 1536 channels: 221, 199; 8192 rows, 2048 channels in 4: 144, 141), and costs
+// where it does not (8 of 1024 rows, 1536 channels: 103, 109; one of 8192: 121, 124).
+bool runs_first(const qssm_sscan_args& a) { return a.seq_offsets && a.nseq > 1; }
+
 bool is_step(const qssm_sscan_args& a) { return !a.seq_offsets && a.tokens == a.nseq; }
+
+template <int NPL, typename T, typename Y>
+qssm_status launch_scan(const SscanParams& p, const qssm_sscan_args& a, int64_t blocks, hipStream_t stream) {
+  if (is_cut(a, p.piece)) {
+    if (p.first) k_selective_scan<NPL, T, Y, true><<<(unsigned)blocks, 256, 0, stream>>>(p);
+    else k_selective_scan<NPL, T, void, true><<<(unsigned)blocks, 256, 0, stream>>>(p);
+    if (const qssm_status s = launch_status("selective_scan")) return s;
+  }
+  k_selective_scan<NPL, T, Y, false><<<(unsigned)blocks, 256, 0, stream>>>(p);
+  return launch_status("selective_scan");
+}
 
 template <int NPL, typename T>
 qssm_status launch(SscanParams p, const qssm_sscan_args& a, hipStream_t stream) {
@@ -487,13 +508,7 @@ qssm_status launch(SscanParams p, const qssm_sscan_args& a, hipStream_t stream) 
   }
   const int64_t blocks = (a.tokens / p.piece + a.nseq) * blocks_of(a);
   if (blocks > kMaxBlocks) return fail(QSSM_ERR_UNSUPPORTED, "tokens * dim too large");
-  if (is_cut(a, p.piece)) {
-    k_selective_scan<NPL, T, void><<<(unsigned)blocks, 256, 0, stream>>>(p);
-    if (const qssm_status s = launch_status("selective_scan")) return s;
-  }
-  if (p.yf16) k_selective_scan<NPL, T, __half><<<(unsigned)blocks, 256, 0, stream>>>(p);
-  else k_selective_scan<NPL, T, float><<<(unsigned)blocks, 256, 0, stream>>>(p);
-  return launch_status("selective_scan");
+  return p.yf16 ? launch_scan<NPL, T, __half>(p, a, blocks, stream) : launch_scan<NPL, T, float>(p, a, blocks, stream);
 }
 
 template <typename T>
@@ -552,6 +567,7 @@ extern "C" qssm_status qssm_selective_scan(const qssm_sscan_args* a, void* works
   if (a->slots > ((int64_t)1 << 58) / (D * N)) return fail(QSSM_ERR_UNSUPPORTED, "slots * dim * dstate above 2^58");
   SscanParams p{};
   p.piece = (int32_t)piece_rows(*a);
+  p.first = runs_first(*a);
   const size_t need = !is_step(*a) && is_cut(*a, p.piece) ? carry_bytes(*a, p.piece) : 0;
   if (need && (!workspace || workspace_bytes < need))
     return fail(QSSM_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : (size_t)0, need);
