@@ -12,10 +12,10 @@
 // registers by then.
 //
 // Bound by vector instructions: an update takes two products, an exponential (half the rate) and two fused
-// multiply-adds, 6 issue slots, of T D N updates. The vector units are 92 % busy with y and 89 % without it. A batch of
-// four rows takes 135 instructions for a lane's 16 updates (N 16), 80 of them the updates'. 16 x 1024 rows, 4096
-// channels, whole: 298 us; the same rows as 24 sequences of very different lengths: 192 us for the pieces' ends and
-// 270 with y (175 for the updates' slots alone); 256 single rows: 35 us, 4.1 TB/s.
+// multiply-adds, 6 issue slots, of T D N updates: vector instructions issue in 89 to 99 % of a CU's busy cycles. A batch
+// of four rows takes 135 of them for a lane's 16 updates (N 16), 80 the updates' own. 16 x 1024 rows, 4096 channels,
+// whole: 298 us; the same number of rows in 24 sequences of very different lengths: 436 us, about 0.4 of it in the first
+// launch (the updates' slots alone: 175); 256 single rows, which the bytes of their states bound: 35 us, 4.1 TB/s.
 //
 // Few sequences with few channels do not fill the chip, so long sequences are cut into pieces (piece_rows()).
 // First the pieces but the last run without y, the first from the initial state, the others from zero; then all run in
@@ -461,7 +461,8 @@ int64_t blocks_of(const qssm_sscan_args& a) { return a.ngroups * cdiv(a.dim / a.
 // 1024 rows, 4096 channels: 298 us, 431 in pieces of 256; 8 of 1024, 1536 channels, three quarters of the SIMDs: 120,
 // and 103 in pieces of 128); others run in pieces that give about 6 waves a SIMD, of 64 to 256 rows (1 x 8192
 // rows, 1536 channels, pieces of 64 / 128 / 256 / 512: 147 / 123 / 118 / 149 us, whole 900; 24 sequences of very different
-// lengths, 16384 rows, 4096 channels: 567 / 485 / 457 / 465, whole 708; 100 of them, 1536 channels: 212 / 203 / 223 / 281, 220).
+// lengths, 16384 rows, 4096 channels, 128 / 256 / 384 / 512: 466 / 433 / 438 / 450, whole 708; 100 of them, 1536 channels:
+// 191 / 198 / 230 / 272, 220).
 int64_t piece_rows(const qssm_sscan_args& a) {
   const int64_t waves = 4 * blocks_of(a), whole = std::max<int64_t>(a.tokens, 1);
   if (!a.seq_offsets && a.nseq * waves >= 900) return whole;
