@@ -629,8 +629,9 @@ qssm_status qssm_causal_conv(const qssm_conv_args* a, hipStream_t stream);
  * gate. A [dim, dstate], Dskip [dim] (NULL: 0) and delta_bias [dim] (NULL: 0) are fp32. All arithmetic is
  * fp32; an infinite dt * x makes what follows infinite or NaN. The state [slots, dim, dstate] is fp32, or fp16, which is rounded to nearest even once per call
  * and sequence (the decode cache in half the bytes; inside a call the state is fp32).
- * Long sequences are cut into pieces that run in parallel: every piece but a sequence's last runs from
- * zero, then every piece again from its entering state, which is folded from the ends of the pieces before it (in their order, so results do not vary from call to call). How long the pieces
+ * Long sequences are cut into pieces that run in parallel: the pieces between a sequence's first and last
+ * run from zero, then all that have not run in full from the state that enters them, which is folded from the ends
+ * of the pieces before (in their order, so results do not vary from call to call). How long the pieces
  * are follows from the sizes alone; they meet the sequential results to fp32 rounding.
  * Workspace: qssm_selective_scan_workspace_size bytes (0 when nothing is cut), 16-byte aligned; calls
  * that overlap in time need their own.

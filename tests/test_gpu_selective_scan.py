@@ -122,7 +122,7 @@ def test_against_oracle(dev, T, D, N, groups, kind):
 
 
 @pytest.mark.parametrize("T,D,N,kind", [(3000, 64, 16, 1), (2500, 128, 16, "ragged"), (2049, 20, 8, 1), (1500, 64, 64, "ragged"), (2600, 64, 16, 2),
-                                        (4000, 16, 4, [0, 1, 3000, 3064, 4000])])
+                                        (4000, 16, 4, [0, 1, 3000, 3064, 4000]), (2800, 70, 16, [7, 2790])])
 def test_long_sequences_are_cut(dev, T, D, N, kind):
     """Sequences of many pieces, with decays that carry a state over all of them."""
     import torch
