@@ -282,8 +282,9 @@ __global__ __launch_bounds__(256) void k_causal_conv(ConvParams p) {
   if (t == begin) {
     enter(win);
   } else {
+    // (at least W - 1 rows behind begin; offsets out of order can name a sequence that is not, and no row lies before row 0)
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) win[j] = t < end ? ln.row(t - (W - 1) + j) : Raw<VEC, X>{};
+    for (int j = 0; j < W - 1; ++j) win[j] = t < end ? ln.row(max(t - (W - 1) + j, 0)) : Raw<VEC, X>{};
   }
   const auto load = [&](int64_t from) {
 #pragma unroll

@@ -201,6 +201,23 @@ def test_offsets_that_are_wrong_stay_inside(dev):
         assert np.array_equal(so[keep], c["state"][keep])
 
 
+@pytest.mark.parametrize("off", [[2, 1, 60], [1, 0, 60], [1, 0, 2, 60], [2, 1, 1, 0, 64]])
+def test_offsets_out_of_order_read_no_row_before_the_first(dev, off):
+    """A sequence whose offset is above the next one's: the next one's rows begin behind its first, and what they need of
+    rows before that lies before row 0."""
+    import torch
+    import quantized_state_space_amd as qs
+    print(f"\n[causal_conv offsets {off}]", flush=True)
+    for W in (2, 3, 4):
+        wide = torch.full((67, 72), float("nan"), dtype=torch.float16, device=dev)
+        wide[3:] = torch.randn(64, 72, device=dev).half()
+        y = torch.full((64, 72), 7.0, device=dev)
+        qs.qssm_causal_conv(qs.causal_conv_args(wide[3:], torch.randn(72, W, device=dev), y,
+                                                seq_offsets=torch.tensor(off, dtype=torch.int32, device=dev)))
+        torch.cuda.synchronize()
+        assert bool(torch.isfinite(y).all()), W
+
+
 def test_prompt_then_tokens_equals_the_prompt(dev):
     """A prompt cut anywhere, its rest token by token: the same outputs bit for bit."""
     import torch
