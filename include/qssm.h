@@ -633,8 +633,9 @@ qssm_status qssm_causal_conv(const qssm_conv_args* a, hipStream_t stream);
  * run from zero, then all that have not run in full from the state that enters them, which is folded from the ends
  * of the pieces before (in their order, so results do not vary from call to call). How long the pieces
  * are follows from the sizes alone; they meet the sequential results to fp32 rounding.
- * Workspace: qssm_selective_scan_workspace_size bytes (0 when nothing is cut), 16-byte aligned; calls
- * that overlap in time need their own.
+ * Workspace: qssm_selective_scan_workspace_size bytes (0 when nothing is cut; only sequences longer than a piece
+ * take any, so their number adds nothing beyond what the tokens allow), 16-byte aligned; calls that overlap in
+ * time need their own.
  * 1 <= dstate <= 64, dim <= 2^24, nseq <= 2^24, tokens <= 2^31 - 64, dim % ngroups == 0; strides at most 2^23.
  */
 typedef struct qssm_sscan_args {

@@ -29,6 +29,7 @@
 #include <type_traits>
 
 #include "common.hpp"
+#include "selective_scan_forms.hpp"
 #include "sequences.hpp"
 
 using namespace qssm;
@@ -47,7 +48,7 @@ struct SscanParams {
   void* y;
   const void* state;
   void* state_out;
-  float* carry;  // piece slot: ends [D, 4 NPL], sums of dt [D]
+  float* carry;  // a slot of a piece: ends [D, 4 NPL], sums of dt [D]
 };
 
 constexpr float kLog2e = 1.44269504f;
@@ -330,7 +331,7 @@ __global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
   constexpr int kNP = 4 * NPL;
   __shared__ __align__(16) T lds[2 * kRows * 2 * kNP];
   const int blocks = p.G * p.per_group, cb = blockIdx.x % blocks;
-  const int64_t at = blockIdx.x / blocks;  // piece slot: sequence i has begin(i) / piece + i and the ones behind it
+  const int64_t at = blockIdx.x / blocks;  // piece: sequence i has begin(i) / piece + i and the ones behind it
   const Seqs& sq = p.seq;
   int i;
   if (sq.offsets) i = last_not_above(sq.nseq, at, [&](int k) { return (int64_t)(seq_begin(sq, k) / p.piece + k); });
@@ -348,7 +349,8 @@ __global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
   load_decay(p, d, q, a);
   const int64_t slot = seq_slot(sq, i);
   const int64_t size = (int64_t)p.D * (kNP + 1);
-  float* ends = p.carry + at * size + (int64_t)d * kNP + q * NPL;
+  const int64_t carry = qssm_sscan::first_slot(i, begin / p.piece) + chunk;  // (a sequence of one piece has none)
+  float* ends = p.carry + carry * size + (int64_t)d * kNP + q * NPL;
 #pragma unroll
   for (int j = 0; j < NPL; ++j) h[j] = 0.0f;
   if (chunk == 0 && (last || ENDS)) {
@@ -363,7 +365,7 @@ __global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
     for (int j = 0; j < NPL; ++j) h[j] = ends[(pieces - 1) * size + j];
   } else if (!ENDS) {
     const float* from = ends - chunk * size;
-    const float* sums = p.carry + (at - chunk) * size + (int64_t)p.D * kNP + d;
+    const float* sums = p.carry + (carry - chunk) * size + (int64_t)p.D * kNP + d;
 #pragma unroll
     for (int j = 0; j < NPL; ++j) h[j] = from[j];
 #pragma unroll 4
@@ -376,7 +378,7 @@ __global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
   const int b = begin + chunk * p.piece, e = last ? end : b + p.piece;
   if (ENDS && (chunk > 0 || std::is_same_v<Y, void>)) {
     const float sum = sum4(Piece<NPL, T, void>{p, d, q, g, live, lds}.run(b, e, a, h));
-    if (live && q == 0) p.carry[at * size + (int64_t)p.D * kNP + d] = sum;
+    if (live && q == 0) p.carry[carry * size + (int64_t)p.D * kNP + d] = sum;
   } else if (b < e) {
     Piece<NPL, T, Y>{p, d, q, g, live, lds}.run(b, e, a, h);
   }
@@ -456,25 +458,12 @@ int npl_of(int64_t N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
 int64_t blocks_of(const qssm_sscan_args& a) { return a.ngroups * cdiv(a.dim / a.ngroups, 64); }
 
-// Rows of a piece. A cut costs nearly twice the work, and pays where whole sequences leave SIMDs (1024 of them) without a
-// wave or wait for the longest one: sequences of one length that give nearly all of them a wave run whole (16 of
-// 1024 rows, 4096 channels: 298 us, 431 in pieces of 256; 8 of 1024, 1536 channels, three quarters of the SIMDs: 120,
-// and 103 in pieces of 128); others run in pieces that give about 6 waves a SIMD, of 64 to 256 rows (1 x 8192
-// rows, 1536 channels, pieces of 64 / 128 / 256 / 512: 147 / 123 / 118 / 149 us, whole 900; 24 sequences of very different
-// lengths, 16384 rows, 4096 channels, 128 / 256 / 384 / 512: 466 / 433 / 438 / 450, whole 708; 100 of them, 1536 channels:
-// 191 / 198 / 230 / 272, 220).
-int64_t piece_rows(const qssm_sscan_args& a) {
-  const int64_t waves = 4 * blocks_of(a), whole = std::max<int64_t>(a.tokens, 1);
-  if (!a.seq_offsets && a.nseq * waves >= 900) return whole;
-  return std::min<int64_t>(whole, std::clamp<int64_t>((whole * waves / 6144 + 16) / 32 * 32, 64, 256));
-}
+int64_t piece_rows(const qssm_sscan_args& a) { return qssm_sscan::piece_rows(a.tokens, a.nseq, 4 * blocks_of(a), a.seq_offsets); }
 
-bool is_cut(const qssm_sscan_args& a, int64_t piece) {
-  return piece < (a.seq_offsets ? a.tokens : a.tokens / std::max<int64_t>(a.nseq, 1));
-}
+bool is_cut(const qssm_sscan_args& a, int64_t piece) { return qssm_sscan::is_cut(a.tokens, a.nseq, piece, a.seq_offsets); }
 
 size_t carry_bytes(const qssm_sscan_args& a, int64_t piece) {
-  return (size_t)(a.tokens / piece + a.nseq) * (size_t)a.dim * (size_t)(4 * npl_of(a.dstate) + 1) * sizeof(float);
+  return (size_t)qssm_sscan::carry_slots(a.tokens, a.nseq, piece) * (size_t)a.dim * (size_t)(4 * npl_of(a.dstate) + 1) * sizeof(float);
 }
 
 // First pieces in full with the others' ends: a pass less of their rows, but the first launch then waits for rows with y.
