@@ -635,7 +635,9 @@ qssm_status qssm_causal_conv(const qssm_conv_args* a, hipStream_t stream);
  * are follows from the sizes alone; they meet the sequential results to fp32 rounding.
  * Workspace: qssm_selective_scan_workspace_size bytes (0 when nothing is cut; only sequences longer than a piece
  * take any, so their number adds nothing beyond what the tokens allow), 16-byte aligned; calls that overlap in
- * time need their own.
+ * time need their own. It does not only grow with the tokens (the pieces change with them):
+ * qssm_selective_scan_workspace_bound is enough for every call of up to `tokens` rows in any number of sequences, for
+ * a program that allocates once, before it captures calls into graphs.
  * 1 <= dstate <= 64, dim <= 2^24, nseq <= 2^24, tokens <= 2^31 - 64, dim % ngroups == 0; strides at most 2^23.
  */
 typedef struct qssm_sscan_args {
@@ -670,6 +672,7 @@ typedef struct qssm_sscan_args {
 } qssm_sscan_args;
 
 size_t qssm_selective_scan_workspace_size(const qssm_sscan_args* a);
+size_t qssm_selective_scan_workspace_bound(int64_t tokens, int64_t dim, int64_t dstate, int32_t ngroups);
 qssm_status qssm_selective_scan(const qssm_sscan_args* a, void* workspace, size_t workspace_bytes,
                                 hipStream_t stream);
 

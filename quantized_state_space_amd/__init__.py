@@ -144,6 +144,7 @@ SIGNATURES = {
     "qssm_quant_w8": (_I32, [_P, _I64, _I64, _P, _P]),
     "qssm_causal_conv": (_I32, [ctypes.POINTER(ConvArgs), _P]),
     "qssm_selective_scan_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(SscanArgs)]),
+    "qssm_selective_scan_workspace_bound": (ctypes.c_size_t, [_I64, _I64, _I64, _I32]),
     "qssm_selective_scan": (_I32, [ctypes.POINTER(SscanArgs), _P, ctypes.c_size_t, _P]),
     "qssm_quant_f8": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _I64, _P]),
     "qssm_gemm_f8": (_I32, [ctypes.POINTER(GemmF8Args), _P]),
@@ -824,6 +825,11 @@ def selective_scan_args(x, delta, A, B, C, y, D=None, z=None, delta_bias=None, d
 def qssm_selective_scan_workspace_size(args):
     """Bytes of the workspace; 0 where none is needed."""
     return load().qssm_selective_scan_workspace_size(ctypes.byref(args))
+
+
+def qssm_selective_scan_workspace_bound(tokens, dim, dstate, bc_groups=1):
+    """Bytes that are enough for every call of up to `tokens` rows, in any number of sequences."""
+    return load().qssm_selective_scan_workspace_bound(int(tokens), int(dim), int(dstate), int(bc_groups))
 
 
 def qssm_selective_scan(args, workspace=None, stream=None):

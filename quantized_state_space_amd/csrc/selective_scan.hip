@@ -462,8 +462,10 @@ int64_t piece_rows(const qssm_sscan_args& a) { return qssm_sscan::piece_rows(a.t
 
 bool is_cut(const qssm_sscan_args& a, int64_t piece) { return qssm_sscan::is_cut(a.tokens, a.nseq, piece, a.seq_offsets); }
 
+size_t slot_bytes(int64_t dim, int64_t dstate) { return (size_t)dim * (size_t)(4 * npl_of(dstate) + 1) * sizeof(float); }
+
 size_t carry_bytes(const qssm_sscan_args& a, int64_t piece) {
-  return (size_t)qssm_sscan::carry_slots(a.tokens, a.nseq, piece) * (size_t)a.dim * (size_t)(4 * npl_of(a.dstate) + 1) * sizeof(float);
+  return (size_t)qssm_sscan::carry_slots(a.tokens, a.nseq, piece) * slot_bytes(a.dim, a.dstate);
 }
 
 // First pieces in full with the others' ends: a pass less of their rows, but the first launch then waits for rows with y.
@@ -526,6 +528,14 @@ extern "C" size_t qssm_selective_scan_workspace_size(const qssm_sscan_args* a) {
   if (!a || check_sizes(*a) != QSSM_OK || a->nseq == 0 || a->dim == 0 || is_step(*a)) return 0;
   const int64_t piece = piece_rows(*a);
   return is_cut(*a, piece) ? carry_bytes(*a, piece) : 0;
+}
+
+extern "C" size_t qssm_selective_scan_workspace_bound(int64_t tokens, int64_t dim, int64_t dstate, int32_t ngroups) {
+  qssm_sscan_args a{};
+  a.tokens = tokens, a.dim = dim, a.dstate = dstate, a.ngroups = ngroups, a.nseq = 1;
+  clear_error();
+  if (check_sizes(a) != QSSM_OK || dim == 0) return 0;
+  return (size_t)qssm_sscan::most_slots(tokens, 4 * blocks_of(a)) * slot_bytes(dim, dstate);
 }
 
 extern "C" qssm_status qssm_selective_scan(const qssm_sscan_args* a, void* workspace, size_t workspace_bytes,

@@ -36,4 +36,15 @@ constexpr int first_slot(int i, int f) { return f + (i < f ? i : f); }
 
 inline int64_t carry_slots(int64_t tokens, int64_t nseq, int64_t piece) { return tokens / piece + std::min(nseq, tokens / piece); }
 
+// The most that carry_slots() gives for up to `tokens` rows in any number of sequences: for each length of a piece, at its
+// largest number of rows.
+inline int64_t most_slots(int64_t tokens, int64_t waves) {
+  int64_t most = 0;
+  for (int64_t p = kLeastPiece; p <= kMostPiece; p += kPieceStep) {
+    const int64_t rows = p == kMostPiece ? tokens : std::min(tokens, ((p + kPieceStep - 16) * 6144 - 1) / waves);
+    most = std::max(most, 2 * (rows / p));
+  }
+  return most;
+}
+
 }  // namespace qssm_sscan

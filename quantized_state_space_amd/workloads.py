@@ -21,7 +21,7 @@ from . import (QSSM_F16, QSSM_F32, QSSM_I8, QSSM_I16, QSSM_X_INT8, QSSM_X_SOFTED
                update_args, gemm_args, qssm_gemm_w4a8, qssm_quant_w4, qssm_quant_w8, rmsnorm_args,
                qssm_rmsnorm_i8, gemm_w8a8_args, qssm_gemm_w8a8, qssm_state_quant, qssm_state_dequant,
                qssm_state_update_i8, causal_conv_args, gemm_f8_args, qssm_causal_conv, qssm_gemm_f8, qssm_quant_f8,
-               qssm_quant_f8_weight, qssm_selective_scan, qssm_selective_scan_workspace_size, selective_scan_args)
+               qssm_quant_f8_weight, qssm_selective_scan, qssm_selective_scan_workspace_bound, selective_scan_args)
 
 
 def _dev(a, device, dtype=None):
@@ -609,7 +609,7 @@ class F8MambaBlock:
     slots. Activations between the operators are fp16.
 
     params: host fp32 w_in [2 D, d], conv_w [D, W], conv_b [D], w_x [R + 2 N, D], w_dt [D, R], dt_b [D], A [D, N],
-    Dskip [D], w_out [d, D]. tokens: the most rows of a step."""
+    Dskip [D], w_out [d, D]. tokens: the most rows of a step, for which every buffer is made once."""
 
     def __init__(self, params, slots, tokens, device):
         import torch
@@ -625,12 +625,14 @@ class F8MambaBlock:
         self.dt, self.y, self.out = e(tokens, self.D), e(tokens, self.D), e(tokens, d)
         self.conv_state = e(slots, self.W - 1, self.D)
         self.ssm_state = e(slots, self.D, self.N, dtype=torch.float32)
-        self.workspace = None
+        # for every step of up to `tokens` rows: a captured step keeps its address, so it is never replaced
+        self.workspace = torch.empty(qssm_selective_scan_workspace_bound(tokens, self.D, self.N), dtype=torch.uint8, device=device)
 
     def step(self, hidden, state_slots, seq_offsets=None, has_state=None):
         """hidden [T, d] float16: the sequences of seq_offsets, or without them one token of each. state_slots int32
-        and has_state uint8 [nseq] as in causal_conv_args. Returns the block's output [T, d]."""
-        import torch
+        and has_state uint8 [nseq] as in causal_conv_args. Returns the block's output [T, d], a view of a buffer of its own that
+        the next step overwrites; its rows of no sequence hold nothing of use. Steps and graphs of one block share its buffers
+        and run one after the other."""
         T, D, N, R = hidden.shape[0], self.D, self.N, self.R
         xz, x, dbc, dt, y, out = (t[:T] for t in (self.xz, self.x, self.dbc, self.dt, self.y, self.out))
         seqs = dict(nseq=T) if seq_offsets is None else dict(seq_offsets=seq_offsets)
@@ -642,8 +644,5 @@ class F8MambaBlock:
         self.proj_dt.step(dbc[:, :R], dt)
         args = selective_scan_args(x, dt, self.A, dbc[:, R:R + N], dbc[:, R + N:], y, D=self.Dskip, z=xz[:, D:],
                                    delta_bias=self.dt_b, state=self.ssm_state, state_out=self.ssm_state, **seqs)
-        need = qssm_selective_scan_workspace_size(args)
-        if need > (0 if self.workspace is None else self.workspace.numel()):
-            self.workspace = torch.empty(need, dtype=torch.uint8, device=hidden.device)
         qssm_selective_scan(args, self.workspace)
         return self.proj_out.step(y, out)

@@ -169,3 +169,46 @@ def test_a_stream_that_is_given(dev):
         out.append((c.view(torch.uint8), s, y, cy))
     for a, b in zip(*out):
         assert torch.equal(a, b)
+
+
+def test_a_captured_step_outlives_a_larger_one(dev):
+    """A step is captured, then the same block runs a larger one, and memory that this might have freed is taken: replays give
+    what they gave, and write nothing of others'."""
+    import torch
+    import quantized_state_space_amd.workloads as wl
+    print("\n[f8 block, captured then larger]", flush=True)
+    T = 1000
+    a, b = (wl.F8MambaBlock(params(4), 9, T, dev) for _ in range(2))
+    r = np.random.default_rng(4)
+    dv = lambda x: torch.from_numpy(np.asarray(x)).to(dev)  # noqa: E731
+    hidden = dv(r.standard_normal((T, DIM)).astype(np.float16))
+    slots = torch.arange(9, dtype=torch.int32, device=dev)
+    small, large = dv(np.array([0, 150], np.int32)), dv(np.array([0, 300, 470, 600, 601, 601, 780, 850, 900, T], np.int32))
+    one = slots[:1].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        a.step(hidden[:150], one, small)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    at = a.workspace.data_ptr()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.step(hidden[:150], one, small)
+    for blk in (a, b):
+        blk.conv_state.zero_()
+        blk.ssm_state.zero_()
+    a.step(hidden, slots, large)
+    b.step(hidden, slots, large)
+    torch.cuda.synchronize()
+    assert a.workspace.data_ptr() == at
+    taken = [torch.full((n,), 0x33, dtype=torch.uint8, device=dev) for n in (1 << 10, 1 << 14, 1 << 17, 1 << 18, 1 << 20) for _ in range(8)]
+    for k in range(3):
+        hidden.copy_(dv(r.standard_normal((T, DIM)).astype(np.float16)))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        b.step(hidden[:150], one, small)
+        torch.cuda.synchronize()
+        assert torch.equal(a.out[:150], b.out[:150]) and torch.equal(a.ssm_state, b.ssm_state) and torch.equal(a.conv_state, b.conv_state)
+        assert all(bool((t == 0x33).all()) for t in taken)

@@ -20,7 +20,8 @@ def forms(tmp_path_factory):
     subprocess.run(["g++", "-O1", "-shared", "-fPIC", "-std=c++17", os.path.join(ROOT, "tests", "host_selective_scan_forms.cpp"), "-o", so], check=True)
     lib = ctypes.CDLL(so)
     i64 = ctypes.c_int64
-    for f, args in ((lib.host_piece, [i64] * 3 + [ctypes.c_int]), (lib.host_first_slot, [ctypes.c_int] * 2), (lib.host_slots, [i64] * 3)):
+    for f, args in ((lib.host_piece, [i64] * 3 + [ctypes.c_int]), (lib.host_first_slot, [ctypes.c_int] * 2), (lib.host_slots, [i64] * 3),
+                    (lib.host_most, [i64] * 2)):
         f.argtypes, f.restype = args, i64
     return lib
 
@@ -57,6 +58,22 @@ def test_workspace_does_not_grow_with_sequences_that_are_not_cut():
     assert size(16384, 1) == 65 * slot
     assert size(16384, 24) == 88 * slot
     assert size(16384, 64) == size(16384, 1024) == size(16384, 16384) == size(16384, 1 << 24) == 128 * slot
+
+
+@pytest.mark.parametrize("dim,dstate,groups", [(1, 1, 1), (200, 16, 1), (1536, 16, 1), (4096, 8, 2), (8192, 64, 1), (5000, 33, 5)])
+def test_workspace_bound_covers_every_call(dim, dstate, groups):
+    """Of fewer rows too, with and without offsets, and it is one of them where the sequences are many."""
+    bound = lambda t: qs.qssm_selective_scan_workspace_bound(t, dim, dstate, groups)  # noqa: E731
+    most, last = 0, 0
+    for t in [*range(1, 1500), *range(1500, 40000, 37)]:
+        for nseq, packed in ((1, True), (t, True), (1, False), (2, False), (3, False)):
+            if packed or t % nseq == 0:
+                most = max(most, size(t, nseq, dim, dstate, packed, groups))
+        assert last <= bound(t) and most <= bound(t)
+        last = bound(t)
+    assert bound(39000) <= most * 1.1
+    assert bound(0) == 0 and bound(-1) == 0
+    assert qs.qssm_selective_scan_workspace_bound(100, 64, 65) == 0 and qs.qssm_selective_scan_workspace_bound(100, 64, 16, 0) == 0
 
 
 @pytest.mark.gpu
