@@ -324,6 +324,24 @@ struct Piece {
   }
 };
 
+// The state that enters piece `chunk` where steps below zero make a piece's decay grow out of fp32's range: it is taken as a
+// value of at most 1 and a power of two, so that a state of 0, or one small enough, goes through as row by row. Rare, so it
+// is a pass of its own behind the ordinary one.
+template <int NPL>
+__device__ __forceinline__ void fold_growing(const float (&a)[NPL], const float* from, const float* sums, int64_t size, int chunk, float (&h)[NPL]) {
+#pragma unroll
+  for (int j = 0; j < NPL; ++j) h[j] = from[j];
+  for (int c = 1; c < chunk; ++c) {
+    const float s = sums[c * size];
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+      // (2^1000 takes every state but 0 out of range; a NaN has made the piece's end one)
+      const float x = __builtin_amdgcn_fmed3f(s * a[j], -1000.0f, 1000.0f), n = ceilf(x);
+      h[j] = __builtin_ldexpf(h[j] * __builtin_amdgcn_exp2f(x - n), (int)n) + from[c * size + j];
+    }
+  }
+}
+
 // ENDS: the ends of the pieces that have one behind them, the first ones' from the initial state (with their y unless
 // Y is void), the others' from zero. Else every other piece with y, from the state that it folds from the ends.
 template <int NPL, typename T, typename Y, bool ENDS>
@@ -366,14 +384,20 @@ __global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
   } else if (!ENDS) {
     const float* from = ends - chunk * size;
     const float* sums = p.carry + (carry - chunk) * size + (int64_t)p.D * kNP + d;
+    float most = 0.0f;
 #pragma unroll
     for (int j = 0; j < NPL; ++j) h[j] = from[j];
 #pragma unroll 4
     for (int c = 1; c < chunk; ++c) {
       const float s = sums[c * size];
 #pragma unroll
-      for (int j = 0; j < NPL; ++j) h[j] = fmaf(__builtin_amdgcn_exp2f(s * a[j]), h[j], from[c * size + j]);
+      for (int j = 0; j < NPL; ++j) {
+        const float x = s * a[j];
+        most = fmaxf(most, x);
+        h[j] = fmaf(__builtin_amdgcn_exp2f(x), h[j], from[c * size + j]);
+      }
     }
+    if (__ballot(most > 126.0f)) fold_growing<NPL>(a, from, sums, size, chunk, h);
   }
   const int b = begin + chunk * p.piece, e = last ? end : b + p.piece;
   if (ENDS && (chunk > 0 || std::is_same_v<Y, void>)) {

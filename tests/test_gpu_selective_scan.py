@@ -133,6 +133,31 @@ def test_long_sequences_are_cut(dev, T, D, N, kind):
     assert check(dev, case(501 + T, T, D, N, 1, np.float32, off), torch.float16, in_place=False, pad=5) > 0
 
 
+@pytest.mark.parametrize("T,N,begin", [(400, 16, 0), (400, 16, 3), (700, 5, 0), (500, 64, 1)])
+def test_pieces_over_which_states_grow(dev, T, N, begin):
+    """Steps below zero whose decay over a piece leaves fp32's range, on states of zero and on small ones, which row by row stay
+    finite. Steps and their sums are exact, so the bound of single steps holds for their sum's exponential too."""
+    import torch
+    print(f"\n[selective_scan growing T={T} N={N} begin={begin}]", flush=True)
+    off = 1 if begin == 0 else np.array([0, begin, T], np.int32)
+    c = case(600 + T, T, 64, N, 1, np.float32, off)
+    c["A"][:, :] = -1.0
+    c["delta"][:] = 0.25
+    c["has"][:] = 1
+    c["slot"][:] = np.arange(c["nseq"])
+    c["delta"][:, :16] = -2.0  # zero up to the last rows
+    c["x"][:T - 10, :16] = 0.0
+    c["state"][:, :16] = 0.0
+    c["delta"][:, 16:32] = 0.0  # small, and e^96 over the second piece
+    c["delta"][begin + 64:begin + 128, 16:32] = -1.5
+    c["x"][:begin + 128, 16:32] = 0.0
+    c["state"][:, 16:32] = 1e-37
+    for gate in (True, False):
+        y, so, need = run(dev, c, torch.float32, gate=gate, softplus=False, bias=False)
+        assert need > 0 and bool(torch.isfinite(y).all()) and np.all(np.isfinite(so))
+        check(dev, c, torch.float32, gate=gate, softplus=False, bias=False)
+
+
 def test_no_tokens_hands_the_states_on(dev):
     import torch
     for off in (3, np.zeros(4, np.int32)):
