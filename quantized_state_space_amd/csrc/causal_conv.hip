@@ -20,6 +20,7 @@
 
 #include <type_traits>
 
+#include "causal_conv_forms.hpp"
 #include "common.hpp"
 #include "sequences.hpp"
 
@@ -373,10 +374,7 @@ qssm_status launch(ConvParams p, bool step, hipStream_t stream) {
     return launch_status("causal_conv");
   }
   p.cblocks = (int32_t)cdiv(p.C, 64 * VEC);
-  // strips as long as leaves 8 waves to a SIMD (1024 SIMDs), 8 to 64 rows (16384 rows, 8192 channels, at most 32 / 64 / 128: 146 /
-  // 140 / 142 us; 2777 rows, 1543 channels, 4 / 8 waves: 12.2 / 11.7)
-  int64_t strip = 64;
-  while (strip > 8 && cdiv(p.seq.tokens, strip) * p.cblocks < 8192) strip /= 2;
+  const int64_t strip = qssm_conv::strip_rows(p.seq.tokens, p.cblocks);
   p.strip = (int32_t)strip;
   p.strips = (int32_t)cdiv(p.seq.tokens, strip);
   const bool empties = p.state_out && (p.seq.offsets || p.seq.each == 0);
