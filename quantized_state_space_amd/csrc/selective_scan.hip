@@ -514,8 +514,7 @@ qssm_status launch_scan(const SscanParams& p, const qssm_sscan_args& a, int64_t 
 template <int NPL, typename T>
 qssm_status launch(SscanParams p, const qssm_sscan_args& a, hipStream_t stream) {
   if (is_step(a)) {
-    // four sequences at a time where that leaves a wave to every SIMD
-    const bool four = NPL <= 8 && cdiv(a.nseq, 4) * blocks_of(a) >= 256;
+    const bool four = qssm_sscan::four_at_a_time(a.nseq, blocks_of(a), NPL);
     const int64_t blocks = (four ? cdiv(a.nseq, 4) : a.nseq) * blocks_of(a);
     if (blocks > kMaxBlocks) return fail(QSSM_ERR_UNSUPPORTED, "nseq * dim above 2^30");
     if (four) k_selective_step<NPL, NPL <= 8 ? 4 : 1, T><<<(unsigned)blocks, 256, 0, stream>>>(p);

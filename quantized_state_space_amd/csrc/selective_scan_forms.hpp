@@ -47,4 +47,7 @@ inline int64_t most_slots(int64_t tokens, int64_t waves) {
   return most;
 }
 
+// Single rows: four sequences a lane (of states 4 * npl <= 32) where that leaves a wave to every SIMD; blocks: workgroups of a sequence.
+inline bool four_at_a_time(int64_t nseq, int64_t blocks, int npl) { return npl <= 8 && (nseq + 3) / 4 * blocks >= 256; }
+
 }  // namespace qssm_sscan

@@ -1,5 +1,6 @@
-"""How the selective scan cuts sequences: on the CPU, the rows of a piece for named calls, that the workspace's slots of all cut
-sequences are apart and inside, and its size; on the GPU, that nothing behind the workspace is written."""
+"""The forms of the selective scan: on the CPU, the rows of a piece and the form of single rows for named calls, that the
+workspace's slots of all cut sequences are apart and inside, and its size; on the GPU, these calls against the oracle, and that
+nothing behind the workspace is written."""
 import ctypes
 import os
 import subprocess
@@ -21,9 +22,39 @@ def forms(tmp_path_factory):
     lib = ctypes.CDLL(so)
     i64 = ctypes.c_int64
     for f, args in ((lib.host_piece, [i64] * 3 + [ctypes.c_int]), (lib.host_first_slot, [ctypes.c_int] * 2), (lib.host_slots, [i64] * 3),
-                    (lib.host_most, [i64] * 2)):
+                    (lib.host_most, [i64] * 2), (lib.host_four, [i64] * 2 + [ctypes.c_int])):
         f.argtypes, f.restype = args, i64
     return lib
+
+
+# rows of a piece, tokens, channels, states, sequences: a number of equal ones, or packed ones by their kind
+PIECES = [(64, 3000, 64, 16, 1), (96, 6000, 1536, 16, "ragged"), (128, 8192, 1536, 16, 1), (128, 8190, 1500, 24, "ragged"), (192, 8192, 2304, 16, 1),
+          (256, 16384, 4096, 16, "ragged"), (256, 12000, 4100, 8, 3)]
+# four sequences a lane, sequences, channels, states, B/C groups
+SINGLE = [(1, 256, 256, 16, 1), (1, 257, 256, 16, 2), (1, 258, 256, 5, 1), (1, 259, 250, 24, 2), (1, 260, 256, 32, 1), (1, 1030, 70, 16, 1), (1, 1029, 66, 8, 2),
+          (0, 252, 256, 16, 1), (0, 300, 256, 33, 1), (0, 600, 70, 64, 2)]
+
+
+def waves(D, groups=1):
+    return 4 * groups * -(-(D // groups) // 64)
+
+
+def npl(N):
+    return 2 if N <= 8 else 4 if N <= 16 else 8 if N <= 32 else 16
+
+
+@pytest.mark.parametrize("rows,T,D,N,kind", PIECES)
+def test_piece(forms, rows, T, D, N, kind):
+    assert forms.host_piece(T, 24 if kind == "ragged" else kind, waves(D), kind == "ragged") == rows
+
+
+@pytest.mark.parametrize("four,nseq,D,N,groups", SINGLE)
+def test_single_rows(forms, four, nseq, D, N, groups):
+    assert forms.host_four(nseq, waves(D, groups) // 4, npl(N)) == four
+
+
+def test_equal_sequences_that_fill_the_chip_run_whole(forms):
+    assert forms.host_piece(16 * 1024, 16, waves(4096), 0) == 16 * 1024 and forms.host_piece(8 * 1024, 8, waves(1536), 0) == 128
 
 
 @pytest.mark.parametrize("ordered", [True, False])
@@ -93,3 +124,70 @@ def test_nothing_behind_the_workspace_is_written(dev, T, D, kind):
     qs.qssm_selective_scan(args, ws[:need])
     torch.cuda.synchronize()
     assert bool((ws[need:] == 0x5A).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("four,nseq,D,N,groups", SINGLE)
+def test_single_rows_against_oracle(dev, four, nseq, D, N, groups):
+    import torch
+    from tests.test_gpu_selective_scan import case, check
+    print(f"\n[selective_scan single rows nseq={nseq} D={D} N={N} G={groups}]", flush=True)
+    f16, f32 = np.float16, np.float32
+    i = SINGLE.index((four, nseq, D, N, groups))
+    for j, (xt, st, yt) in enumerate([(f16, f32, torch.float16), (f32, f16, torch.float32), (f16, f16, torch.float32)]):
+        c = case(700 + 10 * i + j, nseq, D, N, groups, xt, nseq, st=st)
+        c["slot"][[5, 11, nseq - 1]] = -1, len(c["state"]), 2 ** 31 - 1  # no slot, in every place of the four
+        check(dev, c, yt, in_place=j != 1, pad=(0, 3, 8)[j], gate=j != 2, softplus=j != 2, bias=j != 2)
+        if j == 0:
+            check(dev, c, yt, slot=False, has=False, skip=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("xt", ["float16", "float32"])
+@pytest.mark.parametrize("rows,T,D,N,kind", PIECES)
+def test_pieces_against_oracle(dev, rows, T, D, N, kind, xt):
+    """The oracle computes some of the channels, the first and last and those on both sides of a workgroup's."""
+    import torch
+    import oracle.packed as op
+    from tests.test_gpu_selective_scan import assert_near
+    print(f"\n[selective_scan pieces of {rows} T={T} D={D} N={N} {kind} {xt}]", flush=True)
+    r = np.random.default_rng([56, T, D])
+    g = torch.Generator(device=dev).manual_seed(T + D)
+    n = lambda *s: torch.randn(*s, generator=g, device=dev)  # noqa: E731
+    if kind == "ragged":
+        off = np.concatenate([[2], np.sort(r.integers(2, T - 3, 19)), [T - 700, T - 700, T - 699, T - 3]]).astype(np.int32)
+        off.sort()
+        where, nseq = dict(seq_offsets=torch.from_numpy(off).to(dev)), len(off) - 1
+    else:
+        off, where, nseq = op.equal_offsets(T, kind), dict(nseq=kind), kind
+    xt = getattr(torch, xt)
+    x, delta, z, B, C = n(T, D).to(xt), (0.5 * n(T, D)).to(xt), n(T, D).to(xt), n(T, N).to(xt), n(T, N).to(xt)
+    A = -0.1 * torch.rand(D, N, generator=g, device=dev) * torch.arange(1, N + 1, device=dev)
+    skip, bias = n(D), -3 + n(D)
+    state = n(nseq + 2, D, N)
+    slot = r.permutation(nseq + 2)[:nseq].astype(np.int32)
+    has = r.integers(0, 2, nseq).astype(np.uint8)
+    has[0] = 1
+    y = torch.full((T, D), 7.0, device=dev)
+    pick = np.unique(np.concatenate([[0, 1, 63, 64, 127, 128], np.arange(D - 3, D), r.integers(0, D, 4)]) % D)
+    at = torch.from_numpy(pick).to(dev)
+    before = state[:, at].cpu().numpy()
+    dv = lambda a: torch.from_numpy(a).to(dev)  # noqa: E731
+    args = qs.selective_scan_args(x, delta, A, B, C, y, D=skip, z=z, delta_bias=bias, state=state, state_out=state, state_slots=dv(slot),
+                                  has_state=dv(has), **where)
+    ws = torch.full((qs.qssm_selective_scan_workspace_size(args),), 0xFF, dtype=torch.uint8, device=dev)
+    assert ws.numel() > 0
+    qs.qssm_selective_scan(args, ws)
+    torch.cuda.synchronize()
+    h = lambda t: t.cpu().numpy()  # noqa: E731
+    init = op.initial_states(before, nseq, (len(pick), N), slot, has)
+    want, ey, final, ef = op.selective_scan(h(x[:, at]), h(delta[:, at]), h(A[at]), h(B), h(C), h(skip[at]), h(z[:, at]), h(bias[at]), True, 1,
+                                            off, init, cut=rows)
+    inside = slice(off[0], off[-1])
+    assert_near(h(y[:, at]).astype(np.float64)[inside], want[inside], ey[inside], False)
+    assert bool((y[:off[0]] == 7.0).all()) and bool((y[off[-1]:] == 7.0).all()), "rows of no sequence were written"
+    got = h(state[:, at])
+    for i in range(nseq):
+        assert_near(got[slot[i]].astype(np.float64), final[i], ef[i], False)
+    keep = np.setdiff1d(np.arange(nseq + 2), slot)
+    assert np.array_equal(got[keep], before[keep])
