@@ -63,3 +63,54 @@ def test_other_forms(dev, M, N, K, pads, shift):
     print(f"\n[gemm_f8 M={M} N={N} K={K} {pads}]", flush=True)
     for f16 in (False, True):
         check(dev, operands(M + N + K, M, N, K), f16=f16, pads=pads, shift=shift)
+
+
+# For an fp16 y: the tile forms, up to 16 tokens, and rows at any address
+F16 = [(n, M, N, K, (0, 0, 0, 0)) for n, M, N, K, f16 in SHAPES if f16] + [
+    ("few", 1, 700, 4096, (0, 0, 0, 0)), ("few", 16, 400, 8192 + 100, (0, 0, 0, 0)), ("any", 40, 300, 1500, (1, 3, 0, 0)), ("any", 130, 200, 4099, (0, 0, 0, 0))]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name,M,N,K,pads", F16)
+def test_fp16_sums_without_a_cut(dev, name, M, N, K, pads):
+    """The codes of a row have one exponent in each block of 128, so all products of a block lie within two powers of two and
+    have their last bits far above 2^-13 of the largest: the matrix cores cut nothing, and an fp16 y keeps the bound of an fp32
+    one and its own rounding. A product more or less is seen: y is about sqrt(K) of them, its half step 2^-11 of that."""
+    import oracle.packed as op
+    from tests.test_gpu_f8 import product
+    print(f"\n[gemm_f8 fp16 {name} M={M} N={N} K={K}]", flush=True)
+    r = np.random.default_rng([57, M, N, K])
+    kb, nb = -(-K // 128), -(-N // 128)
+
+    def codes(rows):
+        e = np.repeat(r.integers(5, 10, (rows, kb)), 128, axis=1)[:, :K]
+        return (r.integers(0, 2, (rows, K)) << 7 | e << 3 | r.integers(0, 8, (rows, K))).astype(np.uint8)
+    a, w = codes(M), codes(N)
+    sa, sw = r.uniform(0.5, 1, (kb, M)).astype(np.float32), r.uniform(0.5, 1, (nb, kb)).astype(np.float32)
+    bias = r.standard_normal(N).astype(np.float32)
+    y = product(dev, a, sa, w, sw, bias, f16=True, pads=pads)
+    want, e = op.gemm_f8(a, sa, w, sw, bias)
+    e = e + 2.0 ** -11 * (np.abs(want) + e) + 2.0 ** -25
+    d = np.abs(y - want)
+    assert np.abs(want).max() < 60000 and np.all(d <= e), (np.argwhere(~(d <= e))[:4], (d / e).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("normal", [True, False])
+@pytest.mark.parametrize("name,M,N,K,pads", F16)
+def test_fp16_sums_over_the_output(dev, name, M, N, K, pads, normal):
+    """The cut is at most 6e-5 of the output, as root mean squares over it, for normal values and for codes of every exponent; an fp16 y's own
+    rounding is uniform in a half step of at most 2^-11 of a value, so 2^-11 / sqrt(3) of it; the two are independent."""
+    import oracle.packed as op
+    from tests.test_gpu_f8 import operands, product
+    print(f"\n[gemm_f8 fp16 rms {name} M={M} N={N} K={K} normal={normal}]", flush=True)
+    a, sa, w, sw, bias = operands(400 + M + N, M, N, K, bias=False)
+    sa, sw = sa / 64, sw / 64  # (no infinities)
+    if normal:
+        r = np.random.default_rng([58, M, N, K])
+        a, w = (op.e4m3_encode((40 * r.standard_normal(s)).astype(np.float32), np.float32(1)) for s in (a.shape, w.shape))
+    y = product(dev, a, sa, w, sw, bias, f16=True, pads=pads)
+    want, _ = op.gemm_f8(a, sa, w, sw, bias)
+    rms = lambda v: np.sqrt(np.mean(np.square(v)))  # noqa: E731
+    assert np.abs(want).max() < 60000
+    assert rms(y - want) <= np.hypot(6e-5, 2.0 ** -11 / np.sqrt(3)) * rms(want) + 2.0 ** -25, (rms(y - want) / rms(want),)
