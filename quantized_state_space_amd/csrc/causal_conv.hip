@@ -8,8 +8,9 @@
 // rows with the last W - 1 inputs in registers, so only the W - 1 rows before a strip are read twice;
 // the next rows are loaded while these are computed. A strip that crosses from one sequence into
 // the next takes the next one's state where it begins, one branch that is uniform over the wave.
-// 16384 rows of 8192 fp16 channels to int8: 133 us, 3.1 TB/s, with vector instructions issued in 91 % of a CU's busy
-// cycles: 28 an element, half of them silu and the code. Fp16 outputs of 256 single rows of 10240 channels: 10 us, 4.2 TB/s.
+// 16384 rows of 8192 fp16 channels to int8: 132 us, 3.1 TB/s, of which the issue of vector instructions takes 112 (6.4e7
+// slots of four cycles over 1024 SIMDs): 28 an element, half of them silu and the code; to fp16 144 us, 3.7 TB/s.
+// 256 single rows of 10240 channels to fp16: 10 us, 4.2 TB/s.
 // Channels of a lane, 8 / 4 / 2 / 1: 220 / 172 / 137 / 168 us for the 16384 rows, 19 / 13.4 / 10.4 / 12.8 for the 256 (more
 // of them leave too few waves, one alone has 2-byte accesses); rows ahead, 4 / 8 / 16: 142 / 137 / 152.
 //

@@ -10,8 +10,8 @@
 //
 // Two products: v_mfma_f32_32x32x64_f8f6f4 adds 8 neighbouring products at a time and cuts each at 2^-13 of the power of
 // two of the largest (seen from 448^2 beside smaller ones; v_mfma_f32_32x32x16_fp8_fp8 gives the same bits):
-// 1.4e-5 of the result for normal data, 5e-5 for codes of every exponent, a tenth of an fp16 y's own
-// rounding. An fp32 y is worth more: there the codes are converted to fp16, exactly, for
+// as root mean squares over the output 1.4e-5 of it for normal data, 5e-5 for codes of every exponent, beside an fp16 y's
+// own rounding of up to 2^-11 of each value. An fp32 y is worth more: there the codes are converted to fp16, exactly, for
 // v_mfma_f32_32x32x16_f16, at half the rate, whose sums are off by 1e-8 to 6e-7.
 #include <hip/hip_runtime.h>
 
@@ -215,6 +215,10 @@ __device__ __forceinline__ void epilogue(const GemmParams& p, uint8_t* sm, const
 // every wave has the step's last fragments in registers. A wave keeps the step's weight fragments and reads its
 // activations' a row tile ahead, and the next step's under the last products. A tile's products of the block go
 // to a sum of their own, which is scaled and added.
+// The stages ahead are waited for earlier than the two stages need: the next step's weight scale is a vector load of every step,
+// vector memory is waited for in order, and so with NS = 2 the wait before the barrier (all but (NS - 2) loads) holds for the
+// load just issued, and the wait for the first scale, issued behind the first stages' loads, for nearly all of
+// those, at the entry of the loop and so at its start in every turn. The costs in gemm_f8_forms.hpp hold with these waits.
 // KG groups of waves take every KG-th step each, in stages of their own, and join their sums in LDS in the groups'
 // order: where one workgroup has a CU, its step's latency bounds it (64x64 tiles, 256 x 4096 x 8192, fp16 y: 29
 // us with one group, 23 with two, 22 with four).

@@ -12,10 +12,11 @@
 // registers by then.
 //
 // Bound by vector instructions: an update takes two products, an exponential (half the rate) and two fused
-// multiply-adds, 6 issue slots, of T D N updates: vector instructions issue in 89 to 99 % of a CU's busy cycles. A batch
-// of four rows takes 135 of them for a lane's 16 updates (N 16), 80 the updates' own. 16 x 1024 rows, 4096 channels,
-// whole: 298 us; the same number of rows in 24 sequences of very different lengths: 436 us, about 0.4 of it in the first
-// launch (the updates' slots alone: 175); 256 single rows, which the bytes of their states bound: 35 us, 4.1 TB/s.
+// multiply-adds, 6 issue slots, of T D N updates. A batch of four rows takes 135 of them for a lane's 16 updates (N 16), 80
+// the updates' own. 16 x 1024 rows, 4096 channels, whole: 298 us; the same number of rows in 24 sequences of very
+// different lengths: 436 us, about 0.4 of it in the first launch, all of it filled by 2.5e8 issue slots of four cycles over
+// 1024 SIMDs (a single pass without cuts: 1.4e8; the updates' slots alone: 175 us); 256 single rows, which the
+// bytes of their states bound: 35 us, 4.1 TB/s.
 //
 // Few sequences with few channels do not fill the chip, so long sequences are cut into pieces (piece_rows()).
 // First the pieces but the last run without y, the first from the initial state, the others from zero; then all run in
@@ -417,7 +418,7 @@ __global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
 
 // One row a sequence: four lanes own a channel of one sequence (R = 1) or of four (R = 4), where each lane prepares one
 // sequence's dt, x and gate for all four, as a batch of the scan does. The bytes of the states bound it, but a wave's many
-// small loads cost as much: 256 sequences, 4096 channels, 16 fp32 states take 40 us with R = 1, and 37 with R = 4.
+// small loads cost as much: 256 sequences, 4096 channels, 16 fp32 states take 44 us with R = 1, and 35 with R = 4.
 template <int NPL, int R, typename T>
 __global__ __launch_bounds__(256) void k_selective_step(SscanParams p) {
   const int cb = blockIdx.x % (p.G * p.per_group), g = cb / p.per_group, q = threadIdx.x & 3;

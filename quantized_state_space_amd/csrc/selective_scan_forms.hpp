@@ -15,7 +15,8 @@ constexpr int64_t kLeastPiece = 64, kMostPiece = 256, kPieceStep = 32;
 // and 103 in pieces of 128); others run in pieces that give about 6 waves a SIMD, of 64 to 256 rows (1 x 8192
 // rows, 1536 channels, pieces of 64 / 128 / 256 / 512: 147 / 123 / 118 / 149 us, whole 900; 24 sequences of very different
 // lengths, 16384 rows, 4096 channels, 128 / 256 / 384 / 512: 466 / 433 / 438 / 450, whole 708; 100 of them, 1536 channels:
-// 191 / 198 / 230 / 272, 220).
+// 191 / 198 / 230 / 272, 220). The six waves are a compromise over these: the one prompt runs in pieces of 128 and the hundred
+// sequences in 256, each 4 % from its best, and the registers hold four waves of 16 states a SIMD, which the rule does not count.
 // waves: of one piece, over its channels; packed: with offsets.
 inline int64_t piece_rows(int64_t tokens, int64_t nseq, int64_t waves, bool packed) {
   const int64_t whole = std::max<int64_t>(tokens, 1);
