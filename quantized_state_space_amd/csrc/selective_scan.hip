@@ -398,7 +398,7 @@ __global__ __launch_bounds__(256) void k_selective_scan(SscanParams p) {
         h[j] = fmaf(__builtin_amdgcn_exp2f(x), h[j], from[c * size + j]);
       }
     }
-    if (__ballot(most > 126.0f)) fold_growing<NPL>(a, from, sums, size, chunk, h);
+    if (most > 126.0f) fold_growing<NPL>(a, from, sums, size, chunk, h);
   }
   const int b = begin + chunk * p.piece, e = last ? end : b + p.piece;
   if (ENDS && (chunk > 0 || std::is_same_v<Y, void>)) {

@@ -158,6 +158,22 @@ def test_pieces_over_which_states_grow(dev, T, N, begin):
         check(dev, c, torch.float32, gate=gate, softplus=False, bias=False)
 
 
+def test_channels_beside_growing_ones_keep_their_bits(dev):
+    import torch
+    c = case(620, 400, 64, 16, 1, np.float32, np.array([0, 3, 400], np.int32))
+    c["A"][:, :] = -1.0
+    c["delta"][:] = 0.25
+    out = []
+    for grows in (False, True):
+        if grows:
+            c["delta"][:, ::4] = -2.0
+        y, so, need = run(dev, c, torch.float32, softplus=False, bias=False, slot=False)
+        assert need > 0
+        keep = np.arange(64) % 4 != 0
+        out.append((y.numpy()[:, keep], so[:, keep]))
+    assert np.array_equal(out[0][0], out[1][0]) and np.array_equal(out[0][1], out[1][1])
+
+
 def test_no_tokens_hands_the_states_on(dev):
     import torch
     for off in (3, np.zeros(4, np.int32)):
